@@ -1,7 +1,7 @@
 /*
  * dattn: split-KV decode attention over a paged KV cache (bf16, 8-bit FP8 E4M3 codes or
- * 4-bit integer codes, the quantized formats with one fp32 scale per row), for GB300
- * (sm_103a).
+ * 4-bit integer codes, the quantized formats with one fp32 scale per row, or 8-bit codes with
+ * one power-of-two scale per 16-token block), for GB300 (sm_103a).
  *
  * The C ABI of libdattn.so. Every entry point takes plain pointers and sizes: no C++ and
  * no framework types. It validates its arguments on the host, then launches asynchronously
@@ -79,6 +79,22 @@
  *    region [num_pages][H4][P][d/2] bytes (this replaces the [num_pages][Hkv][P][d] layout
  *    above); kv_scale keeps the [num_pages][Hkv][P/16][2][16] layout over all heads. One
  *    decode launch reads both regions.
+ *  - The block-scaled 8-bit format (kv_format = DATTN_KV_FP8_BLOCK): E4M3 codes as in the
+ *    8-bit format, but one K scale and one V scale for the 16 tokens of a logical page of a
+ *    KV head: kv_scale is [num_pages][Hkv][P/16][2] floats (K, V), the array padded to a
+ *    multiple of four floats. A scale is 0 or a power of two in [2^-126, 2^119]; a value is
+ *    code * scale, exactly a bf16 number, and the attention runs over exactly these values.
+ *    An append takes, over the rows that it writes into a logical page, the smallest power of
+ *    two s with max |x| <= 448 s (0 when all are zero; beyond 448 * 2^119 codes saturate),
+ *    but no less than the page's scale if the page already holds earlier tokens (slots before
+ *    the first written one), and stores code = E4M3(x / s), a single rounding. Where that
+ *    raises the page's scale from s0 to s1, the earlier tokens' codes become
+ *    E4M3(code * s0 / s1): unchanged values, except that codes below 2^-6 are rounded again.
+ *    So tokens appended in one call and one by one are stored alike but for such codes.
+ *    Compared with a scale per row, a tile carries 8 bytes of scales instead of 128, and a
+ *    prefill can read the pool (dattn_prefill). dattn_append_decode does not take this format:
+ *    an append may rewrite rows that the same launch reads; call dattn_rope_append or
+ *    dattn_kv_append, then dattn_decode.
  *  - Statistics layout: stats is [num_pages][Hkv][P/16][2][d]. Entry [..][lp][0][:] is
  *    k_max and [..][lp][1][:] is k_min of logical page lp, the 16 tokens
  *    lp*16..lp*16+15 of that physical page.
@@ -136,6 +152,10 @@ typedef enum {
 #define DATTN_KV_INT4 2      /* symmetric 4-bit codes, two per byte, one fp32 scale per row */
 #define DATTN_KV_MIXED 3     /* per KV head: FP8 E4M3 or 4-bit rows (layout.head_format) */
 
+/* A further pool format: FP8 E4M3 codes with one power-of-two scale per 16-token logical page
+ * and KV head, K and V apart (see the layout notes). */
+enum { DATTN_KV_FP8_BLOCK = 5 };
+
 /* Shape of the paged KV pool and the block table. A zero-initialised tail (kv_format 0,
  * NULL scales) is the bf16 pool. */
 typedef struct dattn_kv_layout {
@@ -145,11 +165,13 @@ typedef struct dattn_kv_layout {
     int32_t page_size;          /* P: tokens per physical page, a multiple of 16 */
     const int32_t *block_table; /* (device) [B][max_pages_per_req]; -1 = unmapped */
     int32_t max_pages_per_req;  /* row width of block_table */
-    int32_t kv_format;          /* DATTN_KV_BF16, DATTN_KV_FP8_E4M3, DATTN_KV_INT4 or
-                                   DATTN_KV_MIXED */
+    int32_t kv_format;          /* DATTN_KV_BF16, DATTN_KV_FP8_E4M3, DATTN_KV_INT4,
+                                   DATTN_KV_MIXED or DATTN_KV_FP8_BLOCK */
     float *kv_scale;            /* (device) fp32 [num_pages][Hkv][P/16][2][16], 16-byte aligned:
                                    the row scales of the 8-bit and 4-bit formats (ignored for
-                                   bf16), written by dattn_kv_append; see the layout notes */
+                                   bf16), written by dattn_kv_append; see the layout notes
+                                   (DATTN_KV_FP8_BLOCK: [num_pages][Hkv][P/16][2], padded to a
+                                   multiple of four floats) */
     const int8_t *head_format;  /* (host) [Hkv], read during the call, DATTN_KV_MIXED only:
                                    DATTN_KV_FP8_E4M3 or DATTN_KV_INT4 per KV head; NULL or
                                    another value is DATTN_ERR_INVALID_ARG */
@@ -199,6 +221,88 @@ dattn_status_t dattn_kv_append(const dattn_kv_layout *layout, void *k_pool,
                                void *v_pool, dattn_bf16 *stats, const dattn_bf16 *k_new,
                                const dattn_bf16 *v_new, int32_t B, int32_t T,
                                int32_t *seq_lens, int32_t *dev_err, void *stream);
+
+/*
+ * Rotary positions. A row x of d channels at position p becomes, for every pair k of its first
+ * rot_dim channels,
+ *     y_a = A (x_a cos(p f_k) - x_b sin(p f_k)),  y_b = A (x_b cos(p f_k) + x_a sin(p f_k)),
+ * with (a, b) = (k, k + rot_dim/2), or (2k, 2k + 1) when interleaved; channels from rot_dim on
+ * are unchanged. Frequencies are given as turns per position, f_k / (2 pi) mod 1, in units of
+ * 2^-64 (dattn_rope_turns), so that an angle is exact at any int32 position; arithmetic is
+ * fp32, each result rounded once.
+ */
+typedef struct dattn_rotation {
+    int32_t rot_dim;       /* channels [0, rot_dim) are rotated: a multiple of 16, 0 to d */
+    int32_t interleaved;   /* 0: pairs (k, k + rot_dim/2); 1: pairs (2k, 2k + 1) */
+    float amplitude;       /* A, 1 for the plain rotation */
+    const uint64_t *turns; /* (host) [rot_dim/2], read during the call */
+} dattn_rotation;
+
+/* How dattn_rope_frequencies stretches the frequencies f_k = base^(-2k/rot_dim) for contexts
+ * longer than the original: */
+enum {
+    DATTN_ROPE_PLAIN = 0,   /* f_k */
+    DATTN_ROPE_LINEAR = 1,  /* f_k / factor */
+    DATTN_ROPE_NTK = 2,     /* base * factor^(rot_dim / (rot_dim - 2)) in place of base */
+    DATTN_ROPE_BY_PARTS = 3 /* with r = original_len * f_k / (2 pi) turns over the original
+                               length and w = (r - low) / (high - low) inside [0, 1]:
+                               f_k (w + (1 - w) / factor) */
+};
+
+/* Fills inv_freq [rot_dim/2] (host) with the frequencies of a scaling (DATTN_ROPE_*). factor > 0;
+ * original_len, low and high > low are read by DATTN_ROPE_BY_PARTS only. */
+dattn_status_t dattn_rope_frequencies(int32_t rot_dim, float base, int32_t scaling, float factor,
+                                      float original_len, float low, float high,
+                                      double *inv_freq);
+
+/* turns[k] (host) = inv_freq[k] / (2 pi) mod 1 in units of 2^-64; the frequencies are finite. */
+dattn_status_t dattn_rope_turns(int32_t n, const double *inv_freq, uint64_t *turns);
+
+/*
+ * Rotates N tokens of H heads. With inverse = 1 the angles are negated: the transposed rotation,
+ * which is the gradient of the call with inverse = 0 (and, for A = 1, takes it back).
+ *   x, out    (device) bf16, or fp32 when elem_f32 = 1; token n's heads are H * head_dim
+ *             consecutive elements at n * x_stride (n * out_stride) elements, so x can be a slice
+ *             of a fused projection. out may be x when the strides are equal; otherwise the two
+ *             do not overlap. Pointers are 16-byte aligned and strides multiples of 16 bytes.
+ *   positions (device) int32 [N], of any sign
+ */
+dattn_status_t dattn_rope(const dattn_rotation *rotation, const void *x, int64_t x_stride,
+                          void *out, int64_t out_stride, int32_t N, int32_t H, int32_t head_dim,
+                          int32_t elem_f32, const int32_t *positions, int32_t inverse,
+                          void *stream);
+
+/*
+ * Append with the rotation applied on the way: dattn_rope of the queries and of the new keys
+ * (the rotated keys rounded to bf16), then dattn_kv_append of the rotated keys and the values,
+ * in one launch (a second small one advances the lengths when T > 113). Every pool format.
+ *
+ *   rotation     nullable: nothing is rotated
+ *   q            (device, nullable) bf16, token n = b * T + t at n * q_stride elements, Hq heads
+ *   k_new, v_new (device) bf16, token n at n * k_stride (v_stride) elements, Hkv heads of d
+ *   q_out        (device) bf16 [B][T][Hq][d]; may be q when q_stride = Hq * d. NULL with q.
+ *   seq_lens     (device) int32 [B]; advanced by the new tokens when advance = 1. With
+ *                advance = 0 it is left as it is: the layers of a model share one array, and the
+ *                last layer's append advances it.
+ *   positions    (device, nullable) int32 [B][T]: the positions to rotate by, when they are not
+ *                the slots' seq_lens[b] + t
+ *   new_lens     (device, nullable) int32 [B]: the new tokens of request b are its first
+ *                new_lens[b] of the T (a padded batch); the others are neither rotated nor
+ *                written, and their rows of q_out stay as they are. A value outside [0, T] is
+ *                clamped and flagged with DATTN_DEVERR_LEN_OOB. NULL: all T.
+ *   stats, dev_err  as for dattn_kv_append. A token whose page is unmapped or out of range is
+ *                not written (its query is still rotated). A length below 0 or from 2^30 on is
+ *                flagged with DATTN_DEVERR_LEN_OOB, and nothing of that request is done.
+ * Strides are multiples of 8 elements and pointers 16-byte aligned. Hq <= 4096.
+ */
+dattn_status_t dattn_rope_append(const dattn_kv_layout *layout, void *k_pool, void *v_pool,
+                                 dattn_bf16 *stats, const dattn_rotation *rotation,
+                                 const dattn_bf16 *q, int64_t q_stride, const dattn_bf16 *k_new,
+                                 int64_t k_stride, const dattn_bf16 *v_new, int64_t v_stride,
+                                 int32_t B, int32_t T, int32_t Hq, dattn_bf16 *q_out,
+                                 int32_t *seq_lens, const int32_t *positions,
+                                 const int32_t *new_lens, int32_t advance, int32_t *dev_err,
+                                 void *stream);
 
 /*
  * MicroAttention partials over explicit chunks of pages [IL, DistAttention 的等价数学变换].
@@ -317,8 +421,9 @@ dattn_status_t dattn_decode_multi(const dattn_kv_layout *layout, const void *k_p
 
 /*
  * One decode step with its append, in one launch: exactly dattn_kv_append of one new token
- * per request (T = 1) followed by dattn_decode, for every pool format (a quantized pool
- * stores the new rows quantized exactly as dattn_kv_append does). [LS §4.2: the master saves
+ * per request (T = 1) followed by dattn_decode, for every pool format but
+ * DATTN_KV_FP8_BLOCK (DATTN_ERR_UNSUPPORTED; see the layout notes). (A quantized pool
+ * stores the new rows quantized exactly as dattn_kv_append does.) [LS §4.2: the master saves
  * the new token's KV locally, then every instance attends over its KV including it.] The new
  * token of request b is written at position seq_lens[b] (and the logical-page statistics take
  * it in when stats is not NULL); the decode attends tokens 0 .. seq_lens[b] (the new one
@@ -393,8 +498,8 @@ typedef struct dattn_prefill_sparse {
  * One CTA computes one 64-token query block of one query head over all its key blocks, so
  * no workspace is needed.
  *
- *   k_pool, v_pool (device) the pool, bf16 only (DATTN_ERR_UNSUPPORTED for the quantized
- *            formats)
+ *   k_pool, v_pool (device) the pool: bf16 or DATTN_KV_FP8_BLOCK (DATTN_ERR_UNSUPPORTED for
+ *            the other quantized formats)
  *   q        (device) bf16 [B][Tq][Hq][d];  seq_lens (device) int32 [B]
  *   out      (device) fp32 [B][Tq][Hq][d]
  *   m, e     (device, nullable) fp32 [B][Tq][Hq]: the row max (natural-log units) and sum,

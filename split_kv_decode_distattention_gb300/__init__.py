@@ -11,10 +11,12 @@ Entry points, with the same names as in include/dattn.h:
   dattn_partial      MicroAttention partials (m, e, MA) over explicit chunks of pages
   dattn_merge        log-sum-exp aggregation of partials
   dattn_decode       fused split-KV decode, dense or block-sparse
-  dattn_append_decode one decode step with its one-token append, in one launch (bf16 pool)
+  dattn_append_decode one decode step with its one-token append, in one launch
   dattn_decode_multi fused decode of T new query tokens per request, causal over them
   dattn_page_select  page scoring and top-K selection for retrieval heads
   dattn_prefill      block-sparse prefill of a chunk of new tokens (64-token key blocks)
+  dattn_rope         rotary positions of queries or keys, and their gradient
+  dattn_rope_append  the append with the rotation of queries and keys applied on the way
 """
 from __future__ import annotations
 
@@ -27,12 +29,13 @@ import torch
 __all__ = [
     "KVLayout", "SparseConfig", "DattnError", "load_library", "library_path",
     "dattn_kv_append", "dattn_partial", "dattn_merge", "dattn_decode", "dattn_page_select",
-    "dattn_append_decode", "dattn_merge_gathered",
+    "dattn_append_decode", "dattn_merge_gathered", "dattn_rope", "dattn_rope_append",
+    "dattn_rope_frequencies", "Rotation",
     "dattn_decode_noalloc", "dattn_decode_multi", "dattn_prefill", "PrefillSparseConfig",
     "dattn_workspace_size", "dattn_workspace_init", "dattn_auto_splits", "dattn_split_range",
     "dattn_split_owner", "dattn_status_string", "dattn_version", "Workspace",
     "HEAD_DENSE", "HEAD_RETRIEVAL", "HEAD_STREAMING", "DEVERR", "KV_BF16", "KV_FP8_E4M3",
-    "KV_INT4", "KV_MIXED", "mixed_pool_bytes",
+    "KV_INT4", "KV_MIXED", "KV_FP8_BLOCK", "mixed_pool_bytes", "kv_scale_floats",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -42,7 +45,9 @@ _lock = threading.Lock()
 
 HEAD_DENSE, HEAD_RETRIEVAL, HEAD_STREAMING = 0, 1, 2
 KV_BF16, KV_FP8_E4M3, KV_INT4, KV_MIXED = 0, 1, 2, 3
-_QUANT = (KV_FP8_E4M3, KV_INT4, KV_MIXED)
+KV_FP8_BLOCK = 5
+_QUANT = (KV_FP8_E4M3, KV_INT4, KV_MIXED, KV_FP8_BLOCK)
+_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by-parts": 3}
 DEVERR = {"UNMAPPED_PAGE": 0x1, "PAGE_OOB": 0x2, "LEN_OOB": 0x4, "TIMEOUT": 0x8,
           "CHUNK_OOB": 0x10, "SELECT_OOB": 0x20, "SMEM_ALIGN": 0x40}
 
@@ -71,6 +76,11 @@ class _PrefillSparse(ctypes.Structure):
                 ("qblock_stride", ctypes.c_int32), ("block_lists", ctypes.c_void_p)]
 
 
+class _Rotation(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("amplitude", ctypes.c_float), ("turns", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _I64 = ctypes.c_int64
@@ -94,6 +104,13 @@ _SIGS = {
                                 _SZ, _P, _P, _P, _P, _P]),
     "dattn_prefill": (_I, [ctypes.POINTER(_Layout), _P, _P, _P, _I, _I, _I, _F, _P,
                            ctypes.POINTER(_PrefillSparse), _P, _P, _P, _P, _P]),
+    "dattn_rope_frequencies": (_I, [_I, _F, _I, _F, _F, _F, _F, _P]),
+    "dattn_rope_turns": (_I, [_I, _P, _P]),
+    "dattn_rope": (_I, [ctypes.POINTER(_Rotation), _P, _I64, _P, _I64, _I, _I, _I, _I, _P, _I,
+                        _P]),
+    "dattn_rope_append": (_I, [ctypes.POINTER(_Layout), _P, _P, _P, ctypes.POINTER(_Rotation),
+                               _P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _P, _P, _P, _P, _I, _P,
+                               _P]),
     "dattn_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "dattn_workspace_init": (_I, [_P, _SZ, _P]),
     "dattn_auto_splits": (_I, [_I64]),
@@ -184,6 +201,15 @@ def mixed_pool_bytes(num_pages: int, head_format, head_dim: int, page_size: int)
     return num_pages * page_size * (h8 * head_dim + h4 * (head_dim // 2))
 
 
+def kv_scale_floats(kv_format: int, num_pages: int, num_kv_heads: int, page_size: int) -> int:
+    """Floats of kv_scale: two per row (the row-scaled formats), or two per 16-token block, padded
+    to a multiple of four (KV_FP8_BLOCK); 0 for bf16."""
+    n = num_pages * num_kv_heads * page_size
+    if kv_format == KV_FP8_BLOCK:
+        return -(-(n // 16) // 2) * 4
+    return 2 * n if kv_format in _QUANT else 0
+
+
 def _layout_sizes(layout, B: int, k_pool, v_pool, stats=None):
     """The pools, block table, scales and statistics must cover the layout for B requests."""
     c = layout.c
@@ -196,7 +222,8 @@ def _layout_sizes(layout, B: int, k_pool, v_pool, stats=None):
     _size(v_pool, pool, "v_pool")
     _size(layout.block_table, B * c.max_pages_per_req, "block_table")
     if c.kv_format in _QUANT:
-        _size(layout.kv_scale, 2 * n, "kv_scale")
+        _size(layout.kv_scale, kv_scale_floats(c.kv_format, c.num_pages, c.num_kv_heads,
+                                               c.page_size), "kv_scale")
     _size(stats, n // 16 * 2 * c.head_dim, "stats")
 
 
@@ -220,7 +247,9 @@ class KVLayout:
     nibble), with kv_scale as for KV_FP8_E4M3. KV_MIXED: head_format[h] (KV_FP8_E4M3 or
     KV_INT4) gives each KV head's format; the pools are that many bytes
     (mixed_pool_bytes): the 8-bit heads' region, then the 4-bit heads' region, each head at
-    its index among the heads of its format.
+    its index among the heads of its format. KV_FP8_BLOCK: uint8 E4M3 codes with one power-of-two
+    K scale and V scale per logical page, kv_scale float32 [num_pages][Hkv][P/16][2] padded to
+    kv_scale_floats(...) elements.
     """
 
     def __init__(self, num_pages: int, num_kv_heads: int, head_dim: int, page_size: int,
@@ -297,6 +326,49 @@ class PrefillSparseConfig:
                                 block_lists.data_ptr() if block_lists is not None else None)
 
 
+class Rotation:
+    """Rotary positions of the first rot_dim channels (a multiple of 16): pairs (k, k + rot_dim/2),
+    or (2k, 2k + 1) when interleaved, turned by position * f_k and scaled by amplitude.
+
+    f_k comes from base and a scaling for long contexts: "none", "linear" (f_k / factor), "ntk"
+    (the base raised) or "by-parts" (frequencies with fewer than `low` turns over original_len
+    divided by factor, those with more than `high` kept, a ramp between); or is given as inv_freq,
+    rot_dim / 2 numbers. The frequencies are kept as host data: a Rotation belongs to no device.
+    """
+
+    def __init__(self, rot_dim: int, interleaved: bool = False, base: float = 10000.0,
+                 scaling: str = "none", factor: float = 1.0, original_len: float = 8192.0,
+                 low: float = 1.0, high: float = 4.0, amplitude: float = 1.0, inv_freq=None):
+        n = rot_dim // 2
+        if inv_freq is None:
+            inv_freq = dattn_rope_frequencies(rot_dim, base, scaling, factor, original_len, low,
+                                              high) if rot_dim else []
+        elif len(inv_freq) != n:
+            raise ValueError(f"inv_freq holds {len(inv_freq)} frequencies; rot_dim / 2 = {n}")
+        self.inv_freq = [float(f) for f in inv_freq]
+        self._turns = (ctypes.c_uint64 * max(n, 1))()
+        _check(load_library().dattn_rope_turns(n, (ctypes.c_double * max(n, 1))(*self.inv_freq),
+                                               self._turns), "dattn_rope_turns")
+        self.c = _Rotation(rot_dim, int(bool(interleaved)), amplitude,
+                           ctypes.addressof(self._turns))
+
+    @property
+    def rot_dim(self): return self.c.rot_dim
+
+
+def dattn_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
+                           factor: float = 1.0, original_len: float = 8192.0, low: float = 1.0,
+                           high: float = 4.0) -> list:
+    """The rot_dim / 2 inverse frequencies of a scaling ("none", "linear", "ntk", "by-parts")."""
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}")
+    out = (ctypes.c_double * max(rot_dim // 2, 1))()
+    _check(load_library().dattn_rope_frequencies(rot_dim, base, _SCALINGS[scaling], factor,
+                                                 original_len, low, high, out),
+           "dattn_rope_frequencies")
+    return list(out)[:rot_dim // 2]
+
+
 class Workspace:
     """A zeroed device workspace sized by dattn_workspace_size (allocated by torch)."""
 
@@ -352,6 +424,93 @@ def dattn_kv_append(layout: KVLayout, k_pool, v_pool, stats, k_new, v_new, seq_l
     _check(load_library().dattn_kv_append(
         ctypes.byref(layout.c), _ptr(k_pool), _ptr(v_pool), _ptr(stats), _ptr(k_new),
         _ptr(v_new), B, T, _ptr(seq_lens), _ptr(dev_err), _stream(stream)), "dattn_kv_append")
+
+
+def _tokens(t, name):
+    """A [tokens...][H][d] tensor whose heads are packed and whose tokens are evenly spaced (a
+    contiguous tensor or a slice of a fused projection): (pointer, elements between tokens)."""
+    size, step = t.shape, t.stride()
+    if len(size) not in (3, 4):
+        raise ValueError(f"{name} must be [tokens][heads][d] or [B][T][heads][d]")
+    if step[-1] != 1 or (size[-2] > 1 and step[-2] != size[-1]):
+        raise ValueError(f"the heads of {name} must be packed")
+    stride = step[-3]
+    if len(size) == 4 and size[0] > 1:
+        if size[1] == 1:
+            stride = step[0]
+        elif step[0] != size[1] * stride:
+            raise ValueError(f"the tokens of {name} must be evenly spaced")
+    if t.numel() == 0 or (len(size) == 3 and size[0] == 1) or \
+            (len(size) == 4 and size[0] == size[1] == 1):
+        stride = size[-2] * size[-1]  # no second token
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    return ctypes.c_void_p(t.data_ptr()), stride
+
+
+def _same_device(*tensors):
+    """The launch goes to the current device: every tensor must live there."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != here:
+            raise ValueError(f"a tensor of {t.device} in a call on cuda:{here}")
+
+
+def dattn_rope(rotation: Rotation, x, out, positions, inverse: bool = False, stream=None):
+    """Rotate x, bf16 or float32 [N][H][d] or [B][T][H][d], into out (same shape and type; may be
+    x) at the int32 positions, one per token. inverse=True negates the angles: the gradient."""
+    if x.dtype not in (torch.bfloat16, torch.float32) or out.dtype != x.dtype:
+        raise TypeError("x and out must both be bfloat16 or both float32")
+    if out.shape != x.shape:
+        raise ValueError("out must have the shape of x")
+    _i32(positions, "positions")
+    H, d = x.shape[-2:]
+    N = x.numel() // max(H * d, 1)
+    _size(positions, N, "positions")
+    _same_device(x, out, positions)
+    xp, xs = _tokens(x, "x")
+    op, os_ = _tokens(out, "out")
+    _check(load_library().dattn_rope(
+        ctypes.byref(rotation.c), xp, xs, op, os_, N, H, d, int(x.dtype == torch.float32),
+        _ptr(positions), int(bool(inverse)), _stream(stream)), "dattn_rope")
+
+
+def dattn_rope_append(layout: KVLayout, k_pool, v_pool, stats, rotation: Rotation | None, q, k_new,
+                      v_new, q_out, seq_lens, positions=None, new_lens=None, advance: bool = True,
+                      dev_err=None, stream=None):
+    """Rotate q ([B][T][Hq][d] bf16, into q_out, contiguous; both may be None) and k_new, and
+    append the rotated keys and v_new ([B][T][Hkv][d] bf16) at seq_lens (int32 [B]), in one
+    launch. q, k_new and v_new may be slices of a fused projection. positions (int32 [B][T])
+    replaces seq_lens[b] + t as the rotation's positions; new_lens (int32 [B]) gives the new
+    tokens of each request in a padded batch; advance=False leaves seq_lens as it is."""
+    _pool(layout, k_pool, "k_pool"); _pool(layout, v_pool, "v_pool"); _bf16(stats, "stats")
+    _bf16(q, "q"); _bf16(q_out, "q_out"); _bf16(k_new, "k_new"); _bf16(v_new, "v_new")
+    _i32(seq_lens, "seq_lens"); _i32(positions, "positions"); _i32(new_lens, "new_lens")
+    if k_new.dim() != 4 or k_new.shape[2:] != (layout.num_kv_heads, layout.head_dim) or \
+            v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must be bf16 [B][T][Hkv][d]")
+    B, T = k_new.shape[:2]
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    Hq, qp, qs = 0, None, 0
+    if q is not None:
+        Hq = q.shape[2] if q.dim() == 4 else 0
+        if q.shape != (B, T, Hq, layout.head_dim) or Hq == 0:
+            raise ValueError("q must be bf16 [B][T][Hq][d]")
+        _size(q_out, q.numel(), "q_out")
+        qp, qs = _tokens(q, "q")
+    _layout_sizes(layout, B, k_pool, v_pool, stats)
+    _size(seq_lens, B, "seq_lens"); _size(new_lens, B, "new_lens")
+    _size(positions, B * T, "positions")
+    _same_device(k_pool, v_pool, stats, q, k_new, v_new, q_out, seq_lens, positions, new_lens,
+                 layout.block_table, layout.kv_scale, dev_err)
+    kp, ks = _tokens(k_new, "k_new")
+    vp, vs = _tokens(v_new, "v_new")
+    _check(load_library().dattn_rope_append(
+        ctypes.byref(layout.c), _ptr(k_pool), _ptr(v_pool), _ptr(stats),
+        ctypes.byref(rotation.c) if rotation is not None else None, qp, qs, kp, ks, vp, vs, B, T,
+        Hq, _ptr(q_out), _ptr(seq_lens), _ptr(positions), _ptr(new_lens), int(bool(advance)),
+        _ptr(dev_err), _stream(stream)), "dattn_rope_append")
 
 
 def dattn_partial(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_lens, chunk_req,
@@ -439,8 +598,8 @@ def dattn_append_decode(layout: KVLayout, k_pool, v_pool, stats, k_new, v_new, q
                         sparse: SparseConfig | None = None, num_splits=0, dev_err=None,
                         stream=None):
     """dattn_kv_append of one token per request (k_new/v_new bf16 [B][1][Hkv][d]) and
-    dattn_decode over the advanced lengths, in one launch (any pool format; a quantized pool
-    stores the new rows quantized as dattn_kv_append would): out fp32 [B][Hq][d]
+    dattn_decode over the advanced lengths, in one launch (any pool format but KV_FP8_BLOCK; a
+    quantized pool stores the new rows quantized as dattn_kv_append would): out fp32 [B][Hq][d]
     (+ m_g, e_g fp32 [B][Hq]); seq_lens advances by one."""
     _pool(layout, k_pool, "k_pool"); _pool(layout, v_pool, "v_pool"); _bf16(stats, "stats")
     _bf16(k_new, "k_new"); _bf16(v_new, "v_new"); _bf16(q, "q"); _i32(seq_lens, "seq_lens")

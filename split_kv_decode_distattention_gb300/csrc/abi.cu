@@ -5,6 +5,7 @@
 #include <cudaTypedefs.h>
 
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 #include "common.cuh"
@@ -48,7 +49,8 @@ dattn_status_t check_layout(const dattn_kv_layout* L) {
         return DATTN_ERR_UNSUPPORTED;
     if ((int64_t)L->max_pages_per_req * L->page_size >= (1ll << 30)) return DATTN_ERR_UNSUPPORTED;
     if (L->kv_format != DATTN_KV_BF16 && L->kv_format != DATTN_KV_FP8_E4M3 &&
-        L->kv_format != DATTN_KV_INT4 && L->kv_format != DATTN_KV_MIXED)
+        L->kv_format != DATTN_KV_INT4 && L->kv_format != DATTN_KV_MIXED &&
+        L->kv_format != DATTN_KV_FP8_BLOCK)
         return DATTN_ERR_INVALID_ARG;
     if (L->kv_format != DATTN_KV_BF16 && (!L->kv_scale || !aligned16(L->kv_scale)))
         return DATTN_ERR_INVALID_ARG;
@@ -234,8 +236,123 @@ dattn_status_t dattn_kv_append(const dattn_kv_layout* layout, void* k_pool,
         return DATTN_ERR_INVALID_ARG;
     if ((int64_t)B * T >= (1ll << 31) / 8) return DATTN_ERR_UNSUPPORTED;
     if (B > 65535) return DATTN_ERR_UNSUPPORTED;
+    if (layout->kv_format == DATTN_KV_FP8_BLOCK) {
+        const int64_t stride = (int64_t)layout->num_kv_heads * layout->head_dim;
+        return launch_rope_append(*layout, k_pool, v_pool, stats, nullptr, nullptr, 0, k_new,
+                                  stride, v_new, stride, B, T, 0, nullptr, seq_lens, nullptr,
+                                  nullptr, true, dev_err, static_cast<cudaStream_t>(stream));
+    }
     return launch_kv_append(*layout, k_pool, v_pool, stats, k_new, v_new, B, T, seq_lens, dev_err,
                             static_cast<cudaStream_t>(stream));
+}
+
+dattn_status_t dattn_rope_frequencies(int32_t rot_dim, float base, int32_t scaling, float factor,
+                                      float original_len, float low, float high,
+                                      double* inv_freq) {
+    if (rot_dim <= 0 || rot_dim % 16 != 0 || inv_freq == nullptr) return DATTN_ERR_INVALID_ARG;
+    if (!(base > 0.f) || !std::isfinite(base)) return DATTN_ERR_INVALID_ARG;
+    if (scaling < DATTN_ROPE_PLAIN || scaling > DATTN_ROPE_BY_PARTS) return DATTN_ERR_INVALID_ARG;
+    if (scaling != DATTN_ROPE_PLAIN && (!(factor > 0.f) || !std::isfinite(factor)))
+        return DATTN_ERR_INVALID_ARG;
+    if (scaling == DATTN_ROPE_BY_PARTS &&
+        (!(original_len > 0.f) || !std::isfinite(original_len) || !(high > low) ||
+         !std::isfinite(high) || !std::isfinite(low)))
+        return DATTN_ERR_INVALID_ARG;
+    const double r = rot_dim, turn = 6.283185307179586476925;
+    double b = base;
+    if (scaling == DATTN_ROPE_NTK) b *= std::pow((double)factor, r / (r - 2.0));
+    for (int32_t k = 0; k < rot_dim / 2; ++k) {
+        double f = std::pow(b, -2.0 * k / r);
+        if (scaling == DATTN_ROPE_LINEAR) f /= factor;
+        if (scaling == DATTN_ROPE_BY_PARTS) {
+            double w = (original_len * f / turn - low) / ((double)high - low);
+            w = w < 0.0 ? 0.0 : w > 1.0 ? 1.0 : w;
+            f *= w + (1.0 - w) / factor;
+        }
+        inv_freq[k] = f;
+    }
+    return DATTN_OK;
+}
+
+dattn_status_t dattn_rope_turns(int32_t n, const double* inv_freq, uint64_t* turns) {
+    if (n < 0) return DATTN_ERR_INVALID_ARG;
+    if (n == 0) return DATTN_OK;
+    if (!inv_freq || !turns) return DATTN_ERR_INVALID_ARG;
+    for (int32_t k = 0; k < n; ++k)
+        if (!std::isfinite(inv_freq[k])) return DATTN_ERR_INVALID_ARG;
+    for (int32_t k = 0; k < n; ++k) {
+        const double t = inv_freq[k] / 6.283185307179586476925;
+        const double frac = t - std::floor(t);  // [0, 1]
+        turns[k] = frac < 1.0 ? (uint64_t)std::ldexp(frac, 64) : 0u;
+    }
+    return DATTN_OK;
+}
+
+// The checks of a rotation for rows of head_dim channels.
+static dattn_status_t check_rotation(const dattn_rotation* r, int32_t head_dim) {
+    if (r->rot_dim < 0 || r->rot_dim > head_dim || (r->interleaved & ~1) ||
+        !std::isfinite(r->amplitude) || (r->rot_dim > 0 && r->turns == nullptr))
+        return DATTN_ERR_INVALID_ARG;
+    return r->rot_dim % 16 == 0 ? DATTN_OK : DATTN_ERR_UNSUPPORTED;
+}
+
+dattn_status_t dattn_rope(const dattn_rotation* rotation, const void* x, int64_t x_stride,
+                          void* out, int64_t out_stride, int32_t N, int32_t H, int32_t head_dim,
+                          int32_t elem_f32, const int32_t* positions, int32_t inverse,
+                          void* stream) {
+    if (rotation == nullptr || N < 0 || H <= 0 || head_dim <= 0 || (elem_f32 & ~1) ||
+        (inverse & ~1))
+        return DATTN_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return DATTN_ERR_UNSUPPORTED;
+    if (H > kMaxItems) return DATTN_ERR_UNSUPPORTED;
+    const dattn_status_t st = check_rotation(rotation, head_dim);
+    if (st != DATTN_OK) return st;
+    if (N == 0) return DATTN_OK;
+    if (!x || !out || !positions) return DATTN_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)H * head_dim, align = elem_f32 ? 4 : 8;
+    if (!aligned16(x) || !aligned16(out) || x_stride % align != 0 || out_stride % align != 0)
+        return DATTN_ERR_INVALID_ARG;
+    if (N > 1 && (x_stride < row || out_stride < row)) return DATTN_ERR_INVALID_ARG;
+    if (x == out && N > 1 && x_stride != out_stride) return DATTN_ERR_INVALID_ARG;
+    return launch_rope(rotation, x, x_stride, out, out_stride, N, H, head_dim, elem_f32 != 0,
+                       positions, inverse != 0, static_cast<cudaStream_t>(stream));
+}
+
+dattn_status_t dattn_rope_append(const dattn_kv_layout* layout, void* k_pool, void* v_pool,
+                                 dattn_bf16* stats, const dattn_rotation* rotation,
+                                 const dattn_bf16* q, int64_t q_stride, const dattn_bf16* k_new,
+                                 int64_t k_stride, const dattn_bf16* v_new, int64_t v_stride,
+                                 int32_t B, int32_t T, int32_t Hq, dattn_bf16* q_out,
+                                 int32_t* seq_lens, const int32_t* positions,
+                                 const int32_t* new_lens, int32_t advance, int32_t* dev_err,
+                                 void* stream) {
+    dattn_status_t st = check_layout(layout);
+    if (st != DATTN_OK) return st;
+    const int32_t d = layout->head_dim;
+    if (B < 0 || T < 0 || Hq < 0 || (advance & ~1)) return DATTN_ERR_INVALID_ARG;
+    if (rotation != nullptr && (st = check_rotation(rotation, d)) != DATTN_OK) return st;
+    if (Hq > kMaxItems) return DATTN_ERR_UNSUPPORTED;
+    if (B == 0 || T == 0) return DATTN_OK;
+    if (!k_pool || !v_pool || !k_new || !v_new || !seq_lens) return DATTN_ERR_INVALID_ARG;
+    if ((q == nullptr) != (q_out == nullptr) || (q != nullptr && Hq == 0))
+        return DATTN_ERR_INVALID_ARG;
+    if (q == nullptr) Hq = 0;
+    if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(k_new) || !aligned16(v_new) ||
+        !aligned16(q) || !aligned16(q_out) || (stats && !aligned16(stats)))
+        return DATTN_ERR_INVALID_ARG;
+    if (k_stride % 8 != 0 || v_stride % 8 != 0 || (q != nullptr && q_stride % 8 != 0))
+        return DATTN_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)layout->num_kv_heads * d;
+    if ((int64_t)B * T > 1 && (k_stride < row || v_stride < row ||
+                               (q != nullptr && q_stride < (int64_t)Hq * d)))
+        return DATTN_ERR_INVALID_ARG;
+    if (q != nullptr && q == q_out && (int64_t)B * T > 1 && q_stride != (int64_t)Hq * d)
+        return DATTN_ERR_INVALID_ARG;
+    if ((int64_t)B * T >= (1ll << 31) / 8 || B > 65535) return DATTN_ERR_UNSUPPORTED;
+    return launch_rope_append(*layout, k_pool, v_pool, stats, rotation, q, q_stride, k_new,
+                              k_stride, v_new, v_stride, B, T, Hq, q_out, seq_lens, positions,
+                              new_lens, advance != 0, dev_err,
+                              static_cast<cudaStream_t>(stream));
 }
 
 dattn_status_t dattn_partial(const dattn_kv_layout* layout, const void* k_pool,
@@ -347,6 +464,8 @@ dattn_status_t decode_impl(const dattn_kv_layout* layout, const void* k_pool, co
     if (num_splits < 0 || T < 1) return DATTN_ERR_INVALID_ARG;
     if ((Hq / layout->num_kv_heads) * (int64_t)T > kMaxGroup) return DATTN_ERR_UNSUPPORTED;
     if (T > 1 && sparse != nullptr) return DATTN_ERR_UNSUPPORTED;
+    // the fused append would rewrite rows of a block-scaled page that other CTAs are reading
+    if (app != nullptr && layout->kv_format == DATTN_KV_FP8_BLOCK) return DATTN_ERR_UNSUPPORTED;
     if (B == 0) return DATTN_OK;
     if (!k_pool || !v_pool || !q || !seq_lens || !out) return DATTN_ERR_INVALID_ARG;
     if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(q)) return DATTN_ERR_INVALID_ARG;

@@ -74,9 +74,11 @@ struct Smem {
     // head-aligned plan: kAplanScalars scalars, the retrieval heads, the streaming heads
     __device__ int32_t* aplan() const { return reinterpret_cast<int32_t*>(base + L.aplan); }
     __device__ int32_t* scan() const { return reinterpret_cast<int32_t*>(base + L.scan); }
-    // the 8-bit pool's row scales of stage s: 16 K scales, then 16 V scales
+    // the scales of stage s: 16 K row scales, then 16 V row scales (block-scaled pool: the K and
+    // V scales of an even and of the next tile)
+    template <int FMT>
     __device__ const float* scales(int s) const {
-        return reinterpret_cast<const float*>(base + L.scales) + 32 * s;
+        return reinterpret_cast<const float*>(base + L.scales) + attn_scale_bytes(FMT) / 4u * s;
     }
 };
 
@@ -311,16 +313,18 @@ struct PieceIter {
 // With the fused append, the tile that holds the new token carries its row: the consumer
 // writes the new token's K and V into that row of the stage before using it.
 // With the mixed pool, yc is the tile's row in its format's region (y, over all heads, still
-// addresses the row scales) and kTileI4 marks a 4-bit tile.
+// addresses the row scales) and kTileI4 marks a 4-bit tile. With the block-scaled pool, kTileOdd
+// marks a tile whose scales are the second pair of the 16 bytes that hold them.
 struct TileRef {
     int32_t y;
     int32_t lohi;  // lo | hi << 8 | skip << 16 | patch << 17 | patch row << 18 | 4-bit << 22 |
-                   // (cut + 16) << 24, cut clamped to [-16, 16]
+                   // odd << 23 | (cut + 16) << 24, cut clamped to [-16, 16]
     int32_t yc;
 };
 constexpr int32_t kTileSkip = 1 << 16;
 constexpr int32_t kTilePatch = 1 << 17;
 constexpr int32_t kTileI4 = 1 << 22;
+constexpr int32_t kTileOdd = 1 << 23;
 __device__ __forceinline__ int32_t tile_lo(int32_t m) { return m & 0xff; }
 __device__ __forceinline__ int32_t tile_hi(int32_t m) { return (m >> 8) & 0xff; }
 __device__ __forceinline__ int32_t tile_cut(int32_t m) { return ((m >> 24) & 63) - 16; }
@@ -407,6 +411,7 @@ __device__ __forceinline__ TileRef resolve_tile(const AttnParams& p, const Smem&
     }
     r.y = (page * p.Hkv + h) * p.P + (t0 - lp * p.P);
     r.lohi = lo | (hi << 8) | ((cut + 16) << 24);
+    if (p.fmt == DATTN_KV_FP8_BLOCK && ((r.y >> 4) & 1)) r.lohi |= kTileOdd;
     if (p.fmt == DATTN_KV_MIXED) {
         const bool i4 = head_is_i4(p.hf, h);
         const int32_t hc = i4 ? p.hf.h4 : p.Hkv - p.hf.h4;
@@ -450,6 +455,9 @@ __device__ __forceinline__ void write_final(const AttnParams& p, int32_t s, int3
 // when a tile brings a larger one). So 0 <= w_i <= 2^15 always fits fp16, and w_i is
 // split into two fp16 terms (22 significant bits) as the bf16 path splits p_i. The
 // accumulator is multiplied by r * 2^-15 when the piece is published.
+// The block-scaled 8-bit pool takes the same path with one K and one V scale for the tile: the
+// scales are warp-uniform, so raising r needs no reduction, and a tile brings 16 bytes of
+// scales (a bulk copy's least) instead of 128.
 // PK: 2 or 4 query columns over the 4-bit pool, whose PV weights take one product per m-tile
 // (see tile_i4). (A mixed-pool instance would work the same way for its 4-bit heads.)
 template <int D, int FMT, bool PK>
@@ -458,6 +466,7 @@ struct Consumer {
     static constexpr bool Q = FMT != DATTN_KV_BF16;  // a quantized pool with row scales
     static constexpr bool I4 = FMT == DATTN_KV_INT4;
     static constexpr bool MIX = FMT == DATTN_KV_MIXED;  // 8-bit or 4-bit per KV head
+    static constexpr bool BLK = FMT == DATTN_KV_FP8_BLOCK;  // one K and one V scale per tile
     static_assert(!I4 || Q, "the 4-bit pool is a quantized pool");
     static_assert(!MIX || Q, "the mixed pool is a quantized pool");
     static_assert(!PK || I4 || MIX, "packed columns are a 4-bit form");
@@ -796,7 +805,8 @@ struct Consumer {
     }
 
     // One 16-token tile of the 8-bit pool in stage buffer `st` (K codes, then V codes) with
-    // its row scales `sc`; rows are masked as in tile().
+    // its row scales `sc` (block-scaled pool: its K scale and its V scale); rows are masked as in
+    // tile().
     __device__ void tile_f8(uint32_t st, const float* sc, int lo, int hi, int cut) {
         const uint32_t kbase = st, vbase = st + 16u * D;
         const int g8 = lane >> 2, tig = lane & 3;
@@ -816,15 +826,21 @@ struct Consumer {
             e4m3x4_to_f16(r3, a1, a3);
             mma_f16(sb, a0, a1, a2, a3, qf[2 * c + 1][0], qf[2 * c + 1][1]);
         }
-        const float kc0 = sc[g8] * qsc, kc1 = sc[g8 + 8] * qsc;
+        const float kc0 = sc[BLK ? 0 : g8] * qsc, kc1 = BLK ? kc0 : sc[g8 + 8] * qsc;
         float s0 = (sa[0] + sb[0]) * kc0, s1 = (sa[1] + sb[1]) * kc0;
         float s2 = (sa[2] + sb[2]) * kc1, s3 = (sa[3] + sb[3]) * kc1;
-        float vs0 = sc[16 + g8], vs1 = sc[24 + g8];
+        float vs0 = sc[BLK ? 1 : 16 + g8], vs1 = BLK ? vs0 : sc[24 + g8];
+        const float vtile = vs0;  // block-scaled pool: the tile's V scale
         mask_tile(lo, hi, cut, s0, s1, s2, s3, vs0, vs1);
+        if constexpr (BLK) vs0 = vs1 = vtile;  // masked rows have weight 0
         float p0, p1, p2, p3;
         softmax(s0, s1, s2, s3, p0, p1, p2, p3);
         // ---- V scales: raise r to a power of two >= every V scale of the tile ---------
-        raise_r(fmaxf(vs0, vs1));
+        if constexpr (BLK) {
+            if (vtile > rv) raise_r_to(vtile);  // warp-uniform
+        } else {
+            raise_r(fmaxf(vs0, vs1));
+        }
         const float vn0 = vs0 * inv, vn1 = vs1 * inv;  // in [0, 2^15], exact
         const float w0 = p0 * vn0, w1 = p1 * vn0, w2 = p2 * vn1, w3 = p3 * vn1;
         // ---- W^T as the B operand: two fp16 terms, transposed with movmatrix ----------
@@ -906,22 +922,24 @@ struct Consumer {
     // O (and the 4-bit weight sums). The maximum over the warp is taken only when some lane's
     // exceeds r.
     __device__ __forceinline__ void raise_r(float vl) {
-        if (__any_sync(0xffffffffu, vl > rv)) {
-            const float vt = warp_vmax(vl);  // > r >= 2^-112: a normal number
-            const int32_t bits = __float_as_int(vt);
-            const int32_t k = min(127, ((bits >> 23) & 0xff) - 127 + ((bits & 0x7fffff) != 0));
-            const int32_t dk = rk - k;
-            const float f = dk >= -126 ? __int_as_float((127 + dk) << 23) : 0.f;
+        if (__any_sync(0xffffffffu, vl > rv)) raise_r_to(warp_vmax(vl));
+    }
+
+    // The same for a warp-uniform vt > r (r >= 2^-112, so vt is a normal number).
+    __device__ __forceinline__ void raise_r_to(float vt) {
+        const int32_t bits = __float_as_int(vt);
+        const int32_t k = min(127, ((bits >> 23) & 0xff) - 127 + ((bits & 0x7fffff) != 0));
+        const int32_t dk = rk - k;
+        const float f = dk >= -126 ? __int_as_float((127 + dk) << 23) : 0.f;
 #pragma unroll
-            for (int mt = 0; mt < KS; ++mt) {
-                o[mt][0] *= f; o[mt][1] *= f; o[mt][2] *= f; o[mt][3] *= f;
-            }
-            ws0 *= f;
-            ws1 *= f;
-            rk = k;
-            rv = __int_as_float((127 + k) << 23);
-            inv = __int_as_float((142 - k) << 23);
+        for (int mt = 0; mt < KS; ++mt) {
+            o[mt][0] *= f; o[mt][1] *= f; o[mt][2] *= f; o[mt][3] *= f;
         }
+        ws0 *= f;
+        ws1 *= f;
+        rk = k;
+        rv = __int_as_float((127 + k) << 23);
+        inv = __int_as_float((142 - k) << 23);
     }
 
     // O^T += V^T W^T for one tile with this lane's weights (rows g8: w0, w1; g8 + 8: w2, w3).
@@ -1423,7 +1441,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
         if (!any) return;
         const uint64_t pol = policy_evict_first();
         const uint32_t tile_bytes = attn_tile_bytes(FMT, D);
-        const uint32_t tx = 2u * tile_bytes + (Q ? 128u : 0u);  // + the tile's 32 scales
+        const uint32_t tx = 2u * tile_bytes + attn_scale_bytes(FMT);  // the tile and its scales
         const uint32_t stages0 = smem_u32(sm.base + sm.L.stages);
         int32_t k = 0;  // real tiles issued so far: tile k uses stage k % NS
         bool stop = false;
@@ -1462,17 +1480,22 @@ attention_kernel(const __grid_constant__ AttnParams p,
                             const uint32_t dst = stages0 + (uint32_t)stg * sm.L.stage_bytes;
                             tma_load_2d(dst, f4 ? &tmap_k4 : &tmap_k, 0, yc, full, pol);
                             tma_load_2d(dst + tb, f4 ? &tmap_v4 : &tmap_v, 0, yc, full, pol);
-                            bulk_copy(smem_u32(sm.scales(stg)), p.kv_scale + 2 * y, 128u, full,
-                                      pol);
+                            bulk_copy(smem_u32(sm.scales<FMT>(stg)), p.kv_scale + 2 * y, 128u,
+                                      full, pol);
                         } else {
                             mbar_arrive_expect_tx(full, tx);
                             const uint32_t dst = stages0 + (uint32_t)stg * sm.L.stage_bytes;
                             if constexpr (Q) {
                                 tma_load_2d(dst, &tmap_k, 0, y, full, pol);
                                 tma_load_2d(dst + tile_bytes, &tmap_v, 0, y, full, pol);
-                                // the tile's scales: 128 bytes at tile index y / 16
-                                bulk_copy(smem_u32(sm.scales(stg)), p.kv_scale + 2 * y, 128u,
-                                          full, pol);
+                                // the tile's scales: 128 bytes at tile index y / 16 (block-
+                                // scaled pool: 16 bytes, those of tiles 2 (y / 32) and the next)
+                                if constexpr (FMT == DATTN_KV_FP8_BLOCK)
+                                    bulk_copy(smem_u32(sm.scales<FMT>(stg)),
+                                              p.kv_scale + 4 * (y >> 5), 16u, full, pol);
+                                else
+                                    bulk_copy(smem_u32(sm.scales<FMT>(stg)), p.kv_scale + 2 * y,
+                                              128u, full, pol);
                             } else {
                                 tma_load_3d(dst, &tmap_k, 0, y, 0, full, pol);
                                 tma_load_3d(dst + tile_bytes, &tmap_v, 0, y, 0, full, pol);
@@ -1614,11 +1637,12 @@ attention_kernel(const __grid_constant__ AttnParams p,
                     // fused append: the new token's codes and scales into this stage, quantized
                     // here exactly as the write half quantizes them (the warp's lanes together)
                     const bool patched = APP && (lohi & kTilePatch) != 0;
+                    const float* sc = sm.scales<FMT>(stg);
                     if (patched)
-                        cons.store_row_q(st, const_cast<float*>(sm.scales(stg)),
-                                         tile_patch_row(lohi), t4);
-                    if (t4) cons.tile_i4(st, sm.scales(stg), lo, hi, cut);
-                    else    cons.tile_f8(st, sm.scales(stg), lo, hi, cut);
+                        cons.store_row_q(st, const_cast<float*>(sc), tile_patch_row(lohi), t4);
+                    if constexpr (FMT == DATTN_KV_FP8_BLOCK) sc += lohi & kTileOdd ? 2 : 0;
+                    if (t4) cons.tile_i4(st, sc, lo, hi, cut);
+                    else    cons.tile_f8(st, sc, lo, hi, cut);
                     // generic writes to the stage before TMA refills it
                     if (patched) fence_proxy_async_smem();
                 } else {
@@ -1858,6 +1882,13 @@ dattn_status_t launch_attention(const AttnParams& p, const void* k_pool, const v
     // 4-bit heads keep two products per m-tile: a packed instance of the mixed kernel slowed
     // its 8-bit tiles, 27.0 against 25.1 µs per sparse-512k launch.)
     const bool pk = p.fmt == DATTN_KV_INT4 && (p.gq == 2 || p.gq == 4);
+    if (p.fmt == DATTN_KV_FP8_BLOCK) {
+        if (p.append != 0) return DATTN_ERR_UNSUPPORTED;  // refused at the entry
+        return D == 64 ? launch_d<64, DATTN_KV_FP8_BLOCK, false, false>(
+                             p, k_pool, v_pool, num_splits, ws, ws_bytes, stream, tiles_bound)
+                       : launch_d<128, DATTN_KV_FP8_BLOCK, false, false>(
+                             p, k_pool, v_pool, num_splits, ws, ws_bytes, stream, tiles_bound);
+    }
     auto pick = [&](auto bf16, auto f8, auto i4, auto mix, auto i4p) {
         return p.fmt == DATTN_KV_MIXED    ? mix
              : p.fmt == DATTN_KV_INT4     ? (pk ? i4p : i4)

@@ -23,20 +23,25 @@ constexpr int kStagesI4 = 16;
 // The mixed pool's stages are 8-bit stages; a 4-bit tile fills half of one.
 __host__ __device__ constexpr int attn_stages(int fmt) {
     return fmt == DATTN_KV_INT4 ? kStagesI4
-         : (fmt == DATTN_KV_FP8_E4M3 || fmt == DATTN_KV_MIXED) ? kStagesF8
-                                                                : kStagesBf16;
+         : fmt != DATTN_KV_BF16   ? kStagesF8
+                                  : kStagesBf16;
 }
 // Bytes of one K (or V) tile of 16 tokens in shared memory for a pool format (the mixed
 // pool: the larger, 8-bit tile).
 __host__ __device__ constexpr uint32_t attn_tile_bytes(int fmt, int D) {
-    return (fmt == DATTN_KV_INT4 ? 8u
-            : (fmt == DATTN_KV_FP8_E4M3 || fmt == DATTN_KV_MIXED) ? 16u
-                                                                   : 32u) * (uint32_t)D;
+    return (fmt == DATTN_KV_INT4 ? 8u : fmt != DATTN_KV_BF16 ? 16u : 32u) * (uint32_t)D;
+}
+// Bytes of a stage's scales: 16 K and 16 V row scales, or, for the block-scaled pool, the
+// aligned 16 bytes that hold the K and V scales of the tile and of its even or odd neighbour
+// (the smallest bulk copy).
+__host__ __device__ constexpr uint32_t attn_scale_bytes(int fmt) {
+    return fmt == DATTN_KV_BF16 ? 0u : fmt == DATTN_KV_FP8_BLOCK ? 16u : 128u;
 }
 constexpr int kMaxItems = 4096;     // B (or C) bound
 constexpr int kMaxKvHeads = 256;
 constexpr int kMaxGroup = 8;        // query heads per KV head
 constexpr int kMaxTopK = 256;
+constexpr int kMaxHeadDim = 128;
 constexpr int kMaxCtasPerSm = 4;    // bound used for workspace sizing with automatic splits
 constexpr int32_t kSegCost = 6;     // cost units per segment in the balanced split
 
@@ -151,7 +156,7 @@ __host__ __device__ inline AttnSmem attn_smem_layout(int D, int g, int nitems, i
     s.stage_bytes = 2u * attn_tile_bytes(fmt, D);
     uint32_t o = 0;
     s.stages = o;      o += ns * s.stage_bytes;
-    s.scales = o;      o += fmt != DATTN_KV_BF16 ? ns * 128u : 0u;
+    s.scales = o;      o += ns * attn_scale_bytes(fmt);
     s.bars = o;        o += 2u * ns * 8u;
     s.meta = o;        o += ns * 4u;
     s.flags = o;       o += 32u;  // abort flag, last flag, then 5 plan constants
@@ -180,6 +185,18 @@ dattn_status_t make_kv_tensor_map(void* tmap_out, const void* pool, int64_t rows
 // d / 2), one box of 16 rows, swizzled by the row size (128, 64 or 32 bytes).
 dattn_status_t make_kv_tensor_map_u8(void* tmap_out, const void* pool, int64_t rows,
                                      int row_bytes);
+
+// The kernels of dattn_rope and dattn_rope_append (rope.cu).
+dattn_status_t launch_rope(const dattn_rotation* rot, const void* x, int64_t x_stride, void* out,
+                           int64_t out_stride, int32_t N, int32_t H, int32_t D, bool f32,
+                           const int32_t* positions, bool inverse, cudaStream_t stream);
+dattn_status_t launch_rope_append(const dattn_kv_layout& L, void* k_pool, void* v_pool,
+                                  uint16_t* stats, const dattn_rotation* rot, const uint16_t* q,
+                                  int64_t q_stride, const uint16_t* k_new, int64_t k_stride,
+                                  const uint16_t* v_new, int64_t v_stride, int32_t B, int32_t T,
+                                  int32_t Hq, uint16_t* q_out, int32_t* seq_lens,
+                                  const int32_t* positions, const int32_t* new_lens, bool advance,
+                                  int32_t* dev_err, cudaStream_t stream);
 
 dattn_status_t launch_attention(const AttnParams& p, const void* k_pool, const void* v_pool,
                                 int D, int32_t num_splits, void* ws, size_t ws_bytes,

@@ -7,10 +7,10 @@ from __future__ import annotations
 
 import torch
 
-from . import (KV_BF16, KV_FP8_E4M3, KV_INT4, KV_MIXED, KVLayout, SparseConfig, Workspace,
-               mixed_pool_bytes,
+from . import (KV_BF16, KV_FP8_BLOCK, KV_FP8_E4M3, KV_INT4, KV_MIXED, KVLayout, SparseConfig,
+               Workspace, kv_scale_floats, mixed_pool_bytes,
                dattn_append_decode, dattn_decode, dattn_decode_multi, dattn_kv_append,
-               dattn_page_select)
+               dattn_page_select, dattn_rope_append)
 from .workloads import Case
 
 
@@ -22,7 +22,8 @@ class PagedCache:
     page: 16 K scales, then 16 V scales); KV_INT4 keeps [num_pages][Hkv][P][d/2] bytes of two
     4-bit codes each, with kv_scale as for KV_FP8_E4M3. KV_MIXED keeps each KV head in the
     format head_format[h] names (flat uint8 pools: the 8-bit heads' region, then the 4-bit
-    heads' region).
+    heads' region). KV_FP8_BLOCK keeps uint8 E4M3 codes plus one power-of-two K scale and V
+    scale per (logical page, KV head) in kv_scale, flat [num_pages][Hkv][P/16][2] and padding.
     """
 
     def __init__(self, case: Case, device="cuda", with_stats: bool = False, fill: bool = True,
@@ -34,7 +35,7 @@ class PagedCache:
         alloc = torch.zeros if zero_pool else torch.empty
         self.kv_format = kv_format
         self.head_format = list(head_format) if head_format is not None else None
-        quant = kv_format in (KV_FP8_E4M3, KV_INT4, KV_MIXED)
+        quant = kv_format in (KV_FP8_E4M3, KV_INT4, KV_MIXED, KV_FP8_BLOCK)
         elem = torch.uint8 if quant else torch.bfloat16
         if kv_format == KV_MIXED:
             nbytes = mixed_pool_bytes(c.num_pages, self.head_format, c.d, c.P)
@@ -45,7 +46,10 @@ class PagedCache:
             self.k_pool = alloc(c.num_pages, c.Hkv, c.P, row, dtype=elem, device=device)
             self.v_pool = alloc(c.num_pages, c.Hkv, c.P, row, dtype=elem, device=device)
         self.kv_scale = None
-        if quant:
+        if kv_format == KV_FP8_BLOCK:
+            self.kv_scale = alloc(kv_scale_floats(kv_format, c.num_pages, c.Hkv, c.P),
+                                  dtype=torch.float32, device=device)
+        elif quant:
             self.kv_scale = alloc(c.num_pages, c.Hkv, c.P // 16, 2, 16, dtype=torch.float32,
                                   device=device)
         self.stats = None
@@ -99,6 +103,18 @@ class PagedCache:
         dattn_kv_append(self.layout, self.k_pool, self.v_pool, self.stats, k_new, v_new,
                         self.seq_lens, self.dev_err)
         self.lens = [L + T for L in self.lens]
+
+    def rope_append(self, rotation, q, k_new, v_new, q_out, positions=None, new_lens=None):
+        """One batched append of k_new/v_new ([B][T][Hkv][d]) at the current lengths, q and k_new
+        rotated on the way (dattn_rope_append); new_lens: a list of the requests' new tokens."""
+        T = k_new.shape[1]
+        counts = [T] * self.case.B if new_lens is None else list(new_lens)
+        if new_lens is not None:
+            new_lens = torch.tensor(counts, dtype=torch.int32, device=self.device)
+        dattn_rope_append(self.layout, self.k_pool, self.v_pool, self.stats, rotation, q, k_new,
+                          v_new, q_out, self.seq_lens, positions=positions, new_lens=new_lens,
+                          dev_err=self.dev_err)
+        self.lens = [L + n for L, n in zip(self.lens, counts)]
 
     def workspace(self, top_k: int = 0, num_splits: int = 0, queries: int = 1) -> Workspace:
         """A workspace for decode (T query tokens per request: queries = T) or selection."""

@@ -1,0 +1,322 @@
+"""The block-scaled 8-bit pool on the GPU: what the append stores, bit for bit, and the attention
+over it against a 64-bit softmax over the reference's own values.
+
+The attention's tolerance is the bound that _block_ref.attention derives, row by row; m and e
+follow from the same logit error (m: the error itself; e: its relative size).
+"""
+import numpy as np
+import pytest
+import torch
+
+import split_kv_decode_distattention_gb300 as dattn
+from split_kv_decode_distattention_gb300 import workloads as W
+from split_kv_decode_distattention_gb300.harness import PagedCache
+
+import _block_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+BLOCK = dattn.KV_FP8_BLOCK
+
+
+def _cache(case, fill=False, stats=False, junk=False, **kw):
+    c = PagedCache(case, DEV, with_stats=stats, kv_format=BLOCK, fill=fill, zero_pool=True, **kw)
+    if junk:  # what recycled pages may hold: NaN codes and any scale
+        c.k_pool.fill_(0x7F)
+        c.v_pool.fill_(0xFF)
+        c.kv_scale.fill_(float("nan"))
+    return c
+
+
+def _pools(case, junk=False):
+    a = dict(codes=0x7F, scale=float("nan")) if junk else {}
+    b = dict(codes=0xFF, scale=float("nan")) if junk else {}
+    n = (case.num_pages, case.Hkv, case.P, case.d)
+    return ref.BlockPool(*n, **a), ref.BlockPool(*n, **b)
+
+
+def _assert_pool(cache, kp, vp):
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(cache.k_pool.cpu().numpy(), kp.codes)
+    np.testing.assert_array_equal(cache.v_pool.cpu().numpy(), vp.codes)
+    n = kp.scale.size
+    sc = cache.kv_scale[:2 * n].cpu().numpy().reshape(*kp.scale.shape, 2)
+    np.testing.assert_array_equal(sc[..., 0].view(np.uint32), kp.scale.view(np.uint32))
+    np.testing.assert_array_equal(sc[..., 1].view(np.uint32), vp.scale.view(np.uint32))
+
+
+def _rows(shape, seed, spread=0):
+    """bf16 rows; spread > 0: each token has its own power-of-two size."""
+    rng = np.random.default_rng(seed)
+    x = rng.normal(size=shape).astype(np.float32)
+    if spread:
+        x *= np.exp2(rng.integers(-spread, spread + 1, size=(*shape[:2], 1, 1))).astype(np.float32)
+    return torch.from_numpy(x).to(torch.bfloat16).to(DEV)
+
+
+@pytest.mark.parametrize("d,P", [(128, 16), (64, 64), (128, 80), (64, 256)])
+def test_append_stores_the_formats_codes_and_scales(d, P):
+    """Single tokens, windows and long chunks, tokens of very different sizes: scales are raised
+    and earlier codes rounded again; recycled pages' contents take no part."""
+    case = W.Case("blk", B=3, Hq=3, Hkv=3, d=d, P=P, lens=[0, 0, 0], seed=3, reserve_tokens=420)
+    cache = _cache(case, junk=True)
+    kp, vp = _pools(case, junk=True)
+    for step, T in enumerate([1, 1, 13, 1, 40, 1, 7, 230, 1, 1]):
+        k, v = _rows((3, T, 3, d), 10 + step, 9), _rows((3, T, 3, d), 90 + step, 3)
+        for b in range(3):
+            for pool, x in ((kp, k), (vp, v)):
+                pool.append(case.block_table[b], cache.lens[b], x[b].double().cpu().numpy())
+        cache.append(k, v)
+        _assert_pool(cache, kp, vp)
+    assert int(cache.dev_err.item()) == 0
+
+
+def test_append_of_corner_values():
+    """Zeros of both signs, a scale's border (448 and the next bf16 value), E4M3 ties and
+    subnormals, the smallest and largest bf16 values, infinities and NaN."""
+    d = 64
+    x = torch.zeros(20, 1, d)
+    x[1, 0, :] = -0.0
+    x[2, 0, 0], x[3, 0, 0] = 448.0, 450.0
+    x[4, 0, :] = 1.0625
+    x[5, 0, :8] = torch.tensor([2.0 ** -9, 2.0 ** -10, 1.5 * 2.0 ** -10, 2.0 ** -11, -2.0 ** -10,
+                                3 * 2.0 ** -10, 5 * 2.0 ** -10, 7 * 2.0 ** -10])
+    x[6, 0, 0] = 2.0 ** -133  # a subnormal bf16 value
+    x[7, 0, 0] = 3.3895313892515355e38
+    x = x.to(torch.bfloat16).to(DEV)
+    for order in ([0, 1], [2], [3], [2, 3], [4], [5, 2], [6], [6, 0, 4], [7], [5, 4, 3, 7],
+                  [0, 6, 5, 4, 2, 3, 7]):
+        case = W.Case("corner", B=1, Hq=1, Hkv=1, d=d, P=16, lens=[0], seed=1)
+        cache, (kp, vp) = _cache(case, junk=True), _pools(case, junk=True)
+        for i in order:  # one by one
+            row = x[i].view(1, 1, 1, d)
+            cache.append(row, -row)
+            kp.append(case.block_table[0], cache.lens[0] - 1, x[i].double().cpu().numpy()[None])
+            vp.append(case.block_table[0], cache.lens[0] - 1, -x[i].double().cpu().numpy()[None])
+            _assert_pool(cache, kp, vp)
+        one, (kp, vp) = _cache(case, junk=True), _pools(case, junk=True)  # in one call
+        rows = x[order].view(1, len(order), 1, d)
+        one.append(rows, -rows)
+        kp.append(case.block_table[0], 0, x[order].double().cpu().numpy())
+        vp.append(case.block_table[0], 0, -x[order].double().cpu().numpy())
+        _assert_pool(one, kp, vp)
+    # infinities saturate, a NaN stays one and does not enter the scale
+    case = W.Case("inf", B=1, Hq=1, Hkv=1, d=d, P=16, lens=[0], seed=1)
+    cache = _cache(case)
+    k = torch.ones(1, 2, 1, d, dtype=torch.bfloat16, device=DEV)
+    k[0, 0, 0, 0], k[0, 1, 0, 1] = float("inf"), float("nan")
+    cache.append(k, k)
+    torch.cuda.synchronize()
+    page = int(case.block_table[0, 0])
+    codes = cache.k_pool[page, 0].cpu().numpy()
+    assert codes[0, 0] == 0x7E and codes[1, 1] & 0x7F == 0x7F and codes[0, 1] == 0
+    assert cache.kv_scale.view(-1, 2)[page, 0].item() == 2.0 ** 119
+
+
+def test_append_statistics_are_the_keys():
+    """k_max and k_min come from the bf16 keys, as for the other pools."""
+    case = W.Case("st", B=2, Hq=2, Hkv=2, d=64, P=32, lens=[50, 19], seed=5)
+    a = _cache(case, fill=True, stats=True)
+    b = PagedCache(case, DEV, with_stats=True, zero_pool=True)
+    for T in (1, 30, 1):
+        k, v = a.new_tokens(T)
+        a.append(k, v)
+        b.append(k, v)
+    torch.cuda.synchronize()
+    assert torch.equal(a.stats.view(torch.int16), b.stats.view(torch.int16))
+
+
+# ---------------------------------------------------------------- attention
+
+def _filled(case, seed, stats=False, junk=True, steps=(1.0,)):
+    """A cache filled request by request, and the reference's pools."""
+    cache, (kp, vp) = _cache(case, stats=stats, junk=junk), _pools(case, junk)
+    for b, L in enumerate(case.lens):
+        if L == 0:
+            continue
+        k = _rows((1, L, case.Hkv, case.d), seed + b, 2)
+        v = _rows((1, L, case.Hkv, case.d), seed + 50 + b, 2)
+        at = 0
+        for part in (L - L // 3, L // 3):  # two calls: a block is extended
+            if part == 0:
+                continue
+            ks, vs = k[:, at:at + part].contiguous(), v[:, at:at + part].contiguous()
+            dattn.dattn_kv_append(cache._row_layout(b), cache.k_pool, cache.v_pool, cache.stats,
+                                  ks, vs, cache.seq_lens[b:b + 1], cache.dev_err)
+            kp.append(case.block_table[b], at, ks[0].double().cpu().numpy())
+            vp.append(case.block_table[b], at, vs[0].double().cpu().numpy())
+            at += part
+        cache.lens[b] = L
+    _assert_pool(cache, kp, vp)
+    return cache, kp, vp
+
+
+def _check(case, q, out, m, e, kp, vp, see_of=None):
+    """q, out [B][T][Hq][d]; see_of(b, kvh) -> [T][L] visible keys (default: causal)."""
+    B, T, Hq, d = q.shape
+    q64, o = q.double().cpu().numpy(), out.double().cpu().numpy()
+    mm, ee = (None if t is None else t.double().cpu().numpy() for t in (m, e))
+    for b in range(B):
+        L = case.lens[b]
+        K, V = kp.values(case.block_table[b], L), vp.values(case.block_table[b], L)
+        causal = np.arange(L)[None] <= (L - T + np.arange(T))[:, None]
+        for h in range(Hq):
+            kvh = h // case.g
+            see = causal if see_of is None else see_of(b, kvh)
+            w, wm, we, tol, t = ref.attention(q64[b, :, h], K[:, kvh], V[:, kvh], case.scale, see)
+            err = np.abs(o[b, :, h] - w).max(-1)
+            assert (err <= tol + 2.0 ** -23 * np.abs(w).max(-1, initial=0.0)).all(), (
+                b, h, L, err, tol)
+            if mm is not None:
+                none = ~np.isfinite(wm)
+                assert (mm[b, none, h] == -np.inf).all() and (ee[b, none, h] == 0).all()
+                ok = ~none
+                assert (np.abs(mm[b, ok, h] - wm[ok]) <= t[ok] + 2.0 ** -22 * np.abs(wm[ok])).all()
+                assert (np.abs(ee[b, ok, h] / we[ok] - 1) <= 2 * t[ok] + 2.0 ** -20).all()
+
+
+CASES = [
+    # B, Hq, Hkv, d, P, lens
+    (4, 4, 4, 128, 16, [1, 0, 17, 300]),
+    (3, 16, 2, 128, 64, [64, 63, 1000]),
+    (2, 6, 2, 64, 48, [2000, 5]),
+    (2, 8, 4, 64, 256, [257, 511]),
+    (1, 5, 1, 128, 16, [3333]),
+]
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,d,P,lens", CASES)
+@pytest.mark.parametrize("splits", [0, 1, 13])
+def test_decode_over_the_block_scaled_pool(B, Hq, Hkv, d, P, lens, splits):
+    case = W.Case("dec", B=B, Hq=Hq, Hkv=Hkv, d=d, P=P, lens=lens, seed=6)
+    cache, kp, vp = _filled(case, 7)
+    q = _rows((B, 1, Hq, d), 77)
+    out = torch.full((B, Hq, d), float("nan"), device=DEV)
+    m, e = torch.full((B, Hq), float("nan"), device=DEV), torch.full((B, Hq), float("nan"),
+                                                                    device=DEV)
+    ws = cache.workspace(num_splits=splits)
+    for _ in range(2):
+        cache.decode(q[:, 0].contiguous(), out, ws, m, e, num_splits=splits)
+    torch.cuda.synchronize()
+    assert int(cache.dev_err.item()) == 0
+    _check(case, q, out[:, None], m[:, None], e[:, None], kp, vp)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv", [(2, 8, 2), (3, 2, 2), (8, 2, 2)])
+def test_multi_query_decode_over_the_block_scaled_pool(T, Hq, Hkv):
+    case = W.Case("multi", B=3, Hq=Hq, Hkv=Hkv, d=128, P=32, lens=[T, 200, 16 + T - 1], seed=6)
+    cache, kp, vp = _filled(case, 8)
+    q = _rows((3, T, Hq, 128), 78)
+    out = torch.empty(3, T, Hq, 128, device=DEV)
+    m, e = torch.empty(3, T, Hq, device=DEV), torch.empty(3, T, Hq, device=DEV)
+    cache.decode(q, out, cache.workspace(queries=T), m, e)
+    torch.cuda.synchronize()
+    assert int(cache.dev_err.item()) == 0
+    _check(case, q, out, m, e, kp, vp)
+
+
+def test_partials_over_the_block_scaled_pool_merge_to_the_whole():
+    case = W.Case("part", B=2, Hq=4, Hkv=2, d=128, P=16, lens=[700, 90], seed=6)
+    cache, kp, vp = _filled(case, 9)
+    q = _rows((2, 1, 4, 128), 79)
+    sets = [case.page_sets_of(b, case.lens[b]) for b in range(2)]
+    req = torch.tensor([b for b in range(2) for _ in sets[b]], dtype=torch.int32, device=DEV)
+    flat = [s for b in range(2) for s in sets[b]]
+    ind = torch.tensor(np.cumsum([0] + [len(s) for s in flat]), dtype=torch.int32, device=DEV)
+    pages = torch.tensor(np.concatenate(flat), dtype=torch.int32, device=DEV)
+    C = len(flat)
+    m, e, MA = (torch.empty(*s, device=DEV) for s in ((C, 4), (C, 4), (C, 4, 128)))
+    ws = dattn.Workspace(C, 4, 2, 128)
+    dattn.dattn_partial(cache.layout, cache.k_pool, cache.v_pool, q[:, 0].contiguous(), case.scale,
+                        cache.seq_lens, req, ind, pages, m, e, MA, ws, dev_err=cache.dev_err)
+    out = torch.empty(2, 4, 128, device=DEV)
+    heads = torch.tensor([0, len(sets[0]), C], dtype=torch.int32, device=DEV)
+    dattn.dattn_merge(heads, m, e, MA, out=out, dev_err=cache.dev_err)
+    torch.cuda.synchronize()
+    assert int(cache.dev_err.item()) == 0
+    _check(case, q, out[:, None], None, None, kp, vp)
+
+
+def test_block_sparse_decode_over_the_block_scaled_pool():
+    kinds = [W.HEAD_RETRIEVAL, W.HEAD_STREAMING, W.HEAD_DENSE]
+    case = W.Case("sparse", B=2, Hq=6, Hkv=3, d=64, P=64, lens=[1500, 70], seed=6, head_kind=kinds,
+                  top_k=5, sinks=4, local=24)
+    cache, kp, vp = _filled(case, 11, stats=True)
+    q = _rows((2, 1, 6, 64), 80)
+    sel = torch.empty(2, 3, 5, dtype=torch.int32, device=DEV)
+    cache.select(q[:, 0].contiguous(), sel, cache.workspace(top_k=5))
+    out = torch.empty(2, 6, 64, device=DEV)
+    cache.decode(q[:, 0].contiguous(), out, cache.workspace(), sparse=cache.sparse_config(sel))
+    torch.cuda.synchronize()
+    assert int(cache.dev_err.item()) == 0
+
+    def see_of(b, kvh):
+        t = np.arange(case.lens[b])
+        if kinds[kvh] == W.HEAD_RETRIEVAL:
+            return np.isin(t // 64, sel[b, kvh].cpu().numpy())[None]
+        if kinds[kvh] == W.HEAD_STREAMING:
+            return ((t < 4) | (t >= max(4, case.lens[b] - 24)))[None]
+        return np.ones((1, case.lens[b]), bool)
+
+    _check(case, q, out[:, None], None, None, kp, vp, see_of)
+
+
+def test_block_scales_of_every_size_in_one_sequence():
+    """Tiles whose V scales span 2^-100 .. 2^100 in any order, and tiles of zeros: the running
+    scale of the weighted sum is raised, and a tile far below it adds nothing."""
+    d, n = 64, 12
+    case = W.Case("range", B=1, Hq=2, Hkv=1, d=d, P=16, lens=[16 * n], seed=2)
+    cache, (kp, vp) = _cache(case, junk=True), _pools(case, junk=True)
+    k, v = _rows((1, 16 * n, 1, d), 1), _rows((1, 16 * n, 1, d), 2)
+    ex = [0, -100, 30, 3, -40, 100, 99, 0, -126, 60, 100, -3]
+    for i, x in enumerate(ex):
+        v[:, 16 * i:16 * i + 16] *= 2.0 ** x
+    v[:, 112:128] = 0
+    k[:, 32:48] = 0
+    cache.append(k, v)
+    kp.append(case.block_table[0], 0, k[0].double().cpu().numpy())
+    vp.append(case.block_table[0], 0, v[0].double().cpu().numpy())
+    _assert_pool(cache, kp, vp)
+    q = _rows((1, 1, 2, d), 3)
+    for splits in (1, 3):
+        out = torch.empty(1, 2, d, device=DEV)
+        cache.decode(q[:, 0].contiguous(), out, cache.workspace(num_splits=splits),
+                     num_splits=splits)
+        torch.cuda.synchronize()
+        _check(case, q, out[:, None], None, None, kp, vp)
+
+
+def test_a_step_appends_with_rotation_and_decodes():
+    """The operators together as a decode loop uses them, captured once and replayed: rotate and
+    append, then decode over the block-scaled pool."""
+    r = dattn.Rotation(128, base=500000.0)
+    case = W.Case("step", B=3, Hq=8, Hkv=2, d=128, P=16, lens=[5, 100, 31], seed=6)
+    cache, kp, vp = _filled(case, 13)
+    q, k, v = (torch.empty(3, 1, h, 128, dtype=torch.bfloat16, device=DEV) for h in (8, 2, 2))
+    qr, out, ws = torch.empty_like(q), torch.empty(3, 8, 128, device=DEV), cache.workspace()
+    lens = list(case.lens)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        dattn.dattn_rope_append(cache.layout, cache.k_pool, cache.v_pool, None, r, q, k, v, qr,
+                                cache.seq_lens, dev_err=cache.dev_err)
+        cache.decode(qr[:, 0], out, ws)
+    for step in range(4):
+        for i, t in enumerate((q, k, v)):
+            t.copy_(_rows(t.shape, 200 + 3 * step + i))
+        pos = cache.seq_lens.clone()
+        g.replay()
+        kr, want_q = torch.empty_like(k), torch.empty_like(q)
+        dattn.dattn_rope(r, k, kr, pos)
+        dattn.dattn_rope(r, q, want_q, pos)
+        torch.cuda.synchronize()
+        assert torch.equal(qr, want_q)
+        for b in range(3):
+            kp.append(case.block_table[b], lens[b], kr[b].double().cpu().numpy())
+            vp.append(case.block_table[b], lens[b], v[b].double().cpu().numpy())
+        lens = [n + 1 for n in lens]
+        case.lens = lens
+        assert cache.seq_lens.tolist() == lens and int(cache.dev_err.item()) == 0
+        _assert_pool(cache, kp, vp)
+        _check(case, qr, out[:, None], None, None, kp, vp)
