@@ -128,6 +128,8 @@ def library_path() -> str:
 def load_library(path: str | None = None):
     """Load libdattn.so (built in-tree by ``_build.build()``); raise if it is missing."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -159,12 +161,15 @@ def _ptr(t):
         raise ValueError("expected a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    """The launch stream's handle: the given stream's, else the current device's current one (by
+    the raw getter: building a Stream object costs about as much as the launch)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _bf16(t, name):
@@ -430,49 +435,52 @@ def _tokens(t, name):
     """A [tokens...][H][d] tensor whose heads are packed and whose tokens are evenly spaced (a
     contiguous tensor or a slice of a fused projection): (pointer, elements between tokens)."""
     size, step = t.shape, t.stride()
-    if len(size) not in (3, 4):
+    dims = len(size)
+    if dims != 3 and dims != 4:
         raise ValueError(f"{name} must be [tokens][heads][d] or [B][T][heads][d]")
-    if step[-1] != 1 or (size[-2] > 1 and step[-2] != size[-1]):
+    H, d = size[-2], size[-1]
+    if step[-1] != 1 or (H > 1 and step[-2] != d):
         raise ValueError(f"the heads of {name} must be packed")
-    stride = step[-3]
-    if len(size) == 4 and size[0] > 1:
-        if size[1] == 1:
-            stride = step[0]
-        elif step[0] != size[1] * stride:
+    if dims == 3:
+        many, stride = size[0] > 1, step[0]
+    else:
+        B, T = size[0], size[1]
+        many, stride = B > 1 or T > 1, step[0] if T == 1 else step[1]
+        if B > 1 and T > 1 and step[0] != T * stride:
             raise ValueError(f"the tokens of {name} must be evenly spaced")
-    if t.numel() == 0 or (len(size) == 3 and size[0] == 1) or \
-            (len(size) == 4 and size[0] == size[1] == 1):
-        stride = size[-2] * size[-1]  # no second token
-    if not t.is_cuda:
+    if t.get_device() < 0:
         raise ValueError("expected a CUDA tensor")
-    return ctypes.c_void_p(t.data_ptr()), stride
+    return t.data_ptr(), stride if many else H * d
 
 
 def _same_device(*tensors):
     """The launch goes to the current device: every tensor must live there."""
     here = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != here:
+        if t is not None and t.get_device() not in (here, -1):  # -1, the CPU: refused by _ptr
             raise ValueError(f"a tensor of {t.device} in a call on cuda:{here}")
 
 
 def dattn_rope(rotation: Rotation, x, out, positions, inverse: bool = False, stream=None):
     """Rotate x, bf16 or float32 [N][H][d] or [B][T][H][d], into out (same shape and type; may be
     x) at the int32 positions, one per token. inverse=True negates the angles: the gradient."""
-    if x.dtype not in (torch.bfloat16, torch.float32) or out.dtype != x.dtype:
+    dtype = x.dtype
+    f32 = dtype == torch.float32
+    if not (f32 or dtype == torch.bfloat16) or out.dtype != dtype:
         raise TypeError("x and out must both be bfloat16 or both float32")
-    if out.shape != x.shape:
+    size = x.shape
+    if out.shape != size:
         raise ValueError("out must have the shape of x")
     _i32(positions, "positions")
-    H, d = x.shape[-2:]
-    N = x.numel() // max(H * d, 1)
-    _size(positions, N, "positions")
-    _same_device(x, out, positions)
     xp, xs = _tokens(x, "x")
     op, os_ = _tokens(out, "out")
+    H, d = size[-2], size[-1]
+    N = size[0] if len(size) == 3 else size[0] * size[1]
+    _size(positions, N, "positions")
+    _same_device(x, out, positions)
     _check(load_library().dattn_rope(
-        ctypes.byref(rotation.c), xp, xs, op, os_, N, H, d, int(x.dtype == torch.float32),
-        _ptr(positions), int(bool(inverse)), _stream(stream)), "dattn_rope")
+        ctypes.byref(rotation.c), xp, xs, op, os_, N, H, d, f32, _ptr(positions), bool(inverse),
+        _stream(stream)), "dattn_rope")
 
 
 def dattn_rope_append(layout: KVLayout, k_pool, v_pool, stats, rotation: Rotation | None, q, k_new,
@@ -509,7 +517,7 @@ def dattn_rope_append(layout: KVLayout, k_pool, v_pool, stats, rotation: Rotatio
     _check(load_library().dattn_rope_append(
         ctypes.byref(layout.c), _ptr(k_pool), _ptr(v_pool), _ptr(stats),
         ctypes.byref(rotation.c) if rotation is not None else None, qp, qs, kp, ks, vp, vs, B, T,
-        Hq, _ptr(q_out), _ptr(seq_lens), _ptr(positions), _ptr(new_lens), int(bool(advance)),
+        Hq, _ptr(q_out), _ptr(seq_lens), _ptr(positions), _ptr(new_lens), bool(advance),
         _ptr(dev_err), _stream(stream)), "dattn_rope_append")
 
 

@@ -172,11 +172,6 @@ __device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&r)[32])
 }
 
 // Packed fp32 pairs (Blackwell's two-wide fp32 FMA and add)
-__device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
 // (r0, r1) = (x0, x1) * m + c, m and c packed pairs, each lane rounded once
 __device__ __forceinline__ void fma_f32x2(float x0, float x1, uint64_t m, uint64_t c, float& r0,
                                           float& r1) {

@@ -1,10 +1,11 @@
 """The rotation and the rotating append on the GPU.
 
 dattn_rope is compared with a 64-bit rotation whose angles are reduced exactly. Error of one
-result, in units of (|x_a| + |x_b|) A: the angle (2^-32 of a turn, its fp32 fraction in half turns
-off by at most 2^-25, pi times that in radians) under 1e-7, sincospi's value (1 ulp of at most 1,
-2^-23) under 1.2e-7, its product with A and the two products and the sum 2^-24 each, 2.4e-7: under
-2^-21 together. To that comes half a step of the result's type.
+result, in units of (|x_a| + |x_b|) A: the angle (2^-32 of a turn, its fp32 value
+of at most an eighth of a turn scaled to radians: 2^-24 of pi/4 three times) under 1.5e-7, the
+polynomials' roundings and omitted terms under 1e-7, the product with A and the two products and
+the sum 2^-24 each, 2.4e-7 and less: under 2^-21 = 4.8e-7 together, as the errors of a pair's sine
+and cosine meet |x_a| and |x_b| once each. To that comes half a step of the result's type.
 
 dattn_rope_append is compared bit for bit with dattn_rope followed by dattn_kv_append.
 """
