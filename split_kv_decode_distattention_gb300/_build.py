@@ -17,8 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdattn.so")
 SOURCES = ["abi.cu", "attention.cu", "kv_append.cu", "merge.cu", "page_select.cu",
-           "decode_static.cu", "prefill.cu", "rope.cu"]
-HEADERS = ["common.cuh", "internal.h"]
+           "decode_static.cu", "prefill.cu", "prefill_block.cu", "rope.cu"]
+HEADERS = ["common.cuh", "internal.h", "prefill.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-warn-spills"]

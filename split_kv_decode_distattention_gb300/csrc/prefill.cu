@@ -39,37 +39,11 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "prefill.cuh"
 
 namespace dattn {
 
 namespace {
-
-#define kPfNegInf (-__int_as_float(0x7f800000))
-
-constexpr int kPfBlock = 64;                       // query and key block, tokens
-constexpr int kPfTiles = kPfBlock / 16;            // tiles per key block
-
-struct PfParams {
-    int32_t num_pages, Hkv, P, max_pages;
-    const int32_t* block_table;
-    const uint16_t* q;
-    int32_t B, Tq, Hq, g;
-    float sl2;  // scale * log2(e)
-    const int32_t* seq_lens;
-    int32_t nqb;  // 128-row tiles per (request, head slot) a chunk can touch
-    // 1: a CTA's 128 rows are one 64-token query block of two query heads of one KV head
-    // (even g; both halves keep the same key blocks); 0: two query blocks of one query head
-    int32_t head_pairs;
-    int32_t kv_group;  // KV heads whose tiles run together (a divisor of Hkv)
-    // block sparsity (head_kind == nullptr: dense causal)
-    const int8_t* head_kind;
-    int32_t sink_blocks, local_blocks, max_sel, qblock_stride;
-    const int32_t* block_lists;
-    float* out;
-    float* m_out;
-    float* e_out;
-    int32_t* dev_err;
-};
 
 __device__ __forceinline__ uint64_t policy_evict_normal() {
     uint64_t pol;
@@ -90,152 +64,6 @@ constexpr int kTcVStages = 3;        // V blocks in flight
 constexpr int kTcMetaSlots = 4;      // per-block metadata slots (block j in slot j % 4)
 constexpr int kTcBars = 20;          // mbarriers of the pipeline
 constexpr uint32_t kTcCols = 256;    // TMEM: O [0, 128), S0 [128, 192), S1 [192, 256)
-constexpr float kTcRescale = 8.f;    // lazy rescale threshold (log2 units)
-
-__device__ __forceinline__ void tc_alloc(uint32_t dst_smem, uint32_t ncols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
-                 "r"(ncols)
-                 : "memory");
-}
-__device__ __forceinline__ void tc_relinquish() {
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tc_dealloc(uint32_t taddr, uint32_t ncols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
-                 : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-// D (TMEM) (+)= A (smem descriptor) * B (smem descriptor)
-__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                          uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// D (TMEM) (+)= A (TMEM) * B (smem descriptor)
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                          uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// Arrives once on the mbarrier when every tcgen05.mma issued so far by this thread is done.
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void tc_wait_ld() {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tc_wait_st() {
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-// 32 consecutive TMEM columns of this thread's lane (the warp's 32 lanes at once)
-__device__ __forceinline__ void tc_ld32(uint32_t taddr, float (&v)[32]) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-        "%28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-          "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-        "%28, %29, %30, %31, %32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-        "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-
-// Packed fp32 pairs (Blackwell's two-wide fp32 FMA and add)
-// (r0, r1) = (x0, x1) * m + c, m and c packed pairs, each lane rounded once
-__device__ __forceinline__ void fma_f32x2(float x0, float x1, uint64_t m, uint64_t c, float& r0,
-                                          float& r1) {
-    asm("{\n\t.reg .b64 a, d;\n\tmov.b64 a, {%2, %3};\n\tfma.rn.f32x2 d, a, %4, %5;\n\t"
-        "mov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(r0), "=f"(r1)
-        : "f"(x0), "f"(x1), "l"(m), "l"(c));
-}
-// (a0, a1) += (b0, b1)
-__device__ __forceinline__ void add_f32x2(float& a0, float& a1, float b0, float b1) {
-    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
-        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "+f"(a0), "+f"(a1)
-        : "f"(b0), "f"(b1));
-}
-// (r0, r1) = (a0, a1) - (b0, b1)
-__device__ __forceinline__ void sub_f32x2(float a0, float a1, float b0, float b1, float& r0,
-                                          float& r1) {
-    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "sub.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(r0), "=f"(r1)
-        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
-}
-// max(a, b, c) in one instruction
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-// maximum of 64 values over eight independent chains of three-input maxima
-__device__ __forceinline__ float row_max64(const float (&x)[64]) {
-    float m[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) m[k] = fmaxf(x[k], x[k + 8]);
-#pragma unroll
-    for (int i = 16; i < 64; i += 16) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) m[k] = fmax3(m[k], x[i + k], x[i + k + 8]);
-    }
-    return fmax3(fmax3(m[0], m[1], m[2]), fmax3(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
-}
-
-// Shared-memory matrix descriptor of a 128-byte-swizzled operand: start address, leading and
-// stride byte offsets (16-byte units), the descriptor version of this architecture (1 at bit
-// 46) and the 128-byte swizzle mode (2 at bits 61-63).
-__device__ __forceinline__ uint64_t tc_sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
-}
-// Instruction descriptor of kind::f16: fp32 accumulator, bf16 A and B, A K-major, B K-major
-// (b_mn = 0) or MN-major (b_mn = 1), shape M x N.
-__host__ __device__ constexpr uint32_t tc_idesc(uint32_t M, uint32_t N, uint32_t b_mn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
-}
-
-__device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-        "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15])
-        : "memory");
-}
 
 // Shared memory of the tcgen05 prefill (offsets from the dynamic shared base, which the kernel
 // checks to be 1024-byte aligned: no slack is reserved, so that two CTAs with three V stages
@@ -915,7 +743,10 @@ extern "C" dattn_status_t dattn_prefill(const dattn_kv_layout* layout, const voi
         return DATTN_ERR_UNSUPPORTED;
     if ((int64_t)layout->max_pages_per_req * layout->page_size >= (1ll << 30))
         return DATTN_ERR_UNSUPPORTED;
-    if (layout->kv_format != DATTN_KV_BF16) {
+    const bool block = layout->kv_format == DATTN_KV_FP8_BLOCK;
+    if (block && (!layout->kv_scale || !pf_aligned16(layout->kv_scale)))
+        return DATTN_ERR_INVALID_ARG;
+    if (layout->kv_format != DATTN_KV_BF16 && !block) {
         return layout->kv_format == DATTN_KV_FP8_E4M3 || layout->kv_format == DATTN_KV_INT4 ||
                        layout->kv_format == DATTN_KV_MIXED
                    ? DATTN_ERR_UNSUPPORTED
@@ -968,6 +799,8 @@ extern "C" dattn_status_t dattn_prefill(const dattn_kv_layout* layout, const voi
     const int64_t ctas = (int64_t)B * p.nqb * Hq;
     if (ctas >= (1ll << 31)) return DATTN_ERR_UNSUPPORTED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (block)
+        return launch_prefill_block(p, k_pool, v_pool, layout->kv_scale, layout->head_dim, s);
     return layout->head_dim == 64 ? launch_prefill_tc_d<64>(p, k_pool, v_pool, s)
                                   : launch_prefill_tc_d<128>(p, k_pool, v_pool, s);
 }

@@ -113,12 +113,13 @@ class BlockPool:
         return v.transpose(0, 2, 1, 3).reshape(n * self.P, *v.shape[1:2], v.shape[3])[:L]
 
 
-def attention(q, K, V, scale, see=None):
+def attention(q, K, V, scale, see=None, weights=2.0 ** -20):
     """float64 softmax attention of q [T][d] over K, V [L][d]; see [T][L] marks the visible keys.
     Returns out, m, e and an error bound of out for a computation whose logits are sums of d
-    exact products in fp32 (in any order: d * 2^-23 of the sum of magnitudes, and 2^-22 of the
-    logit for its scaling) and whose weights and their products have 2^-20 relative error: a
-    logit error t changes a weighted mean of values by at most 2 t max|v|."""
+    exact products in fp32 (in any order: d * 2^-23 of the sum of magnitudes, its scaling
+    included), whose weights have a relative error `weights`, and whose weighted sums take in 16
+    keys at a time in fp32 (2^-23 of the sum of magnitudes each time): a relative error t of the
+    weights changes a weighted mean of values by at most 2 t max|v|. Also returns t."""
     q, K, V = (np.asarray(t, np.float64) for t in (q, K, V))
     s = q @ K.T * scale
     if see is not None:
@@ -130,6 +131,7 @@ def attention(q, K, V, scale, see=None):
     mag = np.abs(q) @ np.abs(K).T * abs(scale)
     if see is not None:
         mag = np.where(see, mag, 0.0)
-    t = q.shape[1] * 2.0 ** -23 * mag.max(-1, initial=0.0) + 2.0 ** -20
+    t = q.shape[1] * 2.0 ** -23 * mag.max(-1, initial=0.0) + weights + (
+        K.shape[0] / 16 + 1) * 2.0 ** -23
     bound = 2.0 * t * (np.abs(V).max(initial=0.0))
     return out, m, e, bound, t

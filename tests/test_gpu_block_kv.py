@@ -152,7 +152,7 @@ def _filled(case, seed, stats=False, junk=True, steps=(1.0,)):
     return cache, kp, vp
 
 
-def _check(case, q, out, m, e, kp, vp, see_of=None):
+def _check(case, q, out, m, e, kp, vp, see_of=None, weights=2.0 ** -20):
     """q, out [B][T][Hq][d]; see_of(b, kvh) -> [T][L] visible keys (default: causal)."""
     B, T, Hq, d = q.shape
     q64, o = q.double().cpu().numpy(), out.double().cpu().numpy()
@@ -164,7 +164,8 @@ def _check(case, q, out, m, e, kp, vp, see_of=None):
         for h in range(Hq):
             kvh = h // case.g
             see = causal if see_of is None else see_of(b, kvh)
-            w, wm, we, tol, t = ref.attention(q64[b, :, h], K[:, kvh], V[:, kvh], case.scale, see)
+            w, wm, we, tol, t = ref.attention(q64[b, :, h], K[:, kvh], V[:, kvh], case.scale, see,
+                                                weights)
             err = np.abs(o[b, :, h] - w).max(-1)
             assert (err <= tol + 2.0 ** -23 * np.abs(w).max(-1, initial=0.0)).all(), (
                 b, h, L, err, tol)
@@ -320,3 +321,162 @@ def test_a_step_appends_with_rotation_and_decodes():
         assert cache.seq_lens.tolist() == lens and int(cache.dev_err.item()) == 0
         _assert_pool(cache, kp, vp)
         _check(case, qr, out[:, None], None, None, kp, vp)
+
+
+# ---------------------------------------------------------------- prefill
+
+# the weights enter the products as two bf16 terms: half a step of half a step, 2^-18, beside 2^-20
+PREFILL = 2.0 ** -18 + 2.0 ** -20
+
+
+def _prefill(cache, q, sparse=None, out=None):
+    B, Tq, Hq, d = q.shape
+    out = torch.full((B, Tq, Hq, d), float("nan"), device=DEV) if out is None else out
+    m, e = (torch.full((B, Tq, Hq), float("nan"), device=DEV) for _ in range(2))
+    dattn.dattn_prefill(cache.layout, cache.k_pool, cache.v_pool, q, cache.case.scale,
+                        cache.seq_lens, out, m, e, sparse=sparse, dev_err=cache.dev_err)
+    torch.cuda.synchronize()
+    return out, m, e
+
+
+PREFILL_CASES = [
+    # Hq, Hkv, d, P, lens, Tq
+    (4, 1, 128, 16, [64], 64),          # one query block of four heads
+    (4, 1, 64, 16, [1, 77, 300], 1),    # single tokens
+    (8, 2, 128, 64, [129, 70, 500], 70),
+    (2, 2, 128, 16, [300, 700], 280),   # one head: four query blocks, some past the chunk
+    (6, 3, 64, 48, [200, 131], 131),    # pairs of heads
+    (3, 1, 64, 256, [513], 200),
+    (8, 1, 128, 32, [100, 999], 33),
+    (5, 5, 64, 16, [64, 65], 2),
+]
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,P,lens,Tq", PREFILL_CASES)
+def test_causal_prefill_over_the_block_scaled_pool(Hq, Hkv, d, P, lens, Tq):
+    case = W.Case("pf", B=len(lens), Hq=Hq, Hkv=Hkv, d=d, P=P, lens=lens, seed=6)
+    cache, kp, vp = _filled(case, 21)
+    q = _rows((len(lens), Tq, Hq, d), 81)
+    out, m, e = _prefill(cache, q)
+    assert int(cache.dev_err.item()) == 0
+    _check(case, q, out, m, e, kp, vp, weights=PREFILL)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 4, 64), (12, 3, 128), (6, 3, 128), (3, 3, 128)])
+def test_block_sparse_prefill_over_the_block_scaled_pool(Hq, Hkv, d):
+    kinds = [W.HEAD_RETRIEVAL, W.HEAD_STREAMING, W.HEAD_DENSE, W.HEAD_RETRIEVAL][:Hkv]
+    lens, Tq = [900, 450], 333
+    case = W.Case("pfs", B=2, Hq=Hq, Hkv=Hkv, d=d, P=32, lens=lens, seed=6)
+    cache, kp, vp = _filled(case, 22)
+    stride, max_sel = 15, 9
+    rng = np.random.default_rng(3)
+    lists = np.full((2, Hkv, stride, max_sel), -1, np.int32)
+    for row in lists.reshape(-1, max_sel):
+        n = rng.integers(0, max_sel + 1)
+        row[:n] = rng.permutation(17)[:n]  # blocks after the query's too
+    lists[0, 0, 11] = -1  # queries that keep nothing
+    sp = dattn.PrefillSparseConfig(torch.tensor(kinds, dtype=torch.int8, device=DEV), 1, 2,
+                                   torch.from_numpy(lists).to(DEV))
+    q = _rows((2, Tq, Hq, d), 82)
+    out, m, e = _prefill(cache, q, sp)
+    assert int(cache.dev_err.item()) == 0
+
+    def see_of(b, kvh):
+        L = lens[b]
+        key, pos = np.arange(L)[None], (L - Tq + np.arange(Tq))[:, None]
+        kb, qb = key // 64, pos // 64
+        keep = key <= pos
+        if kinds[kvh] == W.HEAD_STREAMING:
+            return keep & ((kb < 1) | (kb > qb - 2))
+        if kinds[kvh] == W.HEAD_RETRIEVAL:
+            held = (lists[b, kvh][:, :, None] == np.arange(17)).any(1)
+            return keep & held[qb, kb]
+        return keep
+
+    _check(case, q, out, m, e, kp, vp, see_of, weights=PREFILL)
+
+
+def test_prefill_with_scales_of_every_size():
+    """Blocks whose scales span 2^-100 .. 2^100 (above and below what one bf16 factor reaches)."""
+    d, n = 128, 16
+    case = W.Case("pfr", B=1, Hq=4, Hkv=1, d=d, P=16, lens=[16 * n], seed=2)
+    cache, (kp, vp) = _cache(case, junk=True), _pools(case, junk=True)
+    k, v = _rows((1, 16 * n, 1, d), 1), _rows((1, 16 * n, 1, d), 2)
+    for i, x in enumerate([0, -100, 30, 3, -40, 100, 99, 0, -126, 60, 100, -3, 15, 16, 17, 8]):
+        v[:, 16 * i:16 * i + 16] *= 2.0 ** x
+        k[:, 16 * i:16 * i + 16] *= 2.0 ** (-x if x > 40 else min(x, 0))
+    k[:, 32:48] = 0
+    cache.append(k, v)
+    kp.append(case.block_table[0], 0, k[0].double().cpu().numpy())
+    vp.append(case.block_table[0], 0, v[0].double().cpu().numpy())
+    q = _rows((1, 70, 4, d), 3)
+    out, m, e = _prefill(cache, q)
+    assert int(cache.dev_err.item()) == 0
+    _check(case, q, out, m, e, kp, vp, weights=PREFILL)
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 3.0])
+def test_prefill_with_other_softmax_scales(scale):
+    case = W.Case("pfn", B=1, Hq=2, Hkv=1, d=64, P=16, lens=[190], seed=6, scale=scale or 1.0)
+    case.scale = scale
+    cache, kp, vp = _filled(case, 23)
+    q = _rows((1, 100, 2, 64), 83)
+    out, m, e = _prefill(cache, q)
+    _check(case, q, out, m, e, kp, vp, weights=PREFILL)
+
+
+def test_prefill_flags_bad_pages_and_lengths():
+    """An unmapped page adds nothing, a length below Tq leaves its request's outputs alone."""
+    case = W.Case("pfb", B=3, Hq=4, Hkv=1, d=64, P=16, lens=[200, 200, 90], seed=6)
+    cache, kp, vp = _filled(case, 24)
+    q = _rows((3, 100, 4, 64), 84)
+    want, _, _ = _prefill(cache, q[:2].contiguous())
+    lay = cache.layout
+    cache.block_table[0, 2] = -1
+    cache.block_table[0, 5] = case.num_pages + 3
+    out = torch.full((3, 100, 4, 64), 9.0, device=DEV)
+    _prefill(cache, q, out=out)
+    E = dattn.DEVERR
+    assert int(cache.dev_err.item()) == E["UNMAPPED_PAGE"] | E["PAGE_OOB"] | E["LEN_OOB"]
+    assert (out[2] == 9.0).all()
+    assert torch.equal(out[1], want[1])
+    hole = np.isin(np.arange(200) // 16, [2, 5])
+    case.lens = case.lens[:1]
+
+    def see_of(b, kvh):
+        return (np.arange(200)[None] <= (100 + np.arange(100))[:, None]) & ~hole[None]
+
+    _check(case, q[:1], out[:1], None, None, kp, vp, see_of, weights=PREFILL)
+
+
+def test_prefill_agrees_with_decode_and_repeats():
+    """Tq = 1 over a long context is a decode; the same call gives the same bits again, after
+    another context's call and in a captured graph."""
+    case = W.Case("pfd", B=2, Hq=16, Hkv=4, d=128, P=16, lens=[5000, 2222], seed=6)
+    cache, kp, vp = _filled(case, 25)
+    q = _rows((2, 1, 16, 128), 85)
+    out, m, e = _prefill(cache, q)
+    _check(case, q, out, m, e, kp, vp, weights=PREFILL)
+    dec = torch.empty(2, 16, 128, device=DEV)
+    cache.decode(q[:, 0].contiguous(), dec, cache.workspace())
+    torch.cuda.synchronize()
+    _check(case, q, dec[:, None], None, None, kp, vp)
+    g = torch.cuda.CUDAGraph()
+    again = torch.empty_like(out)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        dattn.dattn_prefill(cache.layout, cache.k_pool, cache.v_pool, q, case.scale,
+                            cache.seq_lens, again, dev_err=cache.dev_err)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(again, out)
+    assert int(cache.dev_err.item()) == 0
+
+
+def test_other_quantized_pools_still_have_no_prefill():
+    case = W.Case("no", B=1, Hq=2, Hkv=2, d=64, P=16, lens=[20], seed=6)
+    for fmt in (dattn.KV_FP8_E4M3, dattn.KV_INT4):
+        c = PagedCache(case, DEV, kv_format=fmt, zero_pool=True)
+        q = _rows((1, 4, 2, 64), 86)
+        with pytest.raises(dattn.DattnError, match="UNSUPPORTED"):
+            _prefill(c, q)
