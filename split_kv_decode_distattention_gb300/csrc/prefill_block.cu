@@ -2,30 +2,36 @@
 // new query tokens per request attends the paged cache, causally or block-sparsely, exactly as over
 // the bf16 pool (prefill.cu holds the method's sources and the block rules).
 //
-// A block scale is a power of two, so a stored value, code * scale, is a bf16 number: the codes
-// are widened to bf16 in shared memory, scale included, and the products and the softmax see
-// exactly the pool's values.
+// Arithmetic. An E4M3 code is an fp16 number, so the codes are widened to fp16 in shared memory
+// (one conversion for two codes) and both products run in fp16 with fp32 accumulation. The query
+// row is scaled by a power of two 2^a that brings its largest element to [2^14, 2^15) and rounded
+// to fp16: exact for every element within 2^28 of the largest. The K scale of a 16-key tile
+// multiplies its scores; the V scale, a power of two, goes into the exponent of its weights,
+// w = 2^(s - m + log2(scale / r)), where 2^r is a power of two that the scales seen so far exceed
+// by 2^7 at most (raised, and the accumulators rescaled, when a larger one comes), so that w stays
+// below 2^15. w enters the product as two fp16 terms, 22 bits together.
+// The tensor cores add into their fp32 accumulators rounding towards zero, which over a long
+// context shrinks the result (5.6e-5 after 4096 products of a 32K context), so a row's accumulator is
+// emptied into its output row every kPbWindow key blocks, by fp32 additions.
 //
 // What bounds it: the tensor cores. A 64-key block of 128 query rows takes one product S = Q K^T
-// and two products O += P V (P as two bf16 terms, hi rounded to nearest and lo the rounded rest, so
-// the weights keep 17 bits; one term alone would leave 2^-9 in a result that is fp32), 3 x 2 x 128
-// x 64 x d operations for the 2 x 2 x 128 x 64 x d that count: 2/3 of the dense bf16 rate at most.
-// The widening costs five integer and bf16 instructions for two codes, so a key block is widened
-// once for 256 query rows: one CTA per SM holds two tiles of 128 rows, and while one tile is in its
-// softmax the tensor cores work on the other.
+// and two products O += P V, 3 x 2 x 128 x 64 x d operations for the 2 x 2 x 128 x 64 x d that count:
+// 2/3 of the dense 16-bit rate at most. A key block is widened once for 256 query rows: one CTA per
+// SM holds two tiles of 128 rows, and while one tile is in its softmax the tensor cores work on the
+// other.
 //
 // A CTA: 256 rows as four quarters of 64 tokens: one query block of four heads of a KV head (g a
 // multiple of 4), two query blocks of two heads (even g), or four query blocks of one head. A tile
-// (two quarters) takes part in a key block only if one of its quarters keeps it. Warps 0-3 and 4-7
-// hold one query row per thread (softmax, as in prefill.cu), warps 8-11 load codes, widen them and
-// write K and V stages in the 128-byte-swizzled layout of the MMA operands, one thread of warp 12
-// issues the products: S of the next key block for both tiles, then P V of this one.
+// (two quarters) takes part in a key block only if one of its quarters keeps it. Where the last
+// wave of CTAs would fill less than half of the SMs, its tiles get a CTA each. 14 warps:
+//   0-3, 4-7  one query row per thread of tile 0, 1: the softmax;
+//   8-11      load codes, widen them and write the K and V stages in the 128-byte-swizzled layout
+//             of the MMA operands;
+//   12        one thread issues the products: S of the next key block for both tiles, then P V of
+//             this one;
+//   13        walks the key blocks, eight at a time, one lane per 16-key tile, and leaves each
+//             block's place, lengths and scales in a ring in shared memory for the others.
 // Tensor memory: O of the two tiles, then two score buffers for each, all 512 columns.
-//
-// The key blocks of a CTA can be cut over a cluster of 2, 4 or 8 CTAs (launch_prefill_block chooses:
-// few tiles, or a last wave that would be nearly empty). Each leaves its rows' O, maximum and sum
-// in its shared memory, and each merges a part of the rows from all of them through distributed
-// shared memory, with dattn_merge's equations: no workspace.
 #include <mutex>
 
 #include "common.cuh"
@@ -40,19 +46,30 @@ constexpr int kPbRows = 256;                // query rows of a CTA: two tiles of
 constexpr int kPbConvWarp = 8;              // warps 8-11 widen the codes
 constexpr int kPbConvThreads = 128;
 constexpr int kPbMmaWarp = 12;
-constexpr int kPbThreads = 13 * 32;
+constexpr int kPbPlaceWarp = 13;            // the places of the key blocks
+constexpr int kPbThreads = 14 * 32;
 constexpr int kPbStages = 3;                // K stages, and V stages
-constexpr int kPbMetaSlots = 8;             // tile lengths of block i in slot i % 8
+constexpr int kPbGroup = 8;                 // key blocks that warp 13 resolves at once
+constexpr int kPbRing = 2 * kPbGroup;       // the blocks' ring
+constexpr int kPbWindow = 32;               // key blocks between two emptyings of an accumulator
 constexpr uint32_t kPbCols = 512;           // O: [0, 128), [128, 256); S: 256 + 128 tile + 64 buffer
 
 // mbarriers
 constexpr int kBarKFull = 0, kBarKEmpty = 3, kBarVFull = 6, kBarVEmpty = 9;
 constexpr int kBarS = 12, kBarP = 16;       // + 2 tile + buffer
 constexpr int kBarPv = 20;                  // + tile
-constexpr int kBarMeta = 22, kBarDrain = 30, kPbBars = 31;
+constexpr int kBarRingFull = 22, kBarRingEmpty = 24, kBarDrain = 26, kPbBars = 27;
+constexpr int kRingReaders = 13;            // warps 0-12
+
+// A key block in the ring: its 16-key tiles (first row over all heads, tokens, K scale, log2 of the
+// V scale over 2^r), its index, the tiles of rows that keep it (bits) and r.
+struct PbBlock {
+    int4 tile[kPfTiles];
+    int32_t kb, act, r, pad;
+};
 
 struct PbSmem {
-    uint32_t q, blk_bytes, kst, vst, bm, bars, meta, taddr, abort, mrow, trow, lrow, total;
+    uint32_t q, blk_bytes, kst, vst, bm, ring, bars, taddr, abort, qscale, total;
 };
 
 __host__ __device__ inline PbSmem pb_smem_layout(int D, int nq, int nwords) {
@@ -62,118 +79,109 @@ __host__ __device__ inline PbSmem pb_smem_layout(int D, int nq, int nwords) {
     s.blk_bytes = 64u * D * 2u;
     s.kst = o;         o += kPbStages * s.blk_bytes;
     s.vst = o;         o += kPbStages * s.blk_bytes;
-    s.bm = o;          o += (uint32_t)(nq * nwords) * 4u;
-    o = (o + 15u) & ~15u;
+    s.ring = o;        o += kPbRing * (uint32_t)sizeof(PbBlock);
     s.bars = o;        o += (kPbBars + 1) * 8u;
-    s.meta = o;        o += kPbMetaSlots * 16u;
     s.taddr = o;       o += 16u;
     s.abort = o;       o += 16u;
-    s.mrow = o;        o += kPbRows * 4u;  // a split's row references, maxima and sums
-    s.trow = o;        o += kPbRows * 4u;
-    s.lrow = o;        o += kPbRows * 4u;
+    s.qscale = o;      o += kPbRows * 4u;
+    s.bm = o;          o += (uint32_t)(nq * nwords) * 4u;
     s.total = o;
     return s;
 }
 
 struct PbParams {
     PfParams f;
-    int32_t hp, nq;  // heads and query blocks of a CTA: hp * nq = 4
-    int32_t split;   // CTAs of a cluster that share a CTA's key blocks
+    int32_t hp, nq;    // heads and query blocks of a CTA: hp * nq = 4
+    int32_t whole;     // CTAs of two tiles; the others hold one tile each
     const uint8_t* k_pool;
     const uint8_t* v_pool;
     const float2* scale;  // [num_pages][Hkv][P/16] (K, V)
 };
 
-// The key blocks that the two tiles keep: the bitmaps of the CTA's query blocks are bm[i][nwords].
+// The key blocks of words w that the two tiles keep: the bitmaps of the CTA's query blocks are
+// bm[i][nwords]; tmask: the tiles that the CTA holds.
 __device__ __forceinline__ uint32_t tile_word(const uint32_t* bm, int nq, int nwords, int t, int w) {
     if (nq == 1) return bm[w];
     if (nq == 2) return bm[t * nwords + w];
     return bm[2 * t * nwords + w] | bm[(2 * t + 1) * nwords + w];
 }
-
-// The walk over the key blocks that any tile keeps, in order, from the skip'th on.
-struct Walk {
-    const uint32_t* bm;
-    int nq, nwords, nw, w;
-    uint32_t w0, w1, word;
-    __device__ __forceinline__ void fetch() {
-        w0 = w1 = 0u;
-        if (w < nw) {
-            w0 = tile_word(bm, nq, nwords, 0, w);
-            w1 = tile_word(bm, nq, nwords, 1, w);
-        }
-        word = w0 | w1;
-    }
-    __device__ __forceinline__ Walk(const uint32_t* bm_, int nq_, int nwords_, int nw_, int skip)
-        : bm(bm_), nq(nq_), nwords(nwords_), nw(nw_), w(0) {
-        fetch();
-        while (w < nw && __popc(word) <= skip) {
-            skip -= __popc(word);
-            ++w;
-            fetch();
-        }
-        for (; skip > 0; --skip) word &= word - 1u;
-    }
-    // The next key block and which tiles keep it (bit t); the caller counts the blocks.
-    __device__ __forceinline__ void next(int32_t& kb, uint32_t& act) {
-        while (word == 0u && w < nw) {
-            ++w;
-            fetch();
-        }
-        const int bit = __ffs(word) - 1;
-        kb = 32 * w + bit;
-        act = ((w0 >> bit) & 1u) | (((w1 >> bit) & 1u) << 1);
-        word &= word - 1u;
-    }
-};
-
-// Two E4M3 codes (the bytes at 16-bit places 0 and 1 of y's upper bytes) as bf16: sign, exponent and
-// mantissa moved into place make code * 2^-120 (subnormal codes too, as subnormal bf16 numbers),
-// and m = 2^120 * scale restores them exactly. A NaN code becomes 480 * scale.
-__device__ __forceinline__ uint32_t widen2(uint32_t y, __nv_bfloat162 m) {
-    const uint32_t v = (y & 0x80008000u) | ((y >> 4) & 0x07f007f0u);
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v), m);
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b, __nv_bfloat162 m) {
-    return make_uint4(widen2(__byte_perm(a, 0u, 0x1404), m), widen2(__byte_perm(a, 0u, 0x3424), m),
-                      widen2(__byte_perm(b, 0u, 0x1404), m), widen2(__byte_perm(b, 0u, 0x3424), m));
+__device__ __forceinline__ uint32_t held_word(const uint32_t* bm, int nq, int nwords, uint32_t tmask,
+                                              int w, uint32_t& w0, uint32_t& w1) {
+    w0 = (tmask & 1u) ? tile_word(bm, nq, nwords, 0, w) : 0u;
+    w1 = (tmask & 2u) ? tile_word(bm, nq, nwords, 1, w) : 0u;
+    return w0 | w1;
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
+// Matrix descriptors as their lower words: the upper word (stride 1024 bytes, the descriptor version
+// and the 128-byte swizzle, see tc_sdesc) is the same for every operand here, and a step along an
+// operand adds its bytes / 16 to the lower word.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+    return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);
+}
+// The products are predicated on the issuing lane instead of branched around: the code around them
+// stays convergent, so that their operands can live in uniform registers, where tcgen05.mma takes
+// them from.
+template <bool ACC>
+__device__ __forceinline__ void pb_mma_ss(uint32_t lead, uint32_t d_tmem, uint32_t a_lo,
+                                          uint32_t b_lo, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "setp.ne.b32 q, %6, 0;\n\tmov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(kDescHi), "n"(ACC ? 1 : 0), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void pb_mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem,
+                                          uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "setp.ne.b32 q, %6, 0;\n\tmov.b64 b, {%2, %4};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "n"(kDescHi), "r"(acc), "r"(lead)
+        : "memory");
+}
+// tc_commit by the issuing lane
+__device__ __forceinline__ void pb_commit(uint32_t lead, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            bar),
+        "r"(lead)
+        : "memory");
+}
+// 1 in one lane of the (convergent) warp
+__device__ __forceinline__ uint32_t elect_lane() {
     uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+// kind::f16 with fp16 operands (tc_idesc's type fields cleared) and an fp32 accumulator
+__host__ __device__ constexpr uint32_t pb_idesc(uint32_t M, uint32_t N, uint32_t b_mn) {
+    return tc_idesc(M, N, b_mn) & ~((7u << 7) | (7u << 10));
 }
-__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
+
+// out[0..3] += v, at L2; the row belongs to this thread alone
+__device__ __forceinline__ void red_add4(float* out, float a, float b, float c, float d) {
+    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(out), "f"(a), "f"(b), "f"(c),
+                 "f"(d)
                  : "memory");
-    return v;
 }
+
+__device__ __forceinline__ float max16(const float* x) {
+    const float a = fmax3(x[0], x[1], x[2]), b = fmax3(x[3], x[4], x[5]);
+    const float c = fmax3(x[6], x[7], x[8]), d = fmax3(x[9], x[10], x[11]);
+    const float e = fmax3(x[12], x[13], x[14]);
+    return fmaxf(fmax3(a, b, x[15]), fmax3(c, d, e));
+}
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) << 23); }
 
 template <int D>
 __global__ void __launch_bounds__(kPbThreads, 1)
 prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
-    constexpr int KH = D / 64;  // 128-byte halves of a bf16 row
-    constexpr uint32_t kHalf = 64u * 128u;
+    constexpr uint32_t kHalf = 64u * 128u;  // a 128-byte half of a key block's rows
     const PfParams& p = pp.f;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = smem_raw;
@@ -184,12 +192,14 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
         if (tid == 0) set_err(p.dev_err, DATTN_DEVERR_SMEM_ALIGN);
         return;
     }
-    // CTA -> (request b, group of kv_group KV heads, tile J, KV head of the group, head slot, rank
-    // of its cluster): a group's tiles run together, its last (longest) first
+    // CTA -> (request b, group of kv_group KV heads, tile pair J, KV head of the group, head slot):
+    // a group's pairs run together, its last (longest) first. CTAs from `whole` on hold one tile.
     const int hp = pp.hp, nq = pp.nq;
     const int32_t spk = p.g / hp;
     const int32_t ngrp = p.Hkv / p.kv_group;
-    int32_t c = blockIdx.x / pp.split;
+    const int32_t extra = max((int32_t)blockIdx.x - pp.whole, 0);
+    const uint32_t tmask = (int32_t)blockIdx.x < pp.whole ? 3u : 1u << (extra & 1);
+    int32_t c = (int32_t)blockIdx.x < pp.whole ? (int32_t)blockIdx.x : pp.whole + (extra >> 1);
     const int32_t sk = c % spk;
     c /= spk;
     const int32_t hg = c % p.kv_group;
@@ -201,8 +211,9 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
     const int32_t h0 = kvh * p.g + sk * hp;  // the CTA's first query head
     const uint32_t bars = smem_u32(base + L.bars);
     auto bar = [&](int i) { return bars + 8u * i; };
-    int32_t* meta = reinterpret_cast<int32_t*>(base + L.meta);
+    PbBlock* ring = reinterpret_cast<PbBlock*>(base + L.ring);
     uint32_t* bm = reinterpret_cast<uint32_t*>(base + L.bm);
+    float* qscale = reinterpret_cast<float*>(base + L.qscale);
     volatile int* abort_p = reinterpret_cast<volatile int*>(base + L.abort);
     if (tid == 0) {
         for (int s = 0; s < kPbStages; ++s) {
@@ -215,9 +226,11 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
             mbar_init(bar(kBarS + i), 1);
             mbar_init(bar(kBarP + i), 128);
         }
-        mbar_init(bar(kBarPv), 1);
-        mbar_init(bar(kBarPv + 1), 1);
-        for (int i = 0; i < kPbMetaSlots; ++i) mbar_init(bar(kBarMeta + i), D == 128 ? 1 : 2);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kBarPv + i), 1);
+            mbar_init(bar(kBarRingFull + i), 1);
+            mbar_init(bar(kBarRingEmpty + i), kRingReaders);
+        }
         mbar_init(bar(kBarDrain), 1);
         *abort_p = 0;
         fence_mbar_init();
@@ -233,7 +246,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
     tc_fence_after();
     const uint32_t tbase = *reinterpret_cast<volatile uint32_t*>(base + L.taddr);
 
-    // ---- the CTA's query rows and key blocks (uniform over the cluster) -----------------------
+    // ---- the CTA's query rows and key blocks (uniform over the CTA) ---------------------------
     const int32_t Ln = p.seq_lens[b];
     bool active = Ln >= p.Tq && Ln <= p.max_pages * p.P;
     if (!active && tid == 0 && h0 == 0 && J == 0) set_err(p.dev_err, DATTN_DEVERR_LEN_OOB);
@@ -285,267 +298,351 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                 }
             }
         }
-        // the query rows, [half][256 rows][128 B] swizzled; with a negative scale they are negated
-        // (exact), so that the scores scale by |scale|
+        // The query rows as fp16, [half][256 rows][128 B] swizzled, each scaled by its 2^a; with a
+        // negative scale they are negated (exact), so that the scores scale by |scale|. A row's
+        // D/8 threads are neighbours, and the loop's last round is whole warps.
+        constexpr int TPR = D / 8;
         const uint32_t qneg = p.sl2 < 0.f ? 0x80008000u : 0u;
-        for (int idx = tid; idx < kPbRows * (D / 8); idx += kPbThreads) {
-            const int r = idx / (D / 8), ch = idx - r * (D / 8), z = r >> 6;
+        for (int idx = tid; idx < kPbRows * TPR; idx += kPbThreads) {
+            const int r = idx / TPR, ch = idx - r * TPR, z = r >> 6;
             const int32_t pos = (qa + q_block(z)) * kPfBlock + (r & 63);
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (((has >> q_block(z)) & 1u) && pos >= c0 && pos < Ln) {
+            if (((has >> q_block(z)) & 1u) && pos >= c0 && pos < Ln)
                 v = __ldg(reinterpret_cast<const uint4*>(
                     p.q + (((int64_t)b * p.Tq + (pos - c0)) * p.Hq + h0 + q_head(z)) * D) + ch);
-                v = make_uint4(v.x ^ qneg, v.y ^ qneg, v.z ^ qneg, v.w ^ qneg);
-            }
+            float mx = absmax8(v);
+#pragma unroll
+            for (int off = 1; off < TPR; off <<= 1)
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            int a = 0;
+            if (mx > 0.f) a = min(127, max(-113, 14 - ((__float_as_int(mx) >> 23) - 127)));
+            const float up = __int_as_float((127 + a) << 23);
+            uint32_t w[4] = {v.x ^ qneg, v.y ^ qneg, v.z ^ qneg, v.w ^ qneg};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = pack_f16(bf16_lo(w[i]) * up, bf16_hi(w[i]) * up);
             *reinterpret_cast<uint4*>(base + L.q + (ch >> 3) * (kPbRows * 128u) +
-                                      swz128((uint32_t)r, (uint32_t)(ch & 7))) = v;
+                                      swz128((uint32_t)r, (uint32_t)(ch & 7))) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+            // 2^-a |scale| log2(e)
+            if (ch == 0)
+                qscale[r] = fabsf(p.sl2) *
+                            (a < 127 ? __int_as_float((127 - a) << 23) : 5.877471754e-39f);
         }
         fence_proxy_async_smem();  // the tensor cores read these rows through the async proxy
     }
     __syncthreads();
-    // This CTA's share of the key blocks that some row keeps: n blocks from the i0'th on.
-    int32_t nall = 0;
-    for (int32_t w = 0; w < nw; ++w)
-        nall += __popc(tile_word(bm, nq, nwords, 0, w) | tile_word(bm, nq, nwords, 1, w));
-    const int32_t rank = pp.split > 1 ? (int32_t)cluster_rank() : 0;
-    const int32_t i0 = (int32_t)((int64_t)nall * rank / pp.split);
-    const int32_t n = (int32_t)((int64_t)nall * (rank + 1) / pp.split) - i0;
+    int32_t n = 0;  // key blocks that some row of the CTA keeps
+    for (int32_t w = 0; w < nw; ++w) {
+        uint32_t w0, w1;
+        n += __popc(held_word(bm, nq, nwords, tmask, w, w0, w1));
+    }
+    // The ring: block i in slot i % 16, ready with its group of eight; a reader's warp gives a group
+    // back after its last block.
+    auto wait = [&](uint32_t bar_addr, uint32_t parity) {  // by a whole warp, one answer
+        return __all_sync(0xffffffffu, mbar_wait(bar_addr, parity, abort_p, p.dev_err)) != 0;
+    };
+    auto ring_ready = [&](int32_t i) {
+        return (i & (kPbGroup - 1)) != 0 ||
+               wait(bar(kBarRingFull) + 8u * ((i / kPbGroup) & 1), (i / kPbRing) & 1);
+    };
+    auto ring_release = [&](int32_t i) {
+        __syncwarp();
+        if ((i & (kPbGroup - 1)) == kPbGroup - 1 && lane == 0)
+            mbar_arrive(bar(kBarRingEmpty) + 8u * ((i / kPbGroup) & 1));
+    };
 
-    if (active && warp >= kPbConvWarp && warp < kPbMmaWarp) {
+    if (active && warp == kPbPlaceWarp) {
+        // ---------------------------------------------------------------- places of the key blocks
+        const int blk = lane >> 2, u = lane & 3;  // this lane: tile u of the group's block blk
+        int32_t w = 0;
+        uint32_t w0 = 0u, w1 = 0u, word = held_word(bm, nq, nwords, tmask, 0, w0, w1);
+        int r = -126;
+        bool ok = true;
+        for (int32_t i = 0; i < n && ok; i += kPbGroup) {
+            const int32_t cnt = min(kPbGroup, n - i);
+            int32_t kb = 0, act = 0;
+            for (int x = 0; x < cnt; ++x) {
+                while (word == 0u && w + 1 < nw) word = held_word(bm, nq, nwords, tmask, ++w, w0, w1);
+                const int bit = __ffs(word) - 1;
+                if (x == blk) {
+                    kb = 32 * w + bit;
+                    act = ((w0 >> bit) & 1u) | (((w1 >> bit) & 1u) << 1);
+                }
+                word &= word - 1u;
+            }
+            const int32_t t0 = kb * kPfBlock + 16 * u;
+            int32_t y = 0, hi = 0;
+            float2 sc = make_float2(0.f, 0.f);
+            if (blk < cnt && t0 < p_hi) {
+                const int32_t lp = t0 / p.P;
+                const int32_t page = __ldg(p.block_table + (int64_t)b * p.max_pages + lp);
+                if (page < 0) {
+                    set_err(p.dev_err, DATTN_DEVERR_UNMAPPED_PAGE);
+                } else if (page >= p.num_pages) {
+                    set_err(p.dev_err, DATTN_DEVERR_PAGE_OOB);
+                } else {
+                    y = (page * p.Hkv + kvh) * p.P + (t0 - lp * p.P);
+                    hi = min(16, Ln - t0);
+                    sc = __ldg(pp.scale + (y >> 4));
+                }
+            }
+            // 2^r: what the V scales up to each block exceed by 2^7 at most
+            const int ve = sc.y > 0.f ? (__float_as_int(sc.y) >> 23) - 127 : -1000;
+            int vm = max(ve, __shfl_xor_sync(0xffffffffu, ve, 1));
+            vm = max(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
+            int mine = r;
+            for (int x = 0; x < kPbGroup; ++x) {
+                const int v = __shfl_sync(0xffffffffu, vm, 4 * x);
+                if (v > r + 7) r = v;
+                if (x == blk) mine = r;
+            }
+            // (far below 2^r a scale counts as 2^(r - 64): nothing beside the others; codes with
+            // scale 0 are zeros)
+            const int lv = sc.y > 0.f ? max(ve - mine, -64) : 0;
+            if (i >= kPbRing)
+                ok = wait(bar(kBarRingEmpty) + 8u * ((i / kPbGroup) & 1), ((i / kPbRing) - 1) & 1);
+            if (ok && blk < cnt) {
+                PbBlock& to = ring[(i + blk) & (kPbRing - 1)];
+                to.tile[u] = make_int4(y, hi, __float_as_int(sc.x), lv);
+                if (u == 0) {
+                    to.kb = kb;
+                    to.act = act;
+                    to.r = mine;
+                }
+            }
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(bar(kBarRingFull) + 8u * ((i / kPbGroup) & 1));
+        }
+    } else if (active && warp >= kPbConvWarp && warp < kPbMmaWarp) {
         // ------------------------------------------------------ widening: codes -> K and V stages
         // A row of D codes is D/16 threads of 16 codes; a pass takes RP rows, NP passes a block.
+        // Eight neighbours store to two rows of one half: all banks.
         constexpr int CPR = D / 16, RP = kPbConvThreads / CPR, NP = 64 / RP;
-        const int ct = tid - kPbConvWarp * 32, c16 = ct % CPR, rr = ct / CPR;
-        const bool teller = (ct & 63) == 0 && (D == 64 || ct == 0);  // publishes its tiles' lengths
-        // the upper row half's threads write their two 16-byte chunks in the other order, so that
-        // eight neighbours hit all banks
-        const bool odd = D == 128 && c16 >= 4;
-        Walk walk(bm, nq, nwords, nw, i0);
-        auto first_row = [&](int k) { return rr + RP * k; };
-        // the pages of this thread's tiles in key block kb, one block ahead of its codes
-        auto read_pages = [&](int32_t kb, int32_t (&pg)[NP]) {
+        const int ct = tid - kPbConvWarp * 32;
+        const int c16 = D == 64 ? ct & 3 : (ct & 3) | ((ct >> 1) & 4);
+        const int rr = D == 64 ? ct >> 2 : ((ct >> 2) & 1) | ((ct >> 4) << 1);
+        uint4 kv[NP], vv[NP];
+        int32_t y[NP], hi[NP];  // the next block's tiles
+        auto place = [&](int32_t i) {
+            const PbBlock& blk = ring[i & (kPbRing - 1)];
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
-                const int32_t t0 = kb * kPfBlock + (first_row(k) & ~15);
-                pg[k] = t0 < p_hi ? __ldg(p.block_table + (int64_t)b * p.max_pages + t0 / p.P) : 0;
-            }
-        };
-        int32_t y[NP], hi[NP];  // the tile's first row over all heads (below 2^31), its tokens
-        auto resolve = [&](int32_t kb, const int32_t (&pg)[NP]) {
-#pragma unroll
-            for (int k = 0; k < NP; ++k) {
-                const int32_t t0 = kb * kPfBlock + (first_row(k) & ~15);
-                y[k] = hi[k] = 0;
-                if (t0 >= p_hi) continue;
-                if (pg[k] < 0 || pg[k] >= p.num_pages) {
-                    if (teller)
-                        set_err(p.dev_err, pg[k] < 0 ? DATTN_DEVERR_UNMAPPED_PAGE
-                                                     : DATTN_DEVERR_PAGE_OOB);
-                    continue;
-                }
-                y[k] = (pg[k] * p.Hkv + kvh) * p.P + (t0 - (t0 / p.P) * p.P);
-                hi[k] = min(16, Ln - t0);
+                const int4 t = blk.tile[(rr + RP * k) >> 4];
+                y[k] = t.x;
+                hi[k] = t.y;
             }
         };
         // 16 codes a row; rows that hold no token of the request are zeros
         auto load = [&](const uint8_t* pool, uint4 (&v)[NP]) {
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
-                const int r = first_row(k) & 15;
+                const int r = (rr + RP * k) & 15;
                 v[k] = make_uint4(0u, 0u, 0u, 0u);
                 if (r < hi[k])
-                    v[k] = __ldg(reinterpret_cast<const uint4*>(pool + (int64_t)(y[k] + r) * D + 16 * c16));
+                    v[k] = __ldg(reinterpret_cast<const uint4*>(pool + (int64_t)(y[k] + r) * D +
+                                                                16 * c16));
             }
         };
-        auto load_scales = [&](float (&ks)[NP], float (&vs)[NP]) {
+        const uint32_t half = (c16 >> 2) * kHalf, ch = 2u * (c16 & 3);
+        auto store = [&](uint8_t* st, const uint4 (&v)[NP]) {
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
-                const float2 s = hi[k] > 0 ? __ldg(pp.scale + (y[k] >> 4)) : make_float2(0.f, 0.f);
-                ks[k] = s.x;
-                vs[k] = s.y;
+                const uint32_t row = (uint32_t)(rr + RP * k);
+                uint4 a, c2;
+                e4m3x4_to_f16(v[k].x, a.x, a.y);
+                e4m3x4_to_f16(v[k].y, a.z, a.w);
+                e4m3x4_to_f16(v[k].z, c2.x, c2.y);
+                e4m3x4_to_f16(v[k].w, c2.z, c2.w);
+                *reinterpret_cast<uint4*>(st + half + swz128(row, ch)) = a;
+                *reinterpret_cast<uint4*>(st + half + swz128(row, ch + 1u)) = c2;
             }
         };
-        auto store = [&](uint8_t* st, const uint4 (&v)[NP], const float (&sc)[NP]) {
-#pragma unroll
-            for (int k = 0; k < NP; ++k) {
-                // 2^120 * scale, in two steps above 2^7 (2^127 is bf16's largest power)
-                const __nv_bfloat162 m =
-                    __float2bfloat162_rn(fminf(sc[k], 128.f) * 1.329227995784916e36f);
-                uint4 a = odd ? widen8(v[k].z, v[k].w, m) : widen8(v[k].x, v[k].y, m);
-                uint4 c2 = odd ? widen8(v[k].x, v[k].y, m) : widen8(v[k].z, v[k].w, m);
-                if (sc[k] > 128.f) {
-                    const __nv_bfloat162 m2 = __float2bfloat162_rn(sc[k] * 0.0078125f);
-                    uint32_t* w = reinterpret_cast<uint32_t*>(&a);
-                    uint32_t* w2 = reinterpret_cast<uint32_t*>(&c2);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        __nv_bfloat162 t = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&w[i]), m2);
-                        w[i] = *reinterpret_cast<uint32_t*>(&t);
-                        t = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&w2[i]), m2);
-                        w2[i] = *reinterpret_cast<uint32_t*>(&t);
-                    }
-                }
-                const uint32_t row = (uint32_t)first_row(k), ch = 2u * (c16 & 3) + (odd ? 1u : 0u);
-                uint8_t* half = st + (c16 >> 2) * kHalf;
-                *reinterpret_cast<uint4*>(half + swz128(row, ch)) = a;
-                *reinterpret_cast<uint4*>(half + swz128(row, ch ^ 1u)) = c2;
-            }
-        };
-        int32_t kb = 0, kb2 = 0, pg[NP];
-        uint32_t act;
-        uint4 kv[NP], vv[NP];
-        float ks[NP], vs[NP], vs2[NP];
-        if (n > 0) {
-            walk.next(kb, act);
-            read_pages(kb, pg);
-            resolve(kb, pg);
-            load_scales(ks, vs);
+        bool ok = n > 0 && ring_ready(0);
+        if (ok) {
+            place(0);
             load(pp.k_pool, kv);
             load(pp.v_pool, vv);
-            if (n > 1) {
-                walk.next(kb2, act);
-                read_pages(kb2, pg);
-            }
         }
-        bool ok = true;
+        ring_release(0);
         for (int32_t i = 0; i < n && ok; ++i) {
             const int s = i % kPbStages, ph = (i / kPbStages) & 1;
-            if (i >= kPbStages) ok = mbar_wait(bar(kBarKEmpty + s), ph ^ 1, abort_p, p.dev_err);
+            const bool more = i + 1 < n;
+            if (i >= kPbStages) ok = wait(bar(kBarKEmpty + s), ph ^ 1);
             if (!ok) break;
-            if (teller) {  // (the readers of block i - 8's lengths are done: P V of block i - 4 is)
-#pragma unroll
-                for (int k = 0; k < NP; ++k)
-                    meta[4 * (i & (kPbMetaSlots - 1)) + (first_row(k) >> 4)] = hi[k];
-                mbar_arrive(bar(kBarMeta + (i & (kPbMetaSlots - 1))));
-            }
-            store(base + L.kst + (uint32_t)s * L.blk_bytes, kv, ks);
+            store(base + L.kst + (uint32_t)s * L.blk_bytes, kv);
             fence_proxy_async_smem();
             mbar_arrive(bar(kBarKFull + s));
-            // the next block: its places, and its K on the way while this block's V is widened
-            const bool more = i + 1 < n;
+            // the next block's K is on its way while this block's V is widened
             if (more) {
-                resolve(kb2, pg);
-                load_scales(ks, vs2);
+                ok = ring_ready(i + 1);
+                if (!ok) break;
+                place(i + 1);
                 load(pp.k_pool, kv);
+                ring_release(i + 1);
             }
-            if (i >= kPbStages) ok = mbar_wait(bar(kBarVEmpty + s), ph ^ 1, abort_p, p.dev_err);
+            if (i >= kPbStages) ok = wait(bar(kBarVEmpty + s), ph ^ 1);
             if (!ok) break;
-            store(base + L.vst + (uint32_t)s * L.blk_bytes, vv, vs);
+            store(base + L.vst + (uint32_t)s * L.blk_bytes, vv);
             fence_proxy_async_smem();
             mbar_arrive(bar(kBarVFull + s));
-            if (more) {
-                load(pp.v_pool, vv);
-#pragma unroll
-                for (int k = 0; k < NP; ++k) vs[k] = vs2[k];
-                if (i + 2 < n) {
-                    walk.next(kb2, act);
-                    read_pages(kb2, pg);
-                }
-            }
+            if (more) load(pp.v_pool, vv);
         }
     } else if (active && warp == kPbMmaWarp) {
         // ---------------------------------------------------------------- MMA issuer
-        if (lane == 0 && n > 0) {
-            constexpr uint32_t idesc_s = tc_idesc(128, 64, 0);
-            constexpr uint32_t idesc_o = tc_idesc(128, D, 1);
-            const uint32_t qs = smem_u32(base + L.q);
-            const uint32_t kst0 = smem_u32(base + L.kst), vst0 = smem_u32(base + L.vst);
+        // The whole warp walks the blocks and waits; one lane issues. What the products depend on
+        // comes out of warp reductions: the compiler then knows it to be uniform.
+        if (n > 0) {
+            const uint32_t lead = elect_lane();
+            constexpr uint32_t idesc_s = pb_idesc(128, 64, 0);
+            constexpr uint32_t idesc_o = pb_idesc(128, D, 1);
+            const uint32_t qd = desc_lo(smem_u32(base + L.q), 16u);
+            const uint32_t kd = desc_lo(smem_u32(base + L.kst), 16u);
+            const uint32_t vd = desc_lo(smem_u32(base + L.vst), kHalf);
+            const uint32_t tb = __reduce_or_sync(0xffffffffu, tbase);
             bool ok = true;
-            int32_t j[2] = {0, 0};  // each tile's blocks so far
+            uint32_t j0 = 0u, j1 = 0u;  // each tile's blocks so far
             uint32_t act = 0u, prev = 0u;
-            int32_t kb;
-            Walk walk(bm, nq, nwords, nw, i0);
+            // S of a tile: its j'th scores into its buffer j % 2 (whose P V, of its block j - 2, was
+            // issued before: products run in order)
+            auto issue_s = [&](int t, uint32_t j, uint32_t k_lo) {
+                const uint32_t to = tb + 256u + 128u * t + 64u * (j & 1u);
+                const uint32_t a_lo = qd + t * (128u * 128u >> 4);
+                pb_mma_ss<false>(lead, to, a_lo, k_lo, idesc_s);
+#pragma unroll
+                for (int kk = 1; kk < D / 16; ++kk)
+                    pb_mma_ss<true>(lead, to, a_lo + (((kk >> 2) * (kPbRows * 128u) + (kk & 3) * 32u) >> 4),
+                                    k_lo + (((kk >> 2) * kHalf + (kk & 3) * 32u) >> 4), idesc_s);
+                pb_commit(lead, bar(kBarS + 2 * t) + 8u * (j & 1u));
+            };
+            // O += P V of a tile's j'th block: P from tensor memory (hi terms, then lo); every
+            // kPbWindow'th block begins a new sum
+            auto issue_pv = [&](int t, uint32_t j, uint32_t v_lo) {
+                const uint32_t from = tb + 256u + 128u * t + 64u * (j & 1u);
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        pb_mma_ts(lead, tb + 128u * t, from + 32u * part + 8u * kk, v_lo + (kk * 2048u >> 4),
+                                  idesc_o, (part > 0 || kk > 0) ? 1u : j & (kPbWindow - 1u));
+                }
+                pb_commit(lead, bar(kBarPv + t));
+            };
             for (int32_t i = 0; i <= n && ok; ++i) {
-                // S of block i: tile t's j'th scores into its buffer j % 2 (whose P V, of its block
-                // j - 2, was issued before: products run in order)
                 prev = act;
                 act = 0u;
                 if (i < n) {
-                    walk.next(kb, act);
+                    ok = ring_ready(i);
+                    if (!ok) break;
+                    act = __reduce_or_sync(0xffffffffu, (uint32_t)ring[i & (kPbRing - 1)].act);
+                    ring_release(i);
                     const int s = i % kPbStages;
-                    ok = mbar_wait(bar(kBarKFull + s), (i / kPbStages) & 1, abort_p, p.dev_err);
+                    ok = wait(bar(kBarKFull + s), (i / kPbStages) & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t kst = kst0 + (uint32_t)s * L.blk_bytes;
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (!((act >> t) & 1u)) continue;
-                        const int buf = j[t] & 1;
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint64_t ad = tc_sdesc(qs + (kk >> 2) * (kPbRows * 128u) +
-                                                             t * (128u * 128u) + (kk & 3) * 32u,
-                                                         16u, 1024u);
-                            const uint64_t bd =
-                                tc_sdesc(kst + (kk >> 2) * kHalf + (kk & 3) * 32u, 16u, 1024u);
-                            tc_mma_ss(tbase + 256u + 128u * t + 64u * buf, ad, bd, idesc_s,
-                                      kk > 0 ? 1u : 0u);
-                        }
-                        tc_commit(bar(kBarS + 2 * t + buf));
-                        ++j[t];
-                    }
-                    tc_commit(bar(kBarKEmpty + s));
+                    const uint32_t k_lo = kd + (uint32_t)s * (64u * D * 2u >> 4);
+                    if (act & 1u) issue_s(0, j0, k_lo);
+                    if (act & 2u) issue_s(1, j1, k_lo);
+                    pb_commit(lead, bar(kBarKEmpty + s));
+                    j0 += act & 1u;
+                    j1 += act >> 1;
                 }
                 if (i == 0) continue;
-                // O += P V of block i - 1: P from tensor memory (hi terms, then lo), V from shared
                 const int sv = (i - 1) % kPbStages;
-                ok = mbar_wait(bar(kBarVFull + sv), ((i - 1) / kPbStages) & 1, abort_p, p.dev_err);
-                const uint32_t vst = vst0 + (uint32_t)sv * L.blk_bytes;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (!((prev >> t) & 1u) || !ok) continue;
-                    const int32_t jt = j[t] - 1 - (int32_t)((act >> t) & 1u);  // its number
-                    const int buf = jt & 1;
-                    ok = mbar_wait(bar(kBarP + 2 * t + buf), (jt >> 1) & 1, abort_p, p.dev_err);
+                ok = wait(bar(kBarVFull + sv), ((i - 1) / kPbStages) & 1);
+                if (!ok) break;
+                const uint32_t v_lo = vd + (uint32_t)sv * (64u * D * 2u >> 4);
+                const uint32_t p0 = j0 - 1u - (act & 1u), p1 = j1 - 1u - (act >> 1);  // its numbers
+                if (prev & 1u) {
+                    ok = wait(bar(kBarP) + 8u * (p0 & 1u), (p0 >> 1) & 1u);
                     if (!ok) break;
                     tc_fence_after();
-#pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            const uint64_t bd = tc_sdesc(vst + kk * 2048u, kHalf, 1024u);
-                            tc_mma_ts(tbase + 128u * t,
-                                      tbase + 256u + 128u * t + 64u * buf + 32u * part + 8u * kk, bd,
-                                      idesc_o, (jt > 0 || part > 0 || kk > 0) ? 1u : 0u);
-                        }
-                    }
-                    tc_commit(bar(kBarPv + t));
+                    issue_pv(0, p0, v_lo);
                 }
-                tc_commit(bar(kBarVEmpty + sv));
+                if (prev & 2u) {
+                    ok = wait(bar(kBarP + 2) + 8u * (p1 & 1u), (p1 >> 1) & 1u);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_pv(1, p1, v_lo);
+                }
+                pb_commit(lead, bar(kBarVEmpty + sv));
             }
             // every product is done: the epilogue's signal, and nothing of this CTA's may still run
             // on the tensor cores when it exits
-            tc_commit(bar(kBarDrain));
+            pb_commit(lead, bar(kBarDrain));
             mbar_wait(bar(kBarDrain), 0, abort_p, p.dev_err);
         }
     } else if (active && warp < 8) {
         // ---------------------------------------------------------------- softmax threads
         const int t = warp >> 2, r = tid, z = r >> 6;  // tile, row and quarter
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t ocol = tbase + lanes + 128u * t;
         const int qi = q_block(z);
         const int32_t pos = (qa + qi) * kPfBlock + (r & 63);
-        const bool rowok = ((has >> qi) & 1u) && pos >= c0 && pos < Ln;
+        const bool rowok = ((has >> qi) & 1u) && ((tmask >> t) & 1u) && pos >= c0 && pos < Ln;
         const uint32_t* mine = bm + qi * nwords;
-        // |scale| log2(e), at least 1e-30 so that a masked key (-inf) never meets a zero factor
-        const float sl2a = fmaxf(fabsf(p.sl2), 1e-30f);
+        const float frow = qscale[r];
+        const int64_t row = ((int64_t)b * p.Tq + (rowok ? pos - c0 : 0)) * p.Hq + h0 + q_head(z);
+        float* orow = p.out + row * D;
         float m_used = kPfNegInf, m_true = kPfNegInf, l = 0.f;  // l is relative to m_used
+        int rexp = -126;  // O is relative to m_used and to 2^rexp
+        // what the output row holds of earlier windows is relative to 2^ref (-inf: nothing)
+        float ref = kPfNegInf;
         int32_t j = 0;  // this tile's blocks
         bool ok = true;
-        Walk walk(bm, nq, nwords, nw, i0);
         for (int32_t i = 0; i < n; ++i) {
-            int32_t kb;
-            uint32_t act;
-            walk.next(kb, act);
-            if (!((act >> t) & 1u)) continue;
-            const int buf = j & 1, ms = i & (kPbMetaSlots - 1);
-            ok = mbar_wait(bar(kBarMeta + ms), (i / kPbMetaSlots) & 1, abort_p, p.dev_err) &&
-                 mbar_wait(bar(kBarS + 2 * t + buf), (j >> 1) & 1, abort_p, p.dev_err);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
+            ok = ring_ready(i);
+            if (!ok) break;
+            const PbBlock& blk = ring[i & (kPbRing - 1)];
+            if (!((blk.act >> t) & 1)) {
+                ring_release(i);
+                continue;
             }
+            const int buf = j & 1;
+            ok = wait(bar(kBarS + 2 * t + buf), (j >> 1) & 1);
+            if (!ok) break;
             tc_fence_after();
-            const int4 his = *reinterpret_cast<const int4*>(meta + 4 * ms);
+            if (j > 0 && (j & (kPbWindow - 1)) == 0) {
+                // A window is over: its sum goes to the output row, the next one begins at zero.
+                // (P V of block j - 2 ended before these scores were made, so the barrier is at most
+                // one phase behind, which its parity can tell.)
+                mbar_wait(bar(kBarPv + t), (j - 1) & 1, abort_p, p.dev_err);
+                tc_fence_after();
+                const bool some = rowok && m_used != kPfNegInf;
+                const float at = m_used + (float)rexp;
+                const bool first = some && ref == kPfNegInf;
+                // far above the row's reference, what it holds moves to the new one first
+                const bool move = some && !first && at > ref + 60.f;
+                const float down = move ? exp2f(ref - at) : 1.f;
+                if (first || move) ref = at;
+                const float f = some ? exp2f(at - ref) : 0.f;
+#pragma unroll 1
+                for (int cc = 0; cc < D / 16; ++cc) {
+                    float v[16];
+                    tc_ld16(ocol + 16u * cc, v);
+                    tc_wait_ld();
+                    float* to = orow + 16 * cc;
+                    if (move) {
+                        __threadfence();
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 o = __ldcg(reinterpret_cast<const float4*>(to + e));
+                            *reinterpret_cast<float4*>(to + e) =
+                                make_float4(fmaf(o.x, down, v[e]), fmaf(o.y, down, v[e + 1]),
+                                            fmaf(o.z, down, v[e + 2]), fmaf(o.w, down, v[e + 3]));
+                        }
+                    } else if (first) {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            *reinterpret_cast<float4*>(to + e) =
+                                make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    } else if (some) {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            red_add4(to + e, v[e] * f, v[e + 1] * f, v[e + 2] * f, v[e + 3] * f);
+                    }
+                }
+                tc_fence_before();
+            }
             const uint32_t sbuf = tbase + lanes + 256u + 128u * t + 64u * buf;
             float x[64];
             {
@@ -556,72 +653,96 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                 tc_ld32(sbuf + 32u, v);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) x[32 + e] = v[e];
-                tc_wait_ld();
             }
+            // the tiles' lengths, score factors (at least 1e-30, so that a masked key, -inf, never
+            // meets a zero factor) and weight exponents
+            int32_t lim[kPfTiles], lv[kPfTiles];
+            float fu[kPfTiles];
+            const int32_t kb = blk.kb, rnew = blk.r;
+#pragma unroll
+            for (int u = 0; u < kPfTiles; ++u) {
+                const int4 tl = blk.tile[u];
+                lim[u] = tl.y;
+                fu[u] = fmaxf(frow * __int_as_float(tl.z), 1e-30f);
+                lv[u] = tl.w;
+            }
+            tc_wait_ld();
             // mask: the row's query block keeps kb, the key is written and at or before the query.
             // Key e of tile u is kept iff e < lim[u]; a block whose keys all pass for every row of
             // the warp skips the selects.
             const bool keep = rowok && ((mine[kb >> 5] >> (kb & 31)) & 1u);
             const int32_t cut = keep ? pos - kb * kPfBlock + 1 : 0;
-            float mxr;  // the row maximum of the raw scores
-            if (__all_sync(0xffffffffu, cut >= kPfBlock &&
-                                            (his.x + his.y + his.z + his.w) == kPfBlock)) {
-                mxr = row_max64(x);
-            } else {
-                const int32_t lim[4] = {min(his.x, cut), min(16 + his.y, cut), min(32 + his.z, cut),
-                                        min(48 + his.w, cut)};
+            if (!__all_sync(0xffffffffu, cut >= kPfBlock && lim[0] + lim[1] + lim[2] + lim[3] ==
+                                                                kPfBlock)) {
+#pragma unroll
+                for (int u = 0; u < kPfTiles; ++u) lim[u] = min(16 * u + lim[u], cut);
 #pragma unroll
                 for (int e = 0; e < 64; ++e) x[e] = e < lim[e >> 4] ? x[e] : kPfNegInf;
-                mxr = row_max64(x);
             }
-            const float mx = mxr * sl2a;  // scaled (log2 units); -inf stays -inf
+            // the row maximum of the scores (log2 units); -inf stays -inf
+            const float mx = fmaxf(fmaxf(max16(x) * fu[0], max16(x + 16) * fu[1]),
+                                   fmaxf(max16(x + 32) * fu[2], max16(x + 48) * fu[3]));
             m_true = fmaxf(m_true, mx);
-            // lazy rescale of O and l when the row maximum grows by more than 2^8; the tensor-memory
-            // traffic is warp-collective, so a warp rescales when any of its rows must
+            // lazy rescale of O and l when the row maximum grows by more than 2^8, and of O when r
+            // is raised; the tensor-memory traffic is warp-collective, so a warp rescales when any
+            // of its rows must
             const bool need = mx > m_used + kTcRescale || (m_used == kPfNegInf && mx != kPfNegInf);
             const float f = need && m_used != kPfNegInf ? exp2f(m_used - mx) : 1.f;
-            if (__any_sync(0xffffffffu, f != 1.f) && j > 0) {
-                // O holds the blocks before this one: wait for them, then scale it
+            const float fo = rnew != rexp ? f * (rexp - rnew < -126 ? 0.f : pow2i(rexp - rnew)) : f;
+            rexp = rnew;
+            if (__any_sync(0xffffffffu, fo != 1.f) && (j & (kPbWindow - 1)) != 0) {
+                // O holds the window's blocks before this one: wait for them, then scale it
                 mbar_wait(bar(kBarPv + t), (j - 1) & 1, abort_p, p.dev_err);
                 tc_fence_after();
 #pragma unroll 1
                 for (int cc = 0; cc < D / 16; ++cc) {  // (16 columns: the scores stay in registers)
                     float v[16];
-                    tc_ld16(tbase + lanes + 128u * t + 16u * cc, v);
+                    tc_ld16(ocol + 16u * cc, v);
                     tc_wait_ld();
-                    uint32_t u[16];
+                    uint32_t o[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(v[e] * f);
-                    tc_st16(tbase + lanes + 128u * t + 16u * cc, u);
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(v[e] * fo);
+                    tc_st16(ocol + 16u * cc, o);
                 }
                 tc_wait_st();
             }
             if (need) m_used = mx;
             const float mu = m_used == kPfNegInf ? 0.f : m_used;
-            // p = 2^(x |scale| log2(e) - mu) in pairs; a masked key (-inf) gives +0. P goes to the
-            // score buffer as two bf16 terms: hi (rounded) into columns [0, 32), lo (the rest,
-            // rounded) into [32, 64).
-            const uint64_t s2 = pack_f32x2(sl2a, sl2a), nmu2 = pack_f32x2(-mu, -mu);
-            float ls[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            // w = 2^(x f - mu + lv) in pairs; a masked key (-inf) gives +0. w goes to the score
+            // buffer as two fp16 terms: hi (its upper 11 bits) into columns [0, 32), lo (the exact
+            // rest, rounded) into [32, 64). The sum takes w without its tile's 2^lv.
+            l *= f;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 uint32_t ph[16], pl[16];
 #pragma unroll
-                for (int cc = 0; cc < 16; ++cc) {
-                    float p0, p1;
-                    fma_f32x2(x[32 * hf + 2 * cc], x[32 * hf + 2 * cc + 1], s2, nmu2, p0, p1);
-                    p0 = ex2_approx(p0);
-                    p1 = ex2_approx(p1);
-                    add_f32x2(ls[2 * (cc & 3)], ls[2 * (cc & 3) + 1], p0, p1);
-                    ph[cc] = pack_bf16(p0, p1);
-                    float r0, r1;
-                    sub_f32x2(p0, p1, bf16_lo(ph[cc]), bf16_hi(ph[cc]), r0, r1);
-                    pl[cc] = pack_bf16(r0, r1);
+                for (int uu = 0; uu < 2; ++uu) {
+                    const int u = 2 * hf + uu;
+                    const uint64_t f2 = pack_f32x2(fu[u], fu[u]);
+                    const float nm = (float)lv[u] - mu;
+                    const uint64_t n2 = pack_f32x2(nm, nm);
+                    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+                    for (int cc = 0; cc < 8; ++cc) {
+                        float p0, p1;
+                        fma_f32x2(x[16 * u + 2 * cc], x[16 * u + 2 * cc + 1], f2, n2, p0, p1);
+                        p0 = ex2_approx(p0);
+                        p1 = ex2_approx(p1);
+                        if (cc & 1) add_f32x2(s2, s3, p0, p1);
+                        else        add_f32x2(s0, s1, p0, p1);
+                        const float h0 = __uint_as_float(__float_as_uint(p0) & 0xffffe000u);
+                        const float h1 = __uint_as_float(__float_as_uint(p1) & 0xffffe000u);
+                        ph[8 * uu + cc] = pack_f16(h0, h1);
+                        float r0, r1;
+                        sub_f32x2(p0, p1, h0, h1, r0, r1);
+                        pl[8 * uu + cc] = pack_f16(r0, r1);
+                    }
+                    l = fmaf((s0 + s1) + (s2 + s3), pow2i(-lv[u]), l);
                 }
                 tc_st16(sbuf + 16u * hf, ph);
                 tc_st16(sbuf + 32u + 16u * hf, pl);
             }
-            l = l * f + (((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7])));
+            ring_release(i);
             tc_wait_st();
             tc_fence_before();
             mbar_arrive(bar(kBarP + 2 * t + buf));
@@ -634,88 +755,45 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
         }
         ok = __all_sync(0xffffffffu, ok);
         const bool any = j > 0 && ok;
-        const int64_t row = ((int64_t)b * p.Tq + (rowok ? pos - c0 : 0)) * p.Hq + h0 + q_head(z);
-        float* orow = p.out + row * D;
+        // out = (O + earlier windows) 2^rexp / l, the exponent and 1 / l multiplied in turn (either
+        // may be far from 1)
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        // a split leaves its unnormalised rows in shared memory (every stage and the query rows are
-        // done with), padded so that the rows of a quarter warp lie in different banks
-        float* srow = reinterpret_cast<float*>(base) + r * (D + 4);
+        const float up = pow2i(rexp);
+        const bool more = ref != kPfNegInf && ok;
+        const float down = more ? exp2f(ref - (m_used + (float)rexp)) : 0.f;
+        if (more) __threadfence();  // the row's earlier additions
 #pragma unroll 1
-        for (int cc = 0; cc < D / 32; ++cc) {
-            float v[32];
+        for (int cc = 0; cc < D / 16; ++cc) {
+            float v[16];
             if (any) {
-                tc_ld32(tbase + lanes + 128u * t + 32u * cc, v);
+                tc_ld16(ocol + 16u * cc, v);
                 tc_wait_ld();
             } else {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = 0.f;
+                for (int e = 0; e < 16; ++e) v[e] = 0.f;
             }
-            if (pp.split > 1) {
+            if (rowok) {
+                float* to = orow + 16 * cc;
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                    *reinterpret_cast<float4*>(srow + 32 * cc + e) =
-                        make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-            } else if (rowok) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                    *reinterpret_cast<float4*>(orow + 32 * cc + e) =
-                        make_float4(v[e] * inv, v[e + 1] * inv, v[e + 2] * inv, v[e + 3] * inv);
+                for (int e = 0; e < 16; e += 4) {
+                    float4 o = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    if (more) {
+                        const float4 a = __ldcg(reinterpret_cast<const float4*>(to + e));
+                        o.x = fmaf(a.x, down, o.x);
+                        o.y = fmaf(a.y, down, o.y);
+                        o.z = fmaf(a.z, down, o.z);
+                        o.w = fmaf(a.w, down, o.w);
+                    }
+                    *reinterpret_cast<float4*>(to + e) =
+                        make_float4(o.x * inv * up, o.y * inv * up, o.z * inv * up, o.w * inv * up);
+                }
             }
         }
-        if (pp.split > 1) {
-            // the sum and O are relative to m_used
-            reinterpret_cast<float*>(base + L.mrow)[r] = l > 0.f ? m_used : kPfNegInf;
-            reinterpret_cast<float*>(base + L.trow)[r] = m_true;
-            reinterpret_cast<float*>(base + L.lrow)[r] = l;
-        } else if (rowok) {
+        if (rowok) {
             // report the true row max and the sum relative to it
             if (p.m_out) p.m_out[row] = m_true == kPfNegInf ? kPfNegInf : m_true * kLn2;
             if (p.e_out) p.e_out[row] = m_true == kPfNegInf ? 0.f : l * exp2f(m_used - m_true);
         }
-    }
-    if (pp.split > 1) {
-        // ---- merge the cluster's parts: rank k takes every split'th row from the k'th on -------
-        // (an inactive CTA's cluster is inactive as a whole; all pass the barriers)
-        cluster_sync();
-        if (active) {
-            const uint32_t o0 = smem_u32(base), m0 = smem_u32(base + L.mrow);
-            const uint32_t t0 = smem_u32(base + L.trow), l0 = smem_u32(base + L.lrow);
-            constexpr int TPR = D / 4;  // threads of a row, a float4 each
-            for (int x = tid; x < kPbRows / pp.split * TPR; x += kPbThreads) {
-                const int r = x / TPR * pp.split + rank, d4 = x % TPR, z = r >> 6;
-                const int qi = q_block(z);
-                const int32_t pos = (qa + qi) * kPfBlock + (r & 63);
-                if (!((has >> qi) & 1u) || pos < c0 || pos >= Ln) continue;
-                float mg = kPfNegInf;
-                for (int k = 0; k < pp.split; ++k)
-                    mg = fmaxf(mg, ld_cluster(map_rank(m0 + 4u * r, k)));
-                float e = 0.f;
-                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int k = 0; k < pp.split && mg != kPfNegInf; ++k) {
-                    const float mk = ld_cluster(map_rank(m0 + 4u * r, k));
-                    if (mk == kPfNegInf) continue;
-                    const float w = exp2f(mk - mg);
-                    e += w * ld_cluster(map_rank(l0 + 4u * r, k));
-                    const float4 v = ld_cluster4(map_rank(o0 + 4u * (r * (D + 4) + 4 * d4), k));
-                    o.x += w * v.x;
-                    o.y += w * v.y;
-                    o.z += w * v.z;
-                    o.w += w * v.w;
-                }
-                const float inv = e > 0.f ? 1.f / e : 0.f;
-                const int64_t row = ((int64_t)b * p.Tq + (pos - c0)) * p.Hq + h0 + q_head(z);
-                *reinterpret_cast<float4*>(p.out + row * D + 4 * d4) =
-                    make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-                if (d4 == 0 && (p.m_out || p.e_out)) {
-                    float mt = kPfNegInf;  // the true row max; e moves to it
-                    for (int k = 0; k < pp.split; ++k)
-                        mt = fmaxf(mt, ld_cluster(map_rank(t0 + 4u * r, k)));
-                    if (p.m_out) p.m_out[row] = mt == kPfNegInf ? kPfNegInf : mt * kLn2;
-                    if (p.e_out) p.e_out[row] = mt == kPfNegInf ? 0.f : e * exp2f(mg - mt);
-                }
-            }
-        }
-        cluster_sync();  // no CTA's shared memory goes away while another reads it
     }
     // ---- teardown: the allocating warp frees the tensor memory --------------------------------
     tc_fence_before();
@@ -745,14 +823,17 @@ static dattn_status_t launch_d(const PfParams& p0, const void* k_pool, const voi
     const int32_t blocks = (p.Tq + kPfBlock - 1) / kPfBlock + 1;  // query blocks a chunk can touch
     p.nqb = (blocks + pp.nq - 1) / pp.nq;
     const int64_t per_head = (int64_t)p.nqb * (p.g / pp.hp);
-    const int64_t tiles = (int64_t)p.B * p.Hkv * per_head;
+    const int64_t pairs = (int64_t)p.B * p.Hkv * per_head;
     const int32_t sms = sm_count_current();
-    pp.split = 1;
-    if (tiles * pp.split >= (1ll << 31)) return DATTN_ERR_UNSUPPORTED;
+    // a last wave of tile pairs for at most half of the SMs: a CTA for each tile instead
+    const int64_t rest = pairs % sms;
+    pp.whole = (int32_t)(2 * rest <= sms ? pairs - rest : pairs);
+    const int64_t ctas = pp.whole + 2 * (pairs - pp.whole);
+    if (pairs >= (1ll << 31) - sms) return DATTN_ERR_UNSUPPORTED;
     // as in prefill.cu: the smallest group of KV heads whose CTAs fill three waves
     p.kv_group = p.Hkv;
     for (int32_t G = 1; G < p.Hkv; ++G)
-        if (p.Hkv % G == 0 && G * per_head * pp.split >= 3ll * sms) {
+        if (p.Hkv % G == 0 && G * per_head >= 3ll * sms) {
             p.kv_group = G;
             break;
         }
@@ -770,19 +851,8 @@ static dattn_status_t launch_d(const PfParams& p0, const void* k_pool, const voi
             set = (int)L.total;
         }
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * pp.split));
-    cfg.blockDim = dim3(kPbThreads);
-    cfg.dynamicSmemBytes = L.total;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {(unsigned)pp.split, 1u, 1u};
-    cfg.attrs = attr;
-    cfg.numAttrs = pp.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, prefill_block_kernel<D>, pp, nwords) == cudaSuccess
+    return launch_pdl(prefill_block_kernel<D>, dim3((unsigned)ctas), dim3(kPbThreads), L.total,
+                      stream, pp, nwords) == cudaSuccess
                ? DATTN_OK
                : DATTN_ERR_CUDA;
 }
