@@ -14,26 +14,24 @@
 // context shrinks the result (5.6e-5 after 4096 products of a 32K context), so a row's accumulator is
 // emptied into its output row every kPbWindow key blocks, by fp32 additions.
 //
-// What bounds it: the tensor cores. A step takes two key blocks, 128 keys. For 128 query rows it
-// needs one product S = Q K^T and two products O += P V, 3 x 2 x 128 x 128 x d operations for the
-// 2 x 2 x 128 x 128 x d that count: 2/3 of the dense 16-bit rate at most. The keys of a step are
-// widened once for 256 query rows: one CTA per SM holds two tiles of 128 rows, and while one tile is
-// in its softmax the tensor cores work on the other. (One key block to a step, with two score
-// buffers for each tile, lost as much again to the waits and the products of half the size.)
+// What bounds it: the tensor cores. A 64-key block of 128 query rows takes one product S = Q K^T
+// and two products O += P V, 3 x 2 x 128 x 64 x d operations for the 2 x 2 x 128 x 64 x d that count:
+// 2/3 of the dense 16-bit rate at most. A key block is widened once for 256 query rows: one CTA per
+// SM holds two tiles of 128 rows, and while one tile is in its softmax the tensor cores work on the
+// other.
 //
 // A CTA: 256 rows as four quarters of 64 tokens: one query block of four heads of a KV head (g a
 // multiple of 4), two query blocks of two heads (even g), or four query blocks of one head. A tile
-// (two quarters) takes part in a step only if one of its quarters keeps one of its blocks. Where the
-// last wave of CTAs would fill less than half of the SMs, its tiles get a CTA each. 22 warps:
-//   0-15   the softmax: a query row is two threads, one for each key block of a step (so that the
-//          two tiles' softmaxes fit beside each other's products); they exchange the row's maximum
-//          through shared memory, and each rescales and writes half of the row's output;
-//   16-19  load codes, widen them and write the K and V stages in the 128-byte-swizzled layout of
-//          the MMA operands;
-//   20     one thread issues the products: for each tile P V of the last step, then S of this one;
-//   21     walks the key blocks, eight at a time, one lane per 16-key tile, and leaves each block's
-//          place, lengths and scales in a ring in shared memory for the others.
-// Tensor memory: O of the two tiles, then their scores, over which P is written: all 512 columns.
+// (two quarters) takes part in a key block only if one of its quarters keeps it. Where the last
+// wave of CTAs would fill less than half of the SMs, its tiles get a CTA each. 14 warps:
+//   0-3, 4-7  one query row per thread of tile 0, 1: the softmax;
+//   8-11      load codes, widen them and write the K and V stages in the 128-byte-swizzled layout
+//             of the MMA operands;
+//   12        one thread issues the products: S of the next key block for both tiles, then P V of
+//             this one;
+//   13        walks the key blocks, eight at a time, one lane per 16-key tile, and leaves each
+//             block's place, lengths and scales in a ring in shared memory for the others.
+// Tensor memory: O of the two tiles, then two score buffers for each, all 512 columns.
 #include <mutex>
 
 #include "common.cuh"
@@ -45,29 +43,27 @@ namespace dattn {
 namespace {
 
 constexpr int kPbRows = 256;                // query rows of a CTA: two tiles of 128
-constexpr int kPbSoftWarps = 16;            // a row's softmax takes two threads
-constexpr int kPbConvWarp = 16;             // warps 16-19 widen the codes
+constexpr int kPbConvWarp = 8;              // warps 8-11 widen the codes
 constexpr int kPbConvThreads = 128;
-constexpr int kPbMmaWarp = 20;
-constexpr int kPbPlaceWarp = 21;            // the places of the key blocks
-constexpr int kPbThreads = 22 * 32;
-constexpr int kPbStages = 2;                // K stages, and V stages, of a step (two key blocks)
-constexpr int kPbGroup = 8;                 // key blocks that warp 21 resolves at once
+constexpr int kPbMmaWarp = 12;              // warps 12, 13 issue the products of tile 0, 1
+constexpr int kPbPlaceWarp = 14;            // the places of the key blocks
+constexpr int kPbThreads = 15 * 32;
+constexpr int kPbStages = 3;                // K stages, and V stages
+constexpr int kPbGroup = 8;                 // key blocks that warp 13 resolves at once
 constexpr int kPbRing = 2 * kPbGroup;       // the blocks' ring
-constexpr int kPbWindow = 8;                // steps between two emptyings of an accumulator
-constexpr uint32_t kPbCols = 512;           // O: [0, 128), [128, 256); S and P: 256 + 128 tile
+constexpr int kPbWindow = 32;               // key blocks between two emptyings of an accumulator
+constexpr uint32_t kPbCols = 512;           // O: [0, 128), [128, 256); S: 256 + 128 tile + 64 buffer
 
 // mbarriers
-constexpr int kBarKFull = 0, kBarKEmpty = 2, kBarVFull = 4, kBarVEmpty = 6;  // + stage
-constexpr int kBarS = 8, kBarP = 10;        // + tile
-constexpr int kBarRingFull = 12, kBarRingEmpty = 14, kBarDrain = 16;
-constexpr int kBarPair = 17, kPbBars = 25;  // + warp & 7: the two warps of the same rows
-constexpr int kRingReaders = 21;            // warps 0-20
+constexpr int kBarKFull = 0, kBarKEmpty = 3, kBarVFull = 6, kBarVEmpty = 9;
+constexpr int kBarS = 12, kBarP = 16;       // + 2 tile + buffer
+constexpr int kBarPv = 20;                  // + tile
+constexpr int kBarRingFull = 22, kBarRingEmpty = 24, kBarDrain = 26, kPbBars = 28;
+constexpr int kRingReaders = 14;            // warps 0-13
 
 // A key block in the ring: its 16-key tiles as the widening reads them (first row over all heads,
 // tokens) and as the softmax does (K scale, -, log2 of the V scale over 2^r, 2 to minus that), its
-// index, the quarters of rows that keep it (bits 0-3; bit 4: all its keys are written) and its
-// step's r.
+// index, the quarters of rows that keep it (bits 0-3; bit 4: all its keys are written) and r.
 struct PbBlock {
     int2 rows[kPfTiles];
     float4 scale[kPfTiles];
@@ -80,22 +76,21 @@ __device__ __forceinline__ uint32_t tiles_of(uint32_t act) {
 }
 
 struct PbSmem {
-    uint32_t q, step_bytes, kst, vst, bm, ring, bars, taddr, abort, qscale, rowx, total;
+    uint32_t q, blk_bytes, kst, vst, bm, ring, bars, taddr, abort, qscale, total;
 };
 
 __host__ __device__ inline PbSmem pb_smem_layout(int D, int nq, int nwords) {
     PbSmem s;
     uint32_t o = 0;
     s.q = o;           o += (uint32_t)kPbRows * D * 2u;
-    s.step_bytes = 128u * D * 2u;
-    s.kst = o;         o += kPbStages * s.step_bytes;
-    s.vst = o;         o += kPbStages * s.step_bytes;
+    s.blk_bytes = 64u * D * 2u;
+    s.kst = o;         o += kPbStages * s.blk_bytes;
+    s.vst = o;         o += kPbStages * s.blk_bytes;
     s.ring = o;        o += kPbRing * (uint32_t)sizeof(PbBlock);
     s.bars = o;        o += (kPbBars + 1) * 8u;
     s.taddr = o;       o += 16u;
     s.abort = o;       o += 16u;
     s.qscale = o;      o += kPbRows * 4u;
-    s.rowx = o;        o += 2u * 2u * kPbRows * 4u;  // [buffer][half][row]
     s.bm = o;          o += (uint32_t)(nq * nwords) * 4u;
     s.total = o;
     return s;
@@ -193,7 +188,7 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) 
 template <int D>
 __global__ void __launch_bounds__(kPbThreads, 1)
 prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
-    constexpr uint32_t kHalf = 128u * 128u;  // a 128-byte half of a step's rows
+    constexpr uint32_t kHalf = 64u * 128u;  // a 128-byte half of a key block's rows
     const PfParams& p = pp.f;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = smem_raw;
@@ -230,18 +225,21 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
     if (tid == 0) {
         for (int s = 0; s < kPbStages; ++s) {
             mbar_init(bar(kBarKFull + s), kPbConvThreads);
-            mbar_init(bar(kBarKEmpty + s), 1);
+            mbar_init(bar(kBarKEmpty + s), 2);
             mbar_init(bar(kBarVFull + s), kPbConvThreads);
-            mbar_init(bar(kBarVEmpty + s), 1);
+            mbar_init(bar(kBarVEmpty + s), 2);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bar(kBarS + i), 1);
+            mbar_init(bar(kBarP + i), 128);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(kBarS + i), 1);
-            mbar_init(bar(kBarP + i), 256);
+            mbar_init(bar(kBarPv + i), 1);
             mbar_init(bar(kBarRingFull + i), 1);
             mbar_init(bar(kBarRingEmpty + i), kRingReaders);
         }
         mbar_init(bar(kBarDrain), 1);
-        for (int i = 0; i < 8; ++i) mbar_init(bar(kBarPair + i), 2);
+        mbar_init(bar(kBarDrain + 1), 1);
         *abort_p = 0;
         fence_mbar_init();
     }
@@ -346,18 +344,19 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
         uint32_t q[4];
         n += __popc(held_word(bm, nq, nwords, tmask, w, q));
     }
-    const int32_t ns = (n + 1) >> 1;  // steps of two key blocks; the last may miss its second
-    // The ring: block x in slot x % 16, ready with its group of eight (four steps); a reader's warp
-    // gives a group back after its last step.
+    // The ring: block i in slot i % 16, ready with its group of eight; a reader's warp gives a group
+    // back after its last block.
     auto wait = [&](uint32_t bar_addr, uint32_t parity) {  // by a whole warp, one answer
         return __all_sync(0xffffffffu, mbar_wait(bar_addr, parity, abort_p, p.dev_err)) != 0;
     };
     auto ring_ready = [&](int32_t i) {
-        return (i & 3) != 0 || wait(bar(kBarRingFull) + 8u * ((i >> 2) & 1), (i >> 3) & 1);
+        return (i & (kPbGroup - 1)) != 0 ||
+               wait(bar(kBarRingFull) + 8u * ((i / kPbGroup) & 1), (i / kPbRing) & 1);
     };
     auto ring_release = [&](int32_t i) {
         __syncwarp();
-        if ((i & 3) == 3 && lane == 0) mbar_arrive(bar(kBarRingEmpty) + 8u * ((i >> 2) & 1));
+        if ((i & (kPbGroup - 1)) == kPbGroup - 1 && lane == 0)
+            mbar_arrive(bar(kBarRingEmpty) + 8u * ((i / kPbGroup) & 1));
     };
 
     if (active && warp == kPbPlaceWarp) {
@@ -396,16 +395,15 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                     sc = __ldg(pp.scale + (y >> 4));
                 }
             }
-            // 2^r: what the V scales up to each step exceed by 2^7 at most
+            // 2^r: what the V scales up to each block exceed by 2^7 at most
             const int ve = sc.y > 0.f ? (__float_as_int(sc.y) >> 23) - 127 : -1000;
             int vm = max(ve, __shfl_xor_sync(0xffffffffu, ve, 1));
             vm = max(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
             int mine = r;
-            for (int x = 0; x < kPbGroup / 2; ++x) {
-                const int v = max(__shfl_sync(0xffffffffu, vm, 8 * x),
-                                  __shfl_sync(0xffffffffu, vm, 8 * x + 4));
+            for (int x = 0; x < kPbGroup; ++x) {
+                const int v = __shfl_sync(0xffffffffu, vm, 4 * x);
                 if (v > r + 7) r = v;
-                if (x == blk >> 1) mine = r;
+                if (x == blk) mine = r;
             }
             // (far below 2^r a scale counts as 2^(r - 64): nothing beside the others; codes with
             // scale 0 are zeros)
@@ -415,7 +413,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
             full &= __shfl_xor_sync(0xffffffffu, full, 2);
             if (i >= kPbRing)
                 ok = wait(bar(kBarRingEmpty) + 8u * ((i / kPbGroup) & 1), ((i / kPbRing) - 1) & 1);
-            if (ok && blk < ((cnt + 1) & ~1)) {  // (an empty block completes the last step)
+            if (ok && blk < cnt) {
                 PbBlock& to = ring[(i + blk) & (kPbRing - 1)];
                 to.rows[u] = make_int2(y, hi);
                 to.scale[u] = make_float4(sc.x, 0.f, (float)lv, pow2i(-lv));
@@ -431,31 +429,38 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
     } else if (active && warp >= kPbConvWarp && warp < kPbMmaWarp) {
         // ------------------------------------------------------ widening: codes -> K and V stages
         // A row of D codes is D/16 threads of 16 codes; a pass takes RP rows, NP passes a block.
-        // Eight neighbours store to two rows of one half: all banks. The loads run two blocks ahead
-        // of the stores: K, K, V, V of a step in turn.
+        // Eight neighbours store to two rows of one half: all banks.
         constexpr int CPR = D / 16, RP = kPbConvThreads / CPR, NP = 64 / RP;
         const int ct = tid - kPbConvWarp * 32;
         const int c16 = D == 64 ? ct & 3 : (ct & 3) | ((ct >> 1) & 4);
         const int rr = D == 64 ? ct >> 2 : ((ct >> 2) & 1) | ((ct >> 4) << 1);
-        uint4 va[NP], vb[NP];  // the two blocks of a step
-        // 16 codes a row of block x; rows that hold no token of the request are zeros
-        auto load = [&](const uint8_t* pool, int32_t x, uint4 (&v)[NP]) {
-            const PbBlock& blk = ring[x & (kPbRing - 1)];
+        uint4 kv[NP], vv[NP];
+        int32_t y[NP], hi[NP];  // the next block's tiles
+        auto place = [&](int32_t i) {
+            const PbBlock& blk = ring[i & (kPbRing - 1)];
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
-                const int2 at = blk.rows[(rr + RP * k) >> 4];
+                const int2 t = blk.rows[(rr + RP * k) >> 4];
+                y[k] = t.x;
+                hi[k] = t.y;
+            }
+        };
+        // 16 codes a row; rows that hold no token of the request are zeros
+        auto load = [&](const uint8_t* pool, uint4 (&v)[NP]) {
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
                 const int r = (rr + RP * k) & 15;
                 v[k] = make_uint4(0u, 0u, 0u, 0u);
-                if (r < at.y)
-                    v[k] = __ldg(reinterpret_cast<const uint4*>(pool + (int64_t)(at.x + r) * D +
+                if (r < hi[k])
+                    v[k] = __ldg(reinterpret_cast<const uint4*>(pool + (int64_t)(y[k] + r) * D +
                                                                 16 * c16));
             }
         };
         const uint32_t half = (c16 >> 2) * kHalf, ch = 2u * (c16 & 3);
-        auto store = [&](uint8_t* st, int row0, const uint4 (&v)[NP]) {
+        auto store = [&](uint8_t* st, const uint4 (&v)[NP]) {
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
-                const uint32_t row = (uint32_t)(row0 + rr + RP * k);
+                const uint32_t row = (uint32_t)(rr + RP * k);
                 uint4 a, c2;
                 e4m3x4_to_f16(v[k].x, a.x, a.y);
                 e4m3x4_to_f16(v[k].y, a.z, a.w);
@@ -465,180 +470,164 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                 *reinterpret_cast<uint4*>(st + half + swz128(row, ch + 1u)) = c2;
             }
         };
-        bool ok = ns > 0 && ring_ready(0);
+        bool ok = n > 0 && ring_ready(0);
         if (ok) {
-            load(pp.k_pool, 0, va);
-            load(pp.k_pool, 1, vb);
+            place(0);
+            load(pp.k_pool, kv);
+            load(pp.v_pool, vv);
         }
-        for (int32_t i = 0; i < ns && ok; ++i) {
+        ring_release(0);
+        for (int32_t i = 0; i < n && ok; ++i) {
             const int s = i % kPbStages, ph = (i / kPbStages) & 1;
+            const bool more = i + 1 < n;
             if (i >= kPbStages) ok = wait(bar(kBarKEmpty + s), ph ^ 1);
             if (!ok) break;
-            uint8_t* st = base + L.kst + (uint32_t)s * L.step_bytes;
-            store(st, 0, va);
-            load(pp.v_pool, 2 * i, va);
-            store(st, 64, vb);
-            load(pp.v_pool, 2 * i + 1, vb);
+            store(base + L.kst + (uint32_t)s * L.blk_bytes, kv);
             fence_proxy_async_smem();
             mbar_arrive(bar(kBarKFull + s));
-            ring_release(i);
+            // the next block's K is on its way while this block's V is widened
+            if (more) {
+                ok = ring_ready(i + 1);
+                if (!ok) break;
+                place(i + 1);
+                load(pp.k_pool, kv);
+                ring_release(i + 1);
+            }
             if (i >= kPbStages) ok = wait(bar(kBarVEmpty + s), ph ^ 1);
             if (!ok) break;
-            const bool more = i + 1 < ns;
-            if (more) ok = ring_ready(i + 1);
-            if (!ok) break;
-            st = base + L.vst + (uint32_t)s * L.step_bytes;
-            store(st, 0, va);
-            if (more) load(pp.k_pool, 2 * i + 2, va);
-            store(st, 64, vb);
-            if (more) load(pp.k_pool, 2 * i + 3, vb);
+            store(base + L.vst + (uint32_t)s * L.blk_bytes, vv);
             fence_proxy_async_smem();
             mbar_arrive(bar(kBarVFull + s));
+            if (more) load(pp.v_pool, vv);
         }
-    } else if (active && warp == kPbMmaWarp) {
-        // ---------------------------------------------------------------- MMA issuer
-        // The whole warp walks the blocks and waits; one lane issues. What the products depend on
-        // comes out of warp reductions: the compiler then knows it to be uniform.
-        if (ns > 0) {
+    } else if (active && (warp == kPbMmaWarp || warp == kPbMmaWarp + 1)) {
+        // ---------------------------------------------------------------- MMA issuers
+        // A warp for each tile, so that neither tile's products wait for the other's softmax. The
+        // whole warp walks the blocks and waits; one lane issues. What the products depend on comes
+        // out of warp reductions: the compiler then knows it to be uniform.
+        if (n > 0) {
             const uint32_t lead = elect_lane();
-            constexpr uint32_t idesc_s = pb_idesc(128, 128, 0);
+            constexpr uint32_t idesc_s = pb_idesc(128, 64, 0);
             constexpr uint32_t idesc_o = pb_idesc(128, D, 1);
-            const uint32_t qd = desc_lo(smem_u32(base + L.q), 16u);
+            const uint32_t t = __reduce_or_sync(0xffffffffu, (uint32_t)(warp - kPbMmaWarp));
+            const uint32_t qd = desc_lo(smem_u32(base + L.q), 16u) + t * (128u * 128u >> 4);
             const uint32_t kd = desc_lo(smem_u32(base + L.kst), 16u);
             const uint32_t vd = desc_lo(smem_u32(base + L.vst), kHalf);
             const uint32_t tb = __reduce_or_sync(0xffffffffu, tbase);
+            const uint32_t oc = tb + 128u * t, sc = tb + 256u + 128u * t;
             bool ok = true;
-            uint32_t j0 = 0u, j1 = 0u;  // each tile's steps so far
+            uint32_t j = 0u;  // the tile's blocks so far
             uint32_t act = 0u, prev = 0u;
-            // S of a tile, over its P of the step before (whose P V was issued before: products run
-            // in order)
-            auto issue_s = [&](int t, uint32_t k_lo) {
-                const uint32_t to = tb + 256u + 128u * t;
-                const uint32_t a_lo = qd + t * (128u * 128u >> 4);
-                pb_mma_ss<false>(lead, to, a_lo, k_lo, idesc_s);
-#pragma unroll
-                for (int kk = 1; kk < D / 16; ++kk)
-                    pb_mma_ss<true>(lead, to,
-                                    a_lo + (((kk >> 2) * (kPbRows * 128u) + (kk & 3) * 32u) >> 4),
-                                    k_lo + (((kk >> 2) * kHalf + (kk & 3) * 32u) >> 4), idesc_s);
-                pb_commit(lead, bar(kBarS + t));
-            };
-            // O += P V of a tile's j'th step; every kPbWindow'th step begins a new sum. P of 32 keys is
-            // 16 columns of hi terms, then 16 of lo terms (see the softmax).
-            auto issue_pv = [&](int t, uint32_t j, uint32_t v_lo) {
-                const uint32_t from = tb + 256u + 128u * t;
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-#pragma unroll
-                    for (int part = 0; part < 2; ++part)
-                        pb_mma_ts(lead, tb + 128u * t,
-                                  from + 32u * (kk >> 1) + 16u * part + 8u * (kk & 1),
-                                  v_lo + (kk * 2048u >> 4), idesc_o,
-                                  (part > 0 || kk > 0) ? 1u : j & (kPbWindow - 1u));
-                }
-            };
-            for (int32_t i = 0; i <= ns && ok; ++i) {
+            for (int32_t i = 0; i <= n && ok; ++i) {
                 prev = act;
                 act = 0u;
-                uint32_t k_lo = 0u, v_lo = 0u;
-                if (i < ns) {
+                if (i < n) {
                     ok = ring_ready(i);
                     if (!ok) break;
-                    const PbBlock* blk = ring + ((2 * i) & (kPbRing - 1));
-                    act = tiles_of(__reduce_or_sync(0xffffffffu, (uint32_t)(blk[0].act | blk[1].act)));
+                    act = (tiles_of(__reduce_or_sync(0xffffffffu,
+                                                     (uint32_t)ring[i & (kPbRing - 1)].act)) >> t) & 1u;
                     ring_release(i);
                     const int s = i % kPbStages;
                     ok = wait(bar(kBarKFull + s), (i / kPbStages) & 1);
                     if (!ok) break;
-                    k_lo = kd + (uint32_t)s * (128u * D * 2u >> 4);
+                    tc_fence_after();
+                    if (act) {
+                        // S: the tile's j'th scores into its buffer j % 2 (whose P V, of its block
+                        // j - 2, was issued before: products run in order)
+                        const uint32_t k_lo = kd + (uint32_t)s * (64u * D * 2u >> 4);
+                        const uint32_t to = sc + 64u * (j & 1u);
+                        pb_mma_ss<false>(lead, to, qd, k_lo, idesc_s);
+#pragma unroll
+                        for (int kk = 1; kk < D / 16; ++kk)
+                            pb_mma_ss<true>(lead, to,
+                                            qd + (((kk >> 2) * (kPbRows * 128u) + (kk & 3) * 32u) >> 4),
+                                            k_lo + (((kk >> 2) * kHalf + (kk & 3) * 32u) >> 4), idesc_s);
+                        pb_commit(lead, bar(kBarS) + 16u * t + 8u * (j & 1u));
+                    }
+                    pb_commit(lead, bar(kBarKEmpty + s));
                 }
                 if (i > 0) {
                     const int sv = (i - 1) % kPbStages;
                     ok = wait(bar(kBarVFull + sv), ((i - 1) / kPbStages) & 1);
                     if (!ok) break;
-                    v_lo = vd + (uint32_t)sv * (128u * D * 2u >> 4);
+                    if (prev) {
+                        // O += P V of its block before: P from tensor memory (hi terms, then lo);
+                        // every kPbWindow'th block begins a new sum
+                        const uint32_t jp = j - 1u;
+                        ok = wait(bar(kBarP) + 16u * t + 8u * (jp & 1u), (jp >> 1) & 1u);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t v_lo = vd + (uint32_t)sv * (64u * D * 2u >> 4);
+                        const uint32_t from = sc + 64u * (jp & 1u);
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                pb_mma_ts(lead, oc, from + 32u * part + 8u * kk, v_lo + (kk * 2048u >> 4),
+                                          idesc_o, (part > 0 || kk > 0) ? 1u : jp & (kPbWindow - 1u));
+                        }
+                        pb_commit(lead, bar(kBarPv) + 8u * t);
+                    }
+                    pb_commit(lead, bar(kBarVEmpty + sv));
                 }
-                if (prev & 1u) {
-                    ok = wait(bar(kBarP), (j0 - 1u) & 1u);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_pv(0, j0 - 1u, v_lo);
-                }
-                if (act & 1u) {
-                    tc_fence_after();
-                    issue_s(0, k_lo);
-                }
-                if (prev & 2u) {
-                    ok = wait(bar(kBarP + 1), (j1 - 1u) & 1u);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_pv(1, j1 - 1u, v_lo);
-                }
-                if (i > 0) pb_commit(lead, bar(kBarVEmpty + (i - 1) % kPbStages));
-                if (act & 2u) {
-                    tc_fence_after();
-                    issue_s(1, k_lo);
-                }
-                if (i < ns) pb_commit(lead, bar(kBarKEmpty + i % kPbStages));
-                j0 += act & 1u;
-                j1 += act >> 1;
+                j += act;
             }
-            // every product is done: the epilogue's signal, and nothing of this CTA's may still run
+            // every product is done: the epilogue's signal, and nothing of this warp's may still run
             // on the tensor cores when it exits
-            pb_commit(lead, bar(kBarDrain));
-            mbar_wait(bar(kBarDrain), 0, abort_p, p.dev_err);
+            pb_commit(lead, bar(kBarDrain) + 8u * t);
+            mbar_wait(bar(kBarDrain) + 8u * t, 0, abort_p, p.dev_err);
         }
-    } else if (active && warp < kPbSoftWarps) {
+    } else if (active && warp < 8) {
         // ---------------------------------------------------------------- softmax threads
-        constexpr int HC = D / 2;  // output columns of a thread
-        const int t = (warp >> 2) & 1, hk = warp >> 3;  // tile; key block of a step, half of the columns
-        const int r = 128 * t + 32 * (warp & 3) + lane, z = r >> 6;  // row and quarter
+        const int t = warp >> 2, r = tid, z = r >> 6;  // tile, row and quarter
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t ocol = tbase + lanes + 128u * t + HC * hk;
-        const uint32_t scol = tbase + lanes + 256u + 128u * t + 64u * hk;
+        const uint32_t ocol = tbase + lanes + 128u * t;
         const int qi = q_block(z);
         const int32_t pos = (qa + qi) * kPfBlock + (r & 63);
         const bool rowok = ((has >> qi) & 1u) && ((tmask >> t) & 1u) && pos >= c0 && pos < Ln;
         const float frow = qscale[r];
-        float* rowx = reinterpret_cast<float*>(base + L.rowx) + r;
-        // Meets the warp of the other half of these rows: the e'th value goes into buffer e % 2, whose
-        // reader of two meetings ago has since come to the last one. (An mbarrier, whose wait is
-        // bounded, and not a named barrier: after a failed wait the two may part.)
-        auto meet = [&](float v, int32_t e, bool& good) {
-            float* x2 = rowx + (2 * (e & 1)) * kPbRows;
-            x2[hk * kPbRows] = v;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarPair + (warp & 7)));
-            good = wait(bar(kBarPair + (warp & 7)), e & 1);
-            return x2[(hk ^ 1) * kPbRows];
-        };
-        float m_used = kPfNegInf, m_true = kPfNegInf, l = 0.f;  // l (of these keys): to m_used
+        const int64_t row = ((int64_t)b * p.Tq + (rowok ? pos - c0 : 0)) * p.Hq + h0 + q_head(z);
+        float* orow = p.out + row * D;
+        float m_used = kPfNegInf, m_true = kPfNegInf, l = 0.f;  // l is relative to m_used
         int rexp = -126;  // O is relative to m_used and to 2^rexp
         // what the output row holds of earlier windows is relative to 2^ref (-inf: nothing)
         float ref = kPfNegInf;
-        int32_t j = 0;  // this tile's steps
+        int32_t j = 0;  // this tile's blocks
         bool ok = true;
-        for (int32_t i = 0; i < ns; ++i) {
+        for (int32_t i = 0; i < n; ++i) {
             ok = ring_ready(i);
             if (!ok) break;
-            const PbBlock* step = ring + ((2 * i) & (kPbRing - 1));
-            if (!((step[0].act | step[1].act) & (3 << (2 * t)))) {
+            const PbBlock& blk = ring[i & (kPbRing - 1)];
+            const int32_t act = blk.act, kb = blk.kb, rnew = blk.r;
+            if (!(act & (3 << (2 * t)))) {
                 ring_release(i);
                 continue;
             }
-            const PbBlock& blk = step[hk];
-            const int32_t act = blk.act, kb = blk.kb, rnew = step[1].r;
+            // the tiles' score factors (at least 1e-30, so that a masked key, -inf, never meets a
+            // zero factor)
+            float fu[kPfTiles];
+#pragma unroll
+            for (int u = 0; u < kPfTiles; ++u) fu[u] = fmaxf(frow * blk.scale[u].x, 1e-30f);
             // The row's query block keeps kb; all keys pass for every row of the warp if they are
             // written and kb is an earlier block (rows without a query compute on zeros).
             const bool keep = (act >> z) & 1;
             const bool all = keep && (act & kPbFull) && kb < qa + qi;
-            const int32_t cut = keep && rowok ? pos - kb * kPfBlock + 1 : 0;
-            ok = wait(bar(kBarS + t), j & 1);
+            int32_t lim[kPfTiles];
+            if (!all) {
+                const int32_t cut = keep && rowok ? pos - kb * kPfBlock + 1 : 0;
+#pragma unroll
+                for (int u = 0; u < kPfTiles; ++u) lim[u] = min(16 * u + blk.rows[u].y, cut);
+            }
+            const int buf = j & 1;
+            ok = wait(bar(kBarS + 2 * t + buf), (j >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
-            // (these scores were made after P V of the step before: O is complete up to it)
             if (j > 0 && (j & (kPbWindow - 1)) == 0) {
-                // a window is over: its sum goes to the output row, the next one begins at zero
+                // A window is over: its sum goes to the output row, the next one begins at zero.
+                // (P V of block j - 2 ended before these scores were made, so the barrier is at most
+                // one phase behind, which its parity can tell.)
+                mbar_wait(bar(kBarPv + t), (j - 1) & 1, abort_p, p.dev_err);
+                tc_fence_after();
                 const bool some = rowok && m_used != kPfNegInf;
                 const float at = m_used + (float)rexp;
                 const bool first = some && ref == kPfNegInf;
@@ -647,10 +636,8 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                 const float down = move ? exp2f(ref - at) : 1.f;
                 if (first || move) ref = at;
                 const float f = some ? exp2f(at - ref) : 0.f;
-                float* orow = p.out + (((int64_t)b * p.Tq + (rowok ? pos - c0 : 0)) * p.Hq + h0 +
-                                       q_head(z)) * D + HC * hk;
 #pragma unroll 1
-                for (int cc = 0; cc < HC / 16; ++cc) {
+                for (int cc = 0; cc < D / 16; ++cc) {
                     float v[16];
                     tc_ld16(ocol + 16u * cc, v);
                     tc_wait_ld();
@@ -674,36 +661,33 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                         for (int e = 0; e < 16; e += 4)
                             red_add4(to + e, v[e] * f, v[e + 1] * f, v[e + 2] * f, v[e + 3] * f);
                     }
-                    __syncwarp();
                 }
+                tc_fence_before();
             }
-            // The row maximum of the scores (log2 units; -inf stays -inf), 32 at a time: they are
-            // loaded again below. A tile's score factor is at least 1e-30, so that a masked key, -inf,
-            // never meets a zero factor. Key e of tile u is kept iff e < min(16 u + its tokens, cut).
-            auto scores = [&](int hf, float (&x)[32]) {
-                tc_ld32(scol + 32u * hf, x);
-                tc_wait_ld();
-                if (!all) {
-                    const int32_t l0 = min(32 * hf + blk.rows[2 * hf].y, cut) - 32 * hf;
-                    const int32_t l1 = min(32 * hf + 16 + blk.rows[2 * hf + 1].y, cut) - 32 * hf;
+            const uint32_t sbuf = tbase + lanes + 256u + 128u * t + 64u * buf;
+            float x[64];
+            {
+                float v[32];
+                tc_ld32(sbuf, v);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = e < (e < 16 ? l0 : l1) ? x[e] : kPfNegInf;
-                }
-            };
-            auto factor = [&](int u) { return fmaxf(frow * blk.scale[u].x, 1e-30f); };
-            float mx = kPfNegInf;
+                for (int e = 0; e < 32; ++e) x[e] = v[e];
+                tc_ld32(sbuf + 32u, v);
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                float x[32];
-                scores(hf, x);
-                mx = fmax3(mx, max16(x) * factor(2 * hf), max16(x + 16) * factor(2 * hf + 1));
+                for (int e = 0; e < 32; ++e) x[32 + e] = v[e];
             }
-            mx = fmaxf(mx, meet(mx, j, ok));
-            if (!ok) break;
+            tc_wait_ld();
+            // Key e of tile u is kept iff e < lim[u].
+            if (!all) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e) x[e] = e < lim[e >> 4] ? x[e] : kPfNegInf;
+            }
+            // the row maximum of the scores (log2 units); -inf stays -inf
+            const float mx = fmaxf(fmaxf(max16(x) * fu[0], max16(x + 16) * fu[1]),
+                                   fmaxf(max16(x + 32) * fu[2], max16(x + 48) * fu[3]));
             m_true = fmaxf(m_true, mx);
-            // lazy rescale of O and l when the row maximum grows by more than 2^8, and of O when r is
-            // raised; the tensor-memory traffic is warp-collective, so a warp rescales when any of its
-            // rows must
+            // lazy rescale of O and l when the row maximum grows by more than 2^8, and of O when r
+            // is raised; the tensor-memory traffic is warp-collective, so a warp rescales when any
+            // of its rows must
             const bool need = mx > m_used + kTcRescale || (m_used == kPfNegInf && mx != kPfNegInf);
             if (__any_sync(0xffffffffu, need) || rnew != rexp) {
                 const float f = need && m_used != kPfNegInf ? exp2f(m_used - mx) : 1.f;
@@ -711,8 +695,11 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                 rexp = rnew;
                 l *= f;
                 if ((j & (kPbWindow - 1)) != 0 && __any_sync(0xffffffffu, fo != 1.f)) {
+                    // O holds the window's blocks before this one: wait for them, then scale it
+                    mbar_wait(bar(kBarPv + t), (j - 1) & 1, abort_p, p.dev_err);
+                    tc_fence_after();
 #pragma unroll 1
-                    for (int cc = 0; cc < HC / 16; ++cc) {
+                    for (int cc = 0; cc < D / 16; ++cc) {  // (16 columns: the scores stay in registers)
                         float v[16];
                         tc_ld16(ocol + 16u * cc, v);
                         tc_wait_ld();
@@ -721,60 +708,57 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                         for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(v[e] * fo);
                         tc_st16(ocol + 16u * cc, o);
                     }
+                    tc_wait_st();
                 }
                 if (need) m_used = mx;
             }
             const float mu = m_used == kPfNegInf ? 0.f : m_used;
-            // w = 2^(x f - mu + lv) in pairs; a masked key (-inf) gives +0. w goes over the scores as
-            // two fp16 terms: of 32 keys, hi (the upper 11 bits) into the first 16 columns, lo (the
-            // exact rest, rounded) into the others. The sum takes w without its tile's 2^lv.
+            // w = 2^(x f - mu + lv) in pairs; a masked key (-inf) gives +0. w goes to the score
+            // buffer as two fp16 terms: hi (its upper 11 bits) into columns [0, 32), lo (the exact
+            // rest, rounded) into [32, 64). The sum takes w without its tile's 2^lv.
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                float x[32];
-                scores(hf, x);
                 uint32_t ph[16], pl[16];
 #pragma unroll
                 for (int uu = 0; uu < 2; ++uu) {
                     const int u = 2 * hf + uu;
-                    const float fu = factor(u);
+                    const uint64_t f2 = pack_f32x2(fu[u], fu[u]);
                     const float2 lv = *reinterpret_cast<const float2*>(&blk.scale[u].z);
-                    const uint64_t f2 = pack_f32x2(fu, fu);
                     const float nm = lv.x - mu;
                     const uint64_t n2 = pack_f32x2(nm, nm);
                     float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
                     for (int cc = 0; cc < 8; ++cc) {
                         float p0, p1;
-                        fma_f32x2(x[16 * uu + 2 * cc], x[16 * uu + 2 * cc + 1], f2, n2, p0, p1);
+                        fma_f32x2(x[16 * u + 2 * cc], x[16 * u + 2 * cc + 1], f2, n2, p0, p1);
                         p0 = ex2_approx(p0);
                         p1 = ex2_approx(p1);
                         if (cc & 1) add_f32x2(s2, s3, p0, p1);
                         else        add_f32x2(s0, s1, p0, p1);
-                        const float g0 = __uint_as_float(__float_as_uint(p0) & 0xffffe000u);
-                        const float g1 = __uint_as_float(__float_as_uint(p1) & 0xffffe000u);
-                        ph[8 * uu + cc] = pack_f16(g0, g1);
+                        const float h0 = __uint_as_float(__float_as_uint(p0) & 0xffffe000u);
+                        const float h1 = __uint_as_float(__float_as_uint(p1) & 0xffffe000u);
+                        ph[8 * uu + cc] = pack_f16(h0, h1);
                         float r0, r1;
-                        sub_f32x2(p0, p1, g0, g1, r0, r1);
+                        sub_f32x2(p0, p1, h0, h1, r0, r1);
                         pl[8 * uu + cc] = pack_f16(r0, r1);
                     }
                     l = fmaf((s0 + s1) + (s2 + s3), lv.y, l);
                 }
-                tc_st16(scol + 32u * hf, ph);
-                tc_st16(scol + 32u * hf + 16u, pl);
+                tc_st16(sbuf + 16u * hf, ph);
+                tc_st16(sbuf + 32u + 16u * hf, pl);
             }
             ring_release(i);
             tc_wait_st();
             tc_fence_before();
-            mbar_arrive(bar(kBarP + t));
+            mbar_arrive(bar(kBarP + 2 * t + buf));
             ++j;
         }
-        // ---- epilogue: this thread's half of the row's O, its maximum and sum -------------------
-        if (ok && ns > 0) {
-            ok = mbar_wait(bar(kBarDrain), 0, abort_p, p.dev_err);
+        // ---- epilogue: this row's O, maximum and sum ------------------------------------------
+        if (ok && n > 0) {
+            ok = mbar_wait(bar(kBarDrain + t), 0, abort_p, p.dev_err);
             tc_fence_after();
         }
         ok = __all_sync(0xffffffffu, ok);
-        if (ok) l += meet(l, j, ok);  // the other half's sum
         const bool any = j > 0 && ok;
         // out = (O + earlier windows) 2^rexp / l, the exponent and 1 / l multiplied in turn (either
         // may be far from 1)
@@ -782,11 +766,9 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
         const float up = pow2i(rexp);
         const bool more = ref != kPfNegInf && ok;
         const float down = more ? exp2f(ref - (m_used + (float)rexp)) : 0.f;
-        const int64_t row = ((int64_t)b * p.Tq + (rowok ? pos - c0 : 0)) * p.Hq + h0 + q_head(z);
-        float* orow = p.out + row * D + HC * hk;
         if (more) __threadfence();  // the row's earlier additions
 #pragma unroll 1
-        for (int cc = 0; cc < HC / 16; ++cc) {
+        for (int cc = 0; cc < D / 16; ++cc) {
             float v[16];
             if (any) {
                 tc_ld16(ocol + 16u * cc, v);
@@ -811,9 +793,8 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                         make_float4(o.x * inv * up, o.y * inv * up, o.z * inv * up, o.w * inv * up);
                 }
             }
-            __syncwarp();
         }
-        if (rowok && hk == 0) {
+        if (rowok) {
             // report the true row max and the sum relative to it
             if (p.m_out) p.m_out[row] = m_true == kPfNegInf ? kPfNegInf : m_true * kLn2;
             if (p.e_out) p.e_out[row] = m_true == kPfNegInf ? 0.f : l * exp2f(m_used - m_true);
