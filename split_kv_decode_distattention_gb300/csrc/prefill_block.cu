@@ -64,7 +64,7 @@ constexpr int kRingReaders = 14;            // warps 0-13
 // A key block in the ring: its 16-key tiles as the widening reads them (first row over all heads,
 // tokens) and as the softmax does (K scale, -, log2 of the V scale over 2^r, 2 to minus that), its
 // index, the quarters of rows that keep it (bits 0-3; bit 4: all its keys are written) and r.
-struct PbBlock {
+struct __align__(16) PbBlock {
     int2 rows[kPfTiles];
     float4 scale[kPfTiles];
     int32_t kb, act, r, pad;
@@ -415,7 +415,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                 ok = wait(bar(kBarRingEmpty) + 8u * ((i / kPbGroup) & 1), ((i / kPbRing) - 1) & 1);
             if (ok && blk < cnt) {
                 PbBlock& to = ring[(i + blk) & (kPbRing - 1)];
-                to.rows[u] = make_int2(y, hi);
+                to.rows[u] = make_int2(y >> 4, hi);
                 to.scale[u] = make_float4(sc.x, 0.f, (float)lv, pow2i(-lv));
                 if (u == 0) {
                     to.kb = kb;
@@ -435,25 +435,25 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
         const int c16 = D == 64 ? ct & 3 : (ct & 3) | ((ct >> 1) & 4);
         const int rr = D == 64 ? ct >> 2 : ((ct >> 2) & 1) | ((ct >> 4) << 1);
         uint4 kv[NP], vv[NP];
-        int32_t y[NP], hi[NP];  // the next block's tiles
-        auto place = [&](int32_t i) {
-            const PbBlock& blk = ring[i & (kPbRing - 1)];
+        // 16 codes a row of block x; rows that hold no token of the request are zeros. A thread's rows
+        // have one place in their tiles, (rr & 15).
+        const int64_t mine = (rr & 15) * D + 16 * c16;
+        auto load = [&](const uint8_t* pool, int32_t x, uint4 (&v)[NP]) {
+            const PbBlock& blk = ring[x & (kPbRing - 1)];
+            const uint8_t* from = pool + mine;
+            if (blk.act & kPbFull) {
 #pragma unroll
-            for (int k = 0; k < NP; ++k) {
-                const int2 t = blk.rows[(rr + RP * k) >> 4];
-                y[k] = t.x;
-                hi[k] = t.y;
+                for (int k = 0; k < NP; ++k)
+                    v[k] = __ldg(reinterpret_cast<const uint4*>(
+                        from + (int64_t)blk.rows[(rr + RP * k) >> 4].x * (16 * D)));
+                return;
             }
-        };
-        // 16 codes a row; rows that hold no token of the request are zeros
-        auto load = [&](const uint8_t* pool, uint4 (&v)[NP]) {
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
-                const int r = (rr + RP * k) & 15;
+                const int2 at = blk.rows[(rr + RP * k) >> 4];
                 v[k] = make_uint4(0u, 0u, 0u, 0u);
-                if (r < hi[k])
-                    v[k] = __ldg(reinterpret_cast<const uint4*>(pool + (int64_t)(y[k] + r) * D +
-                                                                16 * c16));
+                if ((rr & 15) < at.y)
+                    v[k] = __ldg(reinterpret_cast<const uint4*>(from + (int64_t)at.x * (16 * D)));
             }
         };
         const uint32_t half = (c16 >> 2) * kHalf, ch = 2u * (c16 & 3);
@@ -472,11 +472,9 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
         };
         bool ok = n > 0 && ring_ready(0);
         if (ok) {
-            place(0);
-            load(pp.k_pool, kv);
-            load(pp.v_pool, vv);
+            load(pp.k_pool, 0, kv);
+            load(pp.v_pool, 0, vv);
         }
-        ring_release(0);
         for (int32_t i = 0; i < n && ok; ++i) {
             const int s = i % kPbStages, ph = (i / kPbStages) & 1;
             const bool more = i + 1 < n;
@@ -485,20 +483,19 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
             store(base + L.kst + (uint32_t)s * L.blk_bytes, kv);
             fence_proxy_async_smem();
             mbar_arrive(bar(kBarKFull + s));
+            ring_release(i);  // (its V is in registers, or on its way)
             // the next block's K is on its way while this block's V is widened
             if (more) {
                 ok = ring_ready(i + 1);
                 if (!ok) break;
-                place(i + 1);
-                load(pp.k_pool, kv);
-                ring_release(i + 1);
+                load(pp.k_pool, i + 1, kv);
             }
             if (i >= kPbStages) ok = wait(bar(kBarVEmpty + s), ph ^ 1);
             if (!ok) break;
             store(base + L.vst + (uint32_t)s * L.blk_bytes, vv);
             fence_proxy_async_smem();
             mbar_arrive(bar(kBarVFull + s));
-            if (more) load(pp.v_pool, vv);
+            if (more) load(pp.v_pool, i + 1, vv);
         }
     } else if (active && (warp == kPbMmaWarp || warp == kPbMmaWarp + 1)) {
         // ---------------------------------------------------------------- MMA issuers
@@ -735,11 +732,10 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                         p1 = ex2_approx(p1);
                         if (cc & 1) add_f32x2(s2, s3, p0, p1);
                         else        add_f32x2(s0, s1, p0, p1);
-                        const float h0 = __uint_as_float(__float_as_uint(p0) & 0xffffe000u);
-                        const float h1 = __uint_as_float(__float_as_uint(p1) & 0xffffe000u);
-                        ph[8 * uu + cc] = pack_f16(h0, h1);
+                        const uint32_t g = pack_f16(p0, p1);
+                        ph[8 * uu + cc] = g;
                         float r0, r1;
-                        sub_f32x2(p0, p1, h0, h1, r0, r1);
+                        sub_f32x2(p0, p1, f16_lo(g), f16_hi(g), r0, r1);
                         pl[8 * uu + cc] = pack_f16(r0, r1);
                     }
                     l = fmaf((s0 + s1) + (s2 + s3), lv.y, l);
