@@ -217,19 +217,13 @@ def kv_scale_floats(kv_format: int, num_pages: int, num_kv_heads: int, page_size
 
 def _layout_sizes(layout, B: int, k_pool, v_pool, stats=None):
     """The pools, block table, scales and statistics must cover the layout for B requests."""
-    c = layout.c
-    n = c.num_pages * c.num_kv_heads * c.page_size
-    if c.kv_format == KV_MIXED:
-        pool = mixed_pool_bytes(c.num_pages, layout.head_format, c.head_dim, c.page_size)
-    else:
-        pool = n * (c.head_dim // 2 if c.kv_format == KV_INT4 else c.head_dim)
+    pool, scales, stat, table = layout.sizes
     _size(k_pool, pool, "k_pool")
     _size(v_pool, pool, "v_pool")
-    _size(layout.block_table, B * c.max_pages_per_req, "block_table")
-    if c.kv_format in _QUANT:
-        _size(layout.kv_scale, kv_scale_floats(c.kv_format, c.num_pages, c.num_kv_heads,
-                                               c.page_size), "kv_scale")
-    _size(stats, n // 16 * 2 * c.head_dim, "stats")
+    _size(layout.block_table, B * table, "block_table")
+    if scales:
+        _size(layout.kv_scale, scales, "kv_scale")
+    _size(stats, stat, "stats")
 
 
 def _pool(layout, t, name):
@@ -279,6 +273,14 @@ class KVLayout:
                          kv_scale.data_ptr() if kv_scale is not None else None,
                          ctypes.addressof(self._head_format_c)
                          if self._head_format_c is not None else None)
+        # elements of a pool, floats of kv_scale, elements of the statistics, block-table row width
+        n = num_pages * num_kv_heads * page_size
+        if kv_format == KV_MIXED:
+            pool = mixed_pool_bytes(num_pages, self.head_format, head_dim, page_size)
+        else:
+            pool = n * (head_dim // 2 if kv_format == KV_INT4 else head_dim)
+        self.sizes = (pool, kv_scale_floats(kv_format, num_pages, num_kv_heads, page_size),
+                      n // 16 * 2 * head_dim, block_table.shape[-1])
 
     @property
     def kv_format(self): return self.c.kv_format
@@ -494,19 +496,23 @@ def dattn_rope_append(layout: KVLayout, k_pool, v_pool, stats, rotation: Rotatio
     _pool(layout, k_pool, "k_pool"); _pool(layout, v_pool, "v_pool"); _bf16(stats, "stats")
     _bf16(q, "q"); _bf16(q_out, "q_out"); _bf16(k_new, "k_new"); _bf16(v_new, "v_new")
     _i32(seq_lens, "seq_lens"); _i32(positions, "positions"); _i32(new_lens, "new_lens")
-    if k_new.dim() != 4 or k_new.shape[2:] != (layout.num_kv_heads, layout.head_dim) or \
-            v_new.shape != k_new.shape:
+    Hkv, d = layout.num_kv_heads, layout.head_dim
+    size = k_new.shape
+    if len(size) != 4 or size[2] != Hkv or size[3] != d or v_new.shape != size:
         raise ValueError("k_new and v_new must be bf16 [B][T][Hkv][d]")
-    B, T = k_new.shape[:2]
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out come together")
+    B, T = size[0], size[1]
     Hq, qp, qs = 0, None, 0
     if q is not None:
-        Hq = q.shape[2] if q.dim() == 4 else 0
-        if q.shape != (B, T, Hq, layout.head_dim) or Hq == 0:
+        qsize = q.shape
+        if q_out is None:
+            raise ValueError("q and q_out come together")
+        if len(qsize) != 4 or qsize[0] != B or qsize[1] != T or qsize[3] != d or qsize[2] == 0:
             raise ValueError("q must be bf16 [B][T][Hq][d]")
-        _size(q_out, q.numel(), "q_out")
+        Hq = qsize[2]
+        _size(q_out, B * T * Hq * d, "q_out")
         qp, qs = _tokens(q, "q")
+    elif q_out is not None:
+        raise ValueError("q and q_out come together")
     _layout_sizes(layout, B, k_pool, v_pool, stats)
     _size(seq_lens, B, "seq_lens"); _size(new_lens, B, "new_lens")
     _size(positions, B * T, "positions")
