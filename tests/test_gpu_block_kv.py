@@ -480,3 +480,91 @@ def test_other_quantized_pools_still_have_no_prefill():
         q = _rows((1, 4, 2, 64), 86)
         with pytest.raises(dattn.DattnError, match="UNSUPPORTED"):
             _prefill(c, q)
+
+
+def _filled_fast(case, seed):
+    """A cache filled through the append, without the reference's pools, and its values in 64 bits
+    read from the codes on the GPU: [B][Hkv][L][d] of K and V (request 0)."""
+    cache = _cache(case)
+    L = case.lens[0]
+    k, v = _rows((1, L, case.Hkv, case.d), seed), _rows((1, L, case.Hkv, case.d), seed + 1)
+    cache.append(k, v)
+    n = case.num_pages * case.Hkv * (case.P // 16)
+    sc = cache.kv_scale[:2 * n].view(case.num_pages, case.Hkv, case.P // 16, 2).double()
+    pages = cache.block_table[0, :-(-L // case.P)].long()
+    out = []
+    for i, pool in enumerate((cache.k_pool, cache.v_pool)):
+        x = pool.view(torch.float8_e4m3fn)
+        x = x.view(torch.uint8)[pages].view(torch.float8_e4m3fn).double()
+        x = x * sc[pages][..., i].repeat_interleave(16, 2)[..., None]
+        out.append(x.transpose(0, 1).reshape(case.Hkv, -1, case.d)[:, :L])
+    return cache, out[0], out[1]
+
+
+def _attention64(q, K, V, scale):
+    """q [T][Hq][d] (the last T tokens) over K, V [Hkv][L][d], causal, on the GPU in 64 bits."""
+    T, Hq, d = q.shape
+    Hkv, L, _ = K.shape
+    out = torch.empty(T, Hq, d, dtype=torch.float64, device=DEV)
+    see = torch.arange(L, device=DEV)[None] <= (L - T + torch.arange(T, device=DEV))[:, None]
+    for h in range(Hq):
+        w = (q[:, h].double() @ K[h * Hkv // Hq].T * scale).masked_fill_(~see, -np.inf)
+        out[:, h] = torch.softmax(w, -1) @ V[h * Hkv // Hq]
+    return out
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,Tq,L", [(32, 8, 128, 1400, 9000), (16, 16, 64, 700, 7001),
+                                           (12, 6, 128, 1100, 5000)])
+def test_long_prefill_of_many_tiles(Hq, Hkv, d, Tq, L):
+    """Enough tiles for whole waves and single tiles, enough key blocks for several emptyings of
+    the accumulators (every 32). Between two of them a sum takes in 256 products, each losing less
+    than 2^-23 of it: 2^-15 together, beside which the other errors vanish. A repeated call gives
+    the same bits, and so does one beside another call on another stream."""
+    case = W.Case("pfl", B=1, Hq=Hq, Hkv=Hkv, d=d, P=16, lens=[L], seed=6)
+    cache, K, V = _filled_fast(case, 31)
+    q = _rows((1, Tq, Hq, d), 87)
+    out, m, e = _prefill(cache, q)
+    want = _attention64(q[0], K, V, case.scale)
+    assert ((out[0] - want).norm() / want.norm()).item() <= 2.0 ** -15
+    for h in (0, Hq - 1):  # no single row far off
+        err = (out[0, :, h] - want[:, h]).norm(dim=1) / want[:, h].norm(dim=1)
+        assert err.max().item() <= 2.0 ** -14
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = [torch.empty_like(out) for _ in streams]
+    torch.cuda.synchronize()
+    for s, o in zip(streams, outs):
+        for _ in range(2):
+            dattn.dattn_prefill(cache.layout, cache.k_pool, cache.v_pool, q, case.scale,
+                                cache.seq_lens, o, dev_err=cache.dev_err, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], out) and torch.equal(outs[1], out)
+    assert int(cache.dev_err.item()) == 0
+
+
+def test_prefill_whose_row_maxima_climb():
+    """Keys whose scores climb by 2^9 and more from window to window and block to block: what the
+    output row holds of earlier windows is moved to the new reference, or vanishes beside it."""
+    d, L, Tq = 64, 64 * 100, 64
+    case = W.Case("pfc", B=1, Hq=4, Hkv=1, d=d, P=64, lens=[L], seed=6, scale=1.0)
+    cache, kp, vp = _cache(case), *_pools(case)
+    k, v = _rows((1, L, 1, d), 41), _rows((1, L, 1, d), 42)
+    q = torch.zeros(1, Tq, 4, d, dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = torch.tensor([1.0, 0.02, 3.0, -1.0], device=DEV).to(torch.bfloat16)
+    k[0, :, 0, 0] = (torch.arange(L, device=DEV) // 64 * 8).to(torch.bfloat16)
+    cache.append(k, v)
+    kp.append(case.block_table[0], 0, k[0].double().cpu().numpy())
+    vp.append(case.block_table[0], 0, v[0].double().cpu().numpy())
+    out, m, e = _prefill(cache, q)
+    _check(case, q, out, m, e, kp, vp, weights=PREFILL)
+
+
+def test_decode_over_a_long_context_keeps_its_precision():
+    """32K keys: a tile's weighted sum is added rounding to nearest, 2^-24 of the sum a tile in any
+    order, random in sign: under 2^-20 of the output's norm."""
+    case = W.Case("dl", B=1, Hq=8, Hkv=2, d=128, P=16, lens=[32768], seed=6)
+    cache, K, V = _filled_fast(case, 33)
+    q = _rows((1, 1, 8, 128), 88)
+    out = torch.empty(1, 8, 128, device=DEV)
+    cache.decode(q[:, 0].contiguous(), out, cache.workspace(num_splits=1), num_splits=1)
+    want = _attention64(q[0], K, V, case.scale)
+    assert ((out - want).norm() / want.norm()).item() <= 2.0 ** -20
