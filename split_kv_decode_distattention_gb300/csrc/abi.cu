@@ -95,11 +95,11 @@ int sm_count_current() {
     return n;
 }
 
-int32_t choose_splits(int64_t total_tiles, int32_t requested, int occupancy) {
+int32_t choose_splits(int64_t total_tiles, int32_t requested, int occupancy, int32_t min_tiles) {
     if (requested > 0) return requested > (1 << 20) ? (1 << 20) : requested;
     int occ = occupancy < 1 ? 1 : (occupancy > kMaxCtasPerSm ? kMaxCtasPerSm : occupancy);
     int64_t G = (int64_t)sm_count_current() * occ;
-    const int64_t cap = total_tiles / 16 > 1 ? total_tiles / 16 : 1;
+    const int64_t cap = total_tiles / min_tiles > 1 ? total_tiles / min_tiles : 1;
     if (G > cap) G = cap;
     return G < 1 ? 1 : (int32_t)G;
 }

@@ -222,8 +222,9 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
 }
 
-// Number of CTAs for a launch with an upper bound of total_tiles tiles.
-int32_t choose_splits(int64_t total_tiles, int32_t requested, int occupancy);
+// Number of CTAs for a launch with an upper bound of total_tiles tiles, at least min_tiles to a CTA.
+int32_t choose_splits(int64_t total_tiles, int32_t requested, int occupancy,
+                      int32_t min_tiles = 16);
 
 // Bytes of the workspace's counter region: one counter per segment and the append's arrival
 // counter, padded to 256 bytes. The partial slots follow it.
