@@ -90,7 +90,9 @@
  *    the first written one), and stores code = E4M3(x / s), a single rounding. Where that
  *    raises the page's scale from s0 to s1, the earlier tokens' codes become
  *    E4M3(code * s0 / s1): unchanged values, except that codes below 2^-6 are rounded again.
- *    So tokens appended in one call and one by one are stored alike but for such codes.
+ *    So tokens appended in one call and one by one are stored alike but for such codes. A
+ *    logical page that holds tokens of a request is that request's alone: pages are shared
+ *    between requests only where they are full.
  *    Compared with a scale per row, a tile carries 8 bytes of scales instead of 128, and a
  *    prefill can read the pool (dattn_prefill). dattn_append_decode does not take this format:
  *    an append may rewrite rows that the same launch reads; call dattn_rope_append or
@@ -495,8 +497,7 @@ typedef struct dattn_prefill_sparse {
  *   DATTN_HEAD_STREAMING: kb < sink_blocks, or qb - local_blocks < kb <= qb;
  *   DATTN_HEAD_RETRIEVAL: the blocks listed in row qb of block_lists (blocks after qb add
  *                         nothing); a query that keeps no key gives out = 0, m = -inf, e = 0.
- * One CTA computes one 64-token query block of one query head over all its key blocks, so
- * no workspace is needed.
+ * One CTA computes its query blocks over all their key blocks, so no workspace is needed.
  *
  *   k_pool, v_pool (device) the pool: bf16 or DATTN_KV_FP8_BLOCK (DATTN_ERR_UNSUPPORTED for
  *            the other quantized formats)
@@ -504,6 +505,9 @@ typedef struct dattn_prefill_sparse {
  *   out      (device) fp32 [B][Tq][Hq][d]
  *   m, e     (device, nullable) fp32 [B][Tq][Hq]: the row max (natural-log units) and sum,
  *            so a chunk's result merges with others by dattn_merge's equations
+ * The products take a key block as a whole, with weight 0 for the keys that a query does not
+ * see: a NaN among the values of a token (bf16 pool: an infinity too) reaches every query that
+ * keeps its key block, also those before it.
  * A seq_len below Tq, or a query block beyond qblock_stride, is flagged with
  * DATTN_DEVERR_LEN_OOB and that query block is skipped (its outputs are left untouched).
  */

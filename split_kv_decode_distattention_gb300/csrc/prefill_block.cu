@@ -14,22 +14,24 @@
 // context shrinks the result (5.6e-5 after 4096 products of a 32K context), so a row's accumulator is
 // emptied into its output row every kPbWindow key blocks, by fp32 additions.
 //
-// What bounds it: the tensor cores. A 64-key block of 128 query rows takes one product S = Q K^T
-// and two products O += P V, 3 x 2 x 128 x 64 x d operations for the 2 x 2 x 128 x 64 x d that count:
-// 2/3 of the dense 16-bit rate at most. A key block is widened once for 256 query rows: one CTA per
-// SM holds two tiles of 128 rows, and while one tile is in its softmax the tensor cores work on the
-// other.
+// What bounds it: the tensor cores, then the softmax's latency. A 64-key block of 128 query rows
+// takes one product S = Q K^T and two products O += P V, 3 x 2 x 128 x 64 x d operations for the
+// 2 x 2 x 128 x 64 x d that count: 2/3 of the dense 16-bit rate at most. Measured: a causal prompt of
+// 32K tokens, 32 query and 8 KV heads of 128, 9.39 ms (939 TFLOP/s counted, 0.49 of the bf16 rate);
+// without the softmax's arithmetic 6.94 ms. A key block is widened once for 256 query rows: one CTA
+// per SM holds two tiles of 128 rows, which work past each other.
 //
 // A CTA: 256 rows as four quarters of 64 tokens: one query block of four heads of a KV head (g a
 // multiple of 4), two query blocks of two heads (even g), or four query blocks of one head. A tile
 // (two quarters) takes part in a key block only if one of its quarters keeps it. Where the last
-// wave of CTAs would fill less than half of the SMs, its tiles get a CTA each. 14 warps:
-//   0-3, 4-7  one query row per thread of tile 0, 1: the softmax;
+// wave of CTAs would fill less than half of the SMs, its tiles get a CTA each. 15 warps:
+//   0-3, 4-7  one query row per thread of tile 0, 1: the softmax. (Two threads per row took 11% longer:
+//             the second's share of the fixed work costs more than its latency saves.)
 //   8-11      load codes, widen them and write the K and V stages in the 128-byte-swizzled layout
 //             of the MMA operands;
-//   12        one thread issues the products: S of the next key block for both tiles, then P V of
-//             this one;
-//   13        walks the key blocks, eight at a time, one lane per 16-key tile, and leaves each
+//   12, 13    one thread each issues the products of tile 0, 1: S of the next key block, then P V of
+//             this one. (One issuing warp for both tiles made them wait for each other: 12.4 ms.)
+//   14        walks the key blocks, eight at a time, one lane per 16-key tile, and leaves each
 //             block's place, lengths and scales in a ring in shared memory for the others.
 // Tensor memory: O of the two tiles, then two score buffers for each, all 512 columns.
 #include <mutex>
@@ -49,9 +51,11 @@ constexpr int kPbMmaWarp = 12;              // warps 12, 13 issue the products o
 constexpr int kPbPlaceWarp = 14;            // the places of the key blocks
 constexpr int kPbThreads = 15 * 32;
 constexpr int kPbStages = 3;                // K stages, and V stages
-constexpr int kPbGroup = 8;                 // key blocks that warp 13 resolves at once
+constexpr int kPbGroup = 8;                 // key blocks that warp 14 resolves at once
 constexpr int kPbRing = 2 * kPbGroup;       // the blocks' ring
-constexpr int kPbWindow = 32;               // key blocks between two emptyings of an accumulator
+// Key blocks between two emptyings of an accumulator: 256 products that each lose up to 2^-24 of the
+// sum, 4.4e-6 of the result measured. (16: 2.2e-6 for 11% more time on a 32K prompt.)
+constexpr int kPbWindow = 32;
 constexpr uint32_t kPbCols = 512;           // O: [0, 128), [128, 256); S: 256 + 128 tile + 64 buffer
 
 // mbarriers
@@ -61,8 +65,8 @@ constexpr int kBarPv = 20;                  // + tile
 constexpr int kBarRingFull = 22, kBarRingEmpty = 24, kBarDrain = 26, kPbBars = 28;
 constexpr int kRingReaders = 14;            // warps 0-13
 
-// A key block in the ring: its 16-key tiles as the widening reads them (first row over all heads,
-// tokens) and as the softmax does (K scale, -, log2 of the V scale over 2^r, 2 to minus that), its
+// A key block in the ring: its 16-key tiles as the widening reads them (place in the pool, in tiles,
+// and tokens) and as the softmax does (K scale, -, log2 of the V scale over 2^r, 2 to minus that), its
 // index, the quarters of rows that keep it (bits 0-3; bit 4: all its keys are written) and r.
 struct __align__(16) PbBlock {
     int2 rows[kPfTiles];
@@ -711,8 +715,10 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
             }
             const float mu = m_used == kPfNegInf ? 0.f : m_used;
             // w = 2^(x f - mu + lv) in pairs; a masked key (-inf) gives +0. w goes to the score
-            // buffer as two fp16 terms: hi (its upper 11 bits) into columns [0, 32), lo (the exact
-            // rest, rounded) into [32, 64). The sum takes w without its tile's 2^lv.
+            // buffer as two fp16 terms: hi (rounded) into columns [0, 32), lo (the exact rest,
+            // rounded) into [32, 64). hi comes back from fp16 by a conversion, on the FMA pipe:
+            // masking its word would load the ALU pipe, which is the fuller one. The sum takes w
+            // without its tile's 2^lv.
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 uint32_t ph[16], pl[16];
