@@ -30,7 +30,6 @@ dattn_status_t launch_page_select(const dattn_kv_layout& Lay, const uint16_t* st
 
 namespace {
 
-constexpr int kMaxDevices = 64;
 std::atomic<int> g_sm_count[kMaxDevices];
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -81,6 +80,11 @@ dattn_status_t head_formats(const dattn_kv_layout& L, KvHeadFormats& f) {
         }
     }
     return DATTN_OK;
+}
+
+int device_index() {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices ? dev : 0;
 }
 
 int sm_count_current() {

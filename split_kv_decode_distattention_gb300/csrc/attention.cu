@@ -1796,7 +1796,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
 
 // ------------------------------------------------------------------ host side
 struct KernelInfo {
-    int max_smem_set = 0;
+    int max_smem_set[kMaxDevices] = {};  // a function attribute belongs to a device
 };
 
 template <int D, int FMT, bool APP, bool PK>
@@ -1810,13 +1810,13 @@ std::mutex g_attr_mutex;
 template <int D, int FMT, bool APP, bool PK>
 dattn_status_t ensure_smem(uint32_t bytes) {
     std::lock_guard<std::mutex> lock(g_attr_mutex);
-    KernelInfo& ki = kernel_info<D, FMT, APP, PK>();
-    if ((int)bytes > ki.max_smem_set) {
+    int& set = kernel_info<D, FMT, APP, PK>().max_smem_set[device_index()];
+    if ((int)bytes > set) {
         if (cudaFuncSetAttribute(attention_kernel<D, FMT, APP, PK>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)bytes) != cudaSuccess)
             return DATTN_ERR_CUDA;
-        ki.max_smem_set = (int)bytes;
+        set = (int)bytes;
     }
     return DATTN_OK;
 }

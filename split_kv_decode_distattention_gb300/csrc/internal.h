@@ -179,6 +179,9 @@ __host__ __device__ inline AttnSmem attn_smem_layout(int D, int g, int nitems, i
 }
 
 // Device properties and cached driver entry points.
+constexpr int kMaxDevices = 64;
+// The current device, or 0 outside the devices that per-device tables hold.
+int device_index();
 int sm_count_current();
 dattn_status_t make_kv_tensor_map(void* tmap_out, const void* pool, int64_t rows, int D);
 // 2-D map over rows of `row_bytes` one-byte elements (8-bit codes: d; packed 4-bit codes:

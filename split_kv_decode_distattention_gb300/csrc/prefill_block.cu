@@ -812,7 +812,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
 }
 
 std::mutex g_pb_mutex;
-int g_pb_smem_set[2] = {0, 0};
+int g_pb_smem_set[2][kMaxDevices] = {};  // a function attribute belongs to a device
 
 }  // namespace
 
@@ -849,7 +849,7 @@ static dattn_status_t launch_d(const PfParams& p0, const void* k_pool, const voi
     if (L.total > 227u * 1024u) return DATTN_ERR_UNSUPPORTED;
     {
         std::lock_guard<std::mutex> lock(g_pb_mutex);
-        int& set = g_pb_smem_set[D == 128 ? 1 : 0];
+        int& set = g_pb_smem_set[D == 128 ? 1 : 0][device_index()];
         if ((int)L.total > set) {
             if (cudaFuncSetAttribute(prefill_block_kernel<D>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
