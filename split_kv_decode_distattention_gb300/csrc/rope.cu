@@ -12,7 +12,7 @@
 // 0.06 rad at position 10^6. Sine and cosine of that fraction: sincos_turn.
 //
 // The kernels are bound by the bytes they move for long inputs (dattn_rope of 16384 tokens of 32
-// heads of 128 out of a fused projection: 42 us, 0.94 of the copy bandwidth) and by latency for
+// heads of 128 out of a fused projection: 41 us, 0.96 of the copy bandwidth) and by latency for
 // short ones. What costs beside the bytes is the sine and cosine, so a CTA computes them once for
 // 16 tokens (16 x r/2 pairs into shared memory) and uses them for all its heads. A warp takes one head of
 // the 16 tokens: D/16 lanes to a row, each with the two 8-channel chunks that are paired in
@@ -110,48 +110,35 @@ __device__ __forceinline__ void fill_table(RopeTable<D, ROWS>& tab, const RotArg
     }
 }
 
-// One lane's cos and sin of row r: eight pairs, two by two.
-struct Turn {
-    uint64_t c[4], s[4];
-};
-template <int D, int ROWS>
-__device__ __forceinline__ Turn turn_of(const RopeTable<D, ROWS>& tab, int r, int l, const RotArgs& rot) {
-    const int off2 = table_off2<D>(rot);
-    const ulonglong2 c0 = *reinterpret_cast<const ulonglong2*>(&tab.c[r][4 * l]);
-    const ulonglong2 c1 = *reinterpret_cast<const ulonglong2*>(&tab.c[r][off2 + 4 * l]);
-    const ulonglong2 s0 = *reinterpret_cast<const ulonglong2*>(&tab.s[r][4 * l]);
-    const ulonglong2 s1 = *reinterpret_cast<const ulonglong2*>(&tab.s[r][off2 + 4 * l]);
-    return Turn{{c0.x, c0.y, c1.x, c1.y}, {s0.x, s0.y, s1.x, s1.y}};
-}
-// Two pairs at once: x' = x c - y s, y' = y c + x s.
-__device__ __forceinline__ void turn2(uint64_t& x, uint64_t& y, uint64_t c, uint64_t s) {
-    const uint64_t xs = mul_f32x2(x, s);
-    x = sub_f32x2(mul_f32x2(x, c), mul_f32x2(y, s));
-    y = fma_f32x2(y, c, xs);
-}
-
-// Rotates a lane's two chunks (8 channels each) of row r; l is the lane's place in the row.
+// Rotates a lane's two chunks (8 channels each) of row r; l is the lane's place in the row. (Packed
+// fp32 pairs need fewer operations but more moves between registers: 35.3 us for 33.7 in an append
+// of 2 x 4093 tokens.)
 template <int D, int ROWS>
 __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const RopeTable<D, ROWS>& tab,
                                        int r, int l, const RotArgs& rot) {
     if (16 * l >= rot.rot_dim) return;  // unrotated channels
-    const Turn t = turn_of(tab, r, l, rot);
+    const int off2 = table_off2<D>(rot);
+    const float4 c0 = *reinterpret_cast<const float4*>(&tab.c[r][4 * l]);
+    const float4 c1 = *reinterpret_cast<const float4*>(&tab.c[r][off2 + 4 * l]);
+    const float4 s0 = *reinterpret_cast<const float4*>(&tab.s[r][4 * l]);
+    const float4 s1 = *reinterpret_cast<const float4*>(&tab.s[r][off2 + 4 * l]);
+    const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+    const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
     if (rot.interleaved) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float* v = (k < 2 ? a : b) + 4 * (k & 1);
-            uint64_t x = pack_f32x2(v[0], v[2]), y = pack_f32x2(v[1], v[3]);
-            turn2(x, y, t.c[k], t.s[k]);
-            unpack_f32x2(x, v[0], v[2]);
-            unpack_f32x2(y, v[1], v[3]);
+        for (int j = 0; j < 4; ++j) {
+            const float x = a[2 * j], y = a[2 * j + 1], u = b[2 * j], v = b[2 * j + 1];
+            a[2 * j] = fmaf(x, c[j], -(y * s[j]));
+            a[2 * j + 1] = fmaf(y, c[j], x * s[j]);
+            b[2 * j] = fmaf(u, c[4 + j], -(v * s[4 + j]));
+            b[2 * j + 1] = fmaf(v, c[4 + j], u * s[4 + j]);
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint64_t x = pack_f32x2(a[2 * k], a[2 * k + 1]), y = pack_f32x2(b[2 * k], b[2 * k + 1]);
-            turn2(x, y, t.c[k], t.s[k]);
-            unpack_f32x2(x, a[2 * k], a[2 * k + 1]);
-            unpack_f32x2(y, b[2 * k], b[2 * k + 1]);
+        for (int j = 0; j < 8; ++j) {
+            const float x = a[j], y = b[j];
+            a[j] = fmaf(x, c[j], -(y * s[j]));
+            b[j] = fmaf(y, c[j], x * s[j]);
         }
     }
 }
