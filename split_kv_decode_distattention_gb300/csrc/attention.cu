@@ -107,7 +107,7 @@ __device__ __forceinline__ int32_t head_tiles(int kind, int32_t L, const AttnPar
 }
 
 // Every segment (one KV head of one request or chunk) is laid out in "cost units": its real
-// 16-token tiles, then kSegCost units that stand for the fixed cost of a piece (fetching the
+// 16-token tiles, then seg_cost units that stand for the fixed cost of a piece (fetching the
 // query, merging the warps, handing over a partial). The balanced split cuts the cost space,
 // so a CTA whose range crosses many small segments gets fewer tiles. The extra units are
 // never loaded or scheduled: producer and consumers walk real tiles only.
@@ -120,7 +120,7 @@ __device__ __forceinline__ int32_t head_tiles(int kind, int32_t L, const AttnPar
 // its slots evenly: no CTA carries pieces of two retrieval segments, and every retrieval
 // segment is merged from exactly k pieces. The other G - n_r k CTAs take the streaming
 // segments, each whole. k follows the cost units of the balanced split (real tiles plus
-// kSegCost per segment), rounded to the nearest integer, but leaves every streaming segment
+// seg_cost per segment), rounded to the nearest integer, but leaves every streaming segment
 // a CTA of its own when the grid allows: their pieces are short and bound by latency, and a
 // CTA runs its pieces one after another.
 enum AplanIdx : int { AP_ON = 0, AP_K, AP_GR, AP_GS, AP_NRET, AP_NSTR, AP_R, AP_S };
@@ -143,7 +143,7 @@ __device__ void make_aligned_plan(const AttnParams& p, const Smem& sm, int32_t G
     bool on = ndense == 0 && p.T == 1 && (nr > 0 || ns > 0) && (nret == 0 || R > 0) &&
               (nstr == 0 || S > 0);
     if (on && nr > 0) {
-        const int64_t cr = R + kSegCost, cs = S + kSegCost;
+        const int64_t cr = R + p.seg_cost, cs = S + p.seg_cost;
         const int64_t W = nr * cr + ns * cs;
         k = (cr * G + W / 2) / W;
         k = min(max(k, (int64_t)1), (int64_t)R);
@@ -176,7 +176,10 @@ struct Plan {
     const Smem& sm;
     __device__ Plan(const AttnParams& p_, const Smem& sm_) : p(p_), sm(sm_) {}
 
-    __device__ static int32_t cost_of(int32_t real) { return real > 0 ? real + kSegCost : 0; }
+    __device__ int32_t cost_of(int32_t real) const { return cost_of(p, real); }
+    __device__ static int32_t cost_of(const AttnParams& p, int32_t real) {
+        return real > 0 ? real + p.seg_cost : 0;
+    }
 
     // Largest item i with item_start[i] <= t (t < W).
     __device__ int32_t item_of(int32_t t) const {
@@ -1378,17 +1381,17 @@ attention_kernel(const __grid_constant__ AttnParams p,
                     npg = 0;
                 }
                 ln[i] = npg * (p.P >> 4);  // real tiles per head
-                cnt = p.Hkv * Plan::cost_of(ln[i]);
+                cnt = p.Hkv * Plan::cost_of(p, ln[i]);
             } else {
                 const int32_t L = length_of(i);
                 ln[i] = L;
                 if (p.mode == MODE_SPARSE) {
                     const int32_t* kb = sm.kind_before() + 3 * p.Hkv;
-                    cnt = kb[0] * Plan::cost_of(head_tiles(DATTN_HEAD_DENSE, L, p)) +
-                          kb[1] * Plan::cost_of(head_tiles(DATTN_HEAD_RETRIEVAL, L, p)) +
-                          kb[2] * Plan::cost_of(head_tiles(DATTN_HEAD_STREAMING, L, p));
+                    cnt = kb[0] * Plan::cost_of(p, head_tiles(DATTN_HEAD_DENSE, L, p)) +
+                          kb[1] * Plan::cost_of(p, head_tiles(DATTN_HEAD_RETRIEVAL, L, p)) +
+                          kb[2] * Plan::cost_of(p, head_tiles(DATTN_HEAD_STREAMING, L, p));
                 } else {
-                    cnt = p.Hkv * Plan::cost_of(ceil16(L));
+                    cnt = p.Hkv * Plan::cost_of(p, ceil16(L));
                 }
             }
             local_sum += cnt;
