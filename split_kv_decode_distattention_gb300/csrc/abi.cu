@@ -377,11 +377,11 @@ dattn_status_t dattn_partial(const dattn_kv_layout* layout, const void* k_pool,
         return DATTN_ERR_INVALID_ARG;
     if (B == 0) return DATTN_ERR_INVALID_ARG;  // chunks must name a request
     if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(q)) return DATTN_ERR_INVALID_ARG;
-    AttnParams p{};
-    p.seg_cost = seg_cost(layout->kv_format, Hq / layout->num_kv_heads);
     const int64_t bound = (int64_t)C * layout->num_kv_heads *
-                          ((int64_t)layout->max_pages_per_req * (layout->page_size / 16) + p.seg_cost);
+                          ((int64_t)layout->max_pages_per_req * (layout->page_size / 16) +
+                           seg_cost(layout->kv_format, Hq / layout->num_kv_heads));
     if (bound >= (1ll << 31)) return DATTN_ERR_UNSUPPORTED;
+    AttnParams p{};
     p.mode = MODE_PARTIAL;
     p.num_pages = layout->num_pages;
     p.Hkv = layout->num_kv_heads;
@@ -503,8 +503,8 @@ dattn_status_t decode_impl(const dattn_kv_layout* layout, const void* k_pool, co
         if (retr > per_head) per_head = retr;
         if (strm > per_head) per_head = strm;
     }
-    p.seg_cost = seg_cost(layout->kv_format, Hq / layout->num_kv_heads * T);
-    const int64_t bound = (int64_t)B * layout->num_kv_heads * (per_head + p.seg_cost);
+    const int64_t bound = (int64_t)B * layout->num_kv_heads *
+                          (per_head + seg_cost(layout->kv_format, Hq / layout->num_kv_heads * T));
     if (bound >= (1ll << 31)) return DATTN_ERR_UNSUPPORTED;
     p.num_pages = layout->num_pages;
     p.Hkv = layout->num_kv_heads;

@@ -125,6 +125,7 @@ __device__ __forceinline__ int32_t head_tiles(int kind, int32_t L, const AttnPar
 // CTA runs its pieces one after another.
 enum AplanIdx : int { AP_ON = 0, AP_K, AP_GR, AP_GS, AP_NRET, AP_NSTR, AP_R, AP_S };
 
+template <int FMT>
 __device__ void make_aligned_plan(const AttnParams& p, const Smem& sm, int32_t G) {
     int32_t* a = sm.aplan();
     int32_t* ret = a + kAplanScalars;
@@ -143,7 +144,7 @@ __device__ void make_aligned_plan(const AttnParams& p, const Smem& sm, int32_t G
     bool on = ndense == 0 && p.T == 1 && (nr > 0 || ns > 0) && (nret == 0 || R > 0) &&
               (nstr == 0 || S > 0);
     if (on && nr > 0) {
-        const int64_t cr = R + p.seg_cost, cs = S + p.seg_cost;
+        const int64_t cr = R + seg_cost(FMT, p.gq), cs = S + seg_cost(FMT, p.gq);
         const int64_t W = nr * cr + ns * cs;
         k = (cr * G + W / 2) / W;
         k = min(max(k, (int64_t)1), (int64_t)R);
@@ -171,6 +172,7 @@ struct Piece {
 };
 
 // Segment geometry derived from the per-item prefix sums (in cost units) in shared memory.
+template <int FMT>
 struct Plan {
     const AttnParams& p;
     const Smem& sm;
@@ -178,7 +180,7 @@ struct Plan {
 
     __device__ int32_t cost_of(int32_t real) const { return cost_of(p, real); }
     __device__ static int32_t cost_of(const AttnParams& p, int32_t real) {
-        return real > 0 ? real + p.seg_cost : 0;
+        return real > 0 ? real + seg_cost(FMT, p.gq) : 0;
     }
 
     // Largest item i with item_start[i] <= t (t < W).
@@ -254,12 +256,13 @@ struct Plan {
 // the piece at the cursor, or false when there is none, and advance() moves past it.
 // The CTA's constants of its plan sit in shared memory (sm.cplan(): aligned, W, Gw, X0, X1),
 // so that they occupy no registers across the consumer loop.
+template <int FMT>
 struct PieceIter {
     const AttnParams& p;
     const Smem& sm;
-    const Plan& plan;
+    const Plan<FMT>& plan;
     int32_t cta;
-    __device__ PieceIter(const AttnParams& p_, const Smem& sm_, const Plan& pl, int32_t c)
+    __device__ PieceIter(const AttnParams& p_, const Smem& sm_, const Plan<FMT>& pl, int32_t c)
         : p(p_), sm(sm_), plan(pl), cta(c) {}
 
     __device__ bool aligned() const { return sm.cplan()[0] != 0; }
@@ -337,6 +340,7 @@ __device__ __forceinline__ int32_t tile_patch_row(int32_t m) { return (m >> 18) 
 // Tile `local` of segment s. `aligned`: the head-aligned plan's fixed slot layout (streaming
 // segments: ceil(sinks/16) sink slots, then the local-window slots; retrieval segments have
 // slots even when the length is 0).
+template <int FMT>
 __device__ __forceinline__ TileRef resolve_tile(const AttnParams& p, const Smem& sm, int32_t s,
                                                 int32_t local, bool aligned) {
     TileRef r{0, kTileSkip, 0};
@@ -415,7 +419,7 @@ __device__ __forceinline__ TileRef resolve_tile(const AttnParams& p, const Smem&
     }
     r.y = (page * p.Hkv + h) * p.P + (t0 - lp * p.P);
     r.lohi = lo | (hi << 8) | ((cut + 16) << 24);
-    if (p.fmt == DATTN_KV_FP8_BLOCK && ((r.y >> 4) & 1)) r.lohi |= kTileOdd;
+    if (FMT == DATTN_KV_FP8_BLOCK && ((r.y >> 4) & 1)) r.lohi |= kTileOdd;
     if (p.fmt == DATTN_KV_MIXED) {
         const bool i4 = head_is_i4(p.hf, h);
         const int32_t hc = i4 ? p.hf.h4 : p.Hkv - p.hf.h4;
@@ -430,17 +434,28 @@ __device__ __forceinline__ TileRef resolve_tile(const AttnParams& p, const Smem&
     return r;
 }
 
-// Writes the final result of column c of segment s: query token t = c / g of query head
-// kvh*g + c % g. MA is unnormalised; m is in log2 units.
+// Writes four channels d .. d + 3 of the final result of column c of segment s: query token
+// t = c / g of query head kvh*g + c % g. MA is unnormalised; m is in log2 units.
 __device__ __forceinline__ void write_final(const AttnParams& p, int32_t s, int32_t c, int32_t d,
-                                            int D, float m, float e, float ma) {
+                                            int D, float m, float e, float4 ma) {
     const int32_t item = s / p.Hkv, kvh = s - item * p.Hkv;
     const int32_t t = c / p.g, j = c - t * p.g;
     const int64_t row = ((int64_t)item * p.T + t) * p.Hq + kvh * p.g + j;
-    if (p.mode == MODE_PARTIAL) {
-        p.out[row * D + d] = ma;
+    if (p.mode != MODE_PARTIAL) {
+        const bool some = e > 0.f;
+        ma.x = some ? ma.x / e : 0.f;
+        ma.y = some ? ma.y / e : 0.f;
+        ma.z = some ? ma.z / e : 0.f;
+        ma.w = some ? ma.w / e : 0.f;
+    }
+    float* out = p.out + row * D + d;
+    if ((reinterpret_cast<uintptr_t>(p.out) & 15) == 0) {
+        *reinterpret_cast<float4*>(out) = ma;
     } else {
-        p.out[row * D + d] = e > 0.f ? ma / e : 0.f;
+        out[0] = ma.x;
+        out[1] = ma.y;
+        out[2] = ma.z;
+        out[3] = ma.w;
     }
     if (d == 0) {
         if (p.m_out) p.m_out[row] = m == kNegInf ? kNegInf : m * kLn2;
@@ -1314,7 +1329,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
             }
             int32_t* kb = sm.kind_before() + 3 * p.Hkv;
             kb[0] = c0; kb[1] = c1; kb[2] = c2;
-            make_aligned_plan(p, sm, G);
+            make_aligned_plan<FMT>(p, sm, G);
         }
     }
     {  // warm L2 with the metadata read right after the wait (each line by one thread)
@@ -1381,17 +1396,17 @@ attention_kernel(const __grid_constant__ AttnParams p,
                     npg = 0;
                 }
                 ln[i] = npg * (p.P >> 4);  // real tiles per head
-                cnt = p.Hkv * Plan::cost_of(p, ln[i]);
+                cnt = p.Hkv * Plan<FMT>::cost_of(p, ln[i]);
             } else {
                 const int32_t L = length_of(i);
                 ln[i] = L;
                 if (p.mode == MODE_SPARSE) {
                     const int32_t* kb = sm.kind_before() + 3 * p.Hkv;
-                    cnt = kb[0] * Plan::cost_of(p, head_tiles(DATTN_HEAD_DENSE, L, p)) +
-                          kb[1] * Plan::cost_of(p, head_tiles(DATTN_HEAD_RETRIEVAL, L, p)) +
-                          kb[2] * Plan::cost_of(p, head_tiles(DATTN_HEAD_STREAMING, L, p));
+                    cnt = kb[0] * Plan<FMT>::cost_of(p, head_tiles(DATTN_HEAD_DENSE, L, p)) +
+                          kb[1] * Plan<FMT>::cost_of(p, head_tiles(DATTN_HEAD_RETRIEVAL, L, p)) +
+                          kb[2] * Plan<FMT>::cost_of(p, head_tiles(DATTN_HEAD_STREAMING, L, p));
                 } else {
-                    cnt = p.Hkv * Plan::cost_of(p, ceil16(L));
+                    cnt = p.Hkv * Plan<FMT>::cost_of(p, ceil16(L));
                 }
             }
             local_sum += cnt;
@@ -1420,7 +1435,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
         }
         __syncthreads();
     }
-    const Plan plan(p, sm);
+    const Plan<FMT> plan(p, sm);
     int32_t W = 0, Gw = 1, X0 = 0, X1 = 0;
     if (!aligned) {
         W = sm.item_start()[p.nitems];
@@ -1436,8 +1451,9 @@ attention_kernel(const __grid_constant__ AttnParams p,
             int32_t st, real, cost;
             plan.seg_span(s, st, real, cost);
             if (real == 0) {
-                for (int idx = tid; idx < p.gq * D; idx += kAttnThreads)
-                    write_final(p, s, idx / D, idx % D, D, kNegInf, 0.f, 0.f);
+                for (int idx = 4 * tid; idx < p.gq * D; idx += 4 * kAttnThreads)
+                    write_final(p, s, idx / D, idx % D, D, kNegInf, 0.f,
+                                make_float4(0.f, 0.f, 0.f, 0.f));
             }
         }
     }
@@ -1450,7 +1466,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
         cp[4] = X1;
     }
     __syncthreads();
-    const PieceIter pieces(p, sm, plan, cta);
+    const PieceIter<FMT> pieces(p, sm, plan, cta);
     int32_t cur0 = pieces.start();
     Piece first;
     const bool any = pieces.piece(cur0, first);
@@ -1551,7 +1567,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
                     }
                 }
                 TileRef ref{0, kTileSkip, 0};
-                if (my_s >= 0) ref = resolve_tile(p, sm, my_s, my_local, pieces.aligned());
+                if (my_s >= 0) ref = resolve_tile<FMT>(p, sm, my_s, my_local, pieces.aligned());
                 stop = !issue(ref, nb);
             }
         }
@@ -1715,10 +1731,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
                 }
             }
             if (whole) {
-                write_final(p, s, j, d, D, mc, ec, ma.x);
-                write_final(p, s, j, d + 1, D, mc, ec, ma.y);
-                write_final(p, s, j, d + 2, D, mc, ec, ma.z);
-                write_final(p, s, j, d + 3, D, mc, ec, ma.w);
+                write_final(p, s, j, d, D, mc, ec, ma);
             } else {
                 *reinterpret_cast<float4*>(my_slot + 4 * c4) = ma;
                 if (d == 0) {
@@ -1784,10 +1797,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
                         }
                         mrun = mx;
                     }
-                    write_final(p, s, j, d, D, mrun, erun, acc.x);
-                    write_final(p, s, j, d + 1, D, mrun, erun, acc.y);
-                    write_final(p, s, j, d + 2, D, mrun, erun, acc.z);
-                    write_final(p, s, j, d + 3, D, mrun, erun, acc.w);
+                    write_final(p, s, j, d, D, mrun, erun, acc);
                 }
             }
         }

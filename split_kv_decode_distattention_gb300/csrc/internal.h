@@ -50,7 +50,7 @@ constexpr int kMaxCtasPerSm = 4;    // bound used for workspace sizing with auto
 // tokens, 8 KV heads: 60.5 us with 6, 54.5 with 12, 52.9 with 18, 54.9 with 28 for gq = 4; 70.6, 63.0,
 // 58.7 and 58.5 us for gq = 8; 16 requests of 1000-20000 tokens, 32 KV heads, gq = 1: 138.6, 132.7,
 // 131.8 and 133.0 us. The other formats keep 6, and with it the order of their sums.
-constexpr int32_t seg_cost(int32_t fmt, int32_t gq) {
+__host__ __device__ constexpr int32_t seg_cost(int32_t fmt, int32_t gq) {
     return fmt == DATTN_KV_FP8_BLOCK ? 12 + 2 * gq : 6;
 }
 
@@ -97,7 +97,6 @@ struct AttnParams {
     // query tokens per request (1 = decode; T > 1: multi-query decode, causal over the T
     // newest tokens) and the columns of a segment's tile, gq = g * T <= 8
     int32_t T, gq;
-    int32_t seg_cost;  // of the format and gq
     float sl2;  // scale * log2(e)
     const int32_t* seq_lens;
     // dattn_partial
