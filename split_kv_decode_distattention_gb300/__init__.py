@@ -169,7 +169,12 @@ def _stream(stream):
     the raw getter: building a Stream object costs about as much as the launch)."""
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return _stream_on(None, torch.cuda.current_device())
+
+
+def _stream_on(stream, device):
+    return stream.cuda_stream if stream is not None else \
+        torch._C._cuda_getCurrentRawStream(device)
 
 
 def _bf16(t, name):
@@ -229,10 +234,8 @@ def _layout_sizes(layout, B: int, k_pool, v_pool, stats=None):
 def _pool(layout, t, name):
     """A K or V pool must hold the layout's element type: bf16, uint8 E4M3 codes, or uint8
     bytes of two 4-bit codes (the mixed pool: both kinds of bytes)."""
-    want = torch.uint8 if layout.kv_format in _QUANT else torch.bfloat16
-    if t is not None and t.dtype != want and not (
-            want == torch.uint8 and t.dtype == getattr(torch, "float8_e4m3fn", None)):
-        raise TypeError(f"{name} must be {want} for this layout")
+    if t is not None and t.dtype not in layout.pool_types:
+        raise TypeError(f"{name} must be {layout.pool_types[0]} for this layout")
     return t
 
 
@@ -273,6 +276,8 @@ class KVLayout:
                          kv_scale.data_ptr() if kv_scale is not None else None,
                          ctypes.addressof(self._head_format_c)
                          if self._head_format_c is not None else None)
+        self.pool_types = (torch.uint8, getattr(torch, "float8_e4m3fn", torch.uint8)) \
+            if kv_format in _QUANT else (torch.bfloat16,)
         # elements of a pool, floats of kv_scale, elements of the statistics, block-table row width
         n = num_pages * num_kv_heads * page_size
         if kv_format == KV_MIXED:
@@ -433,9 +438,10 @@ def dattn_kv_append(layout: KVLayout, k_pool, v_pool, stats, k_new, v_new, seq_l
         _ptr(v_new), B, T, _ptr(seq_lens), _ptr(dev_err), _stream(stream)), "dattn_kv_append")
 
 
-def _tokens(t, name):
+def _tokens(t, name, here=None):
     """A [tokens...][H][d] tensor whose heads are packed and whose tokens are evenly spaced (a
-    contiguous tensor or a slice of a fused projection): (pointer, elements between tokens)."""
+    contiguous tensor or a slice of a fused projection), on device `here` where that is given:
+    (pointer, elements between tokens)."""
     size, step = t.shape, t.stride()
     dims = len(size)
     if dims != 3 and dims != 4:
@@ -450,17 +456,37 @@ def _tokens(t, name):
         many, stride = B > 1 or T > 1, step[0] if T == 1 else step[1]
         if B > 1 and T > 1 and step[0] != T * stride:
             raise ValueError(f"the tokens of {name} must be evenly spaced")
-    if t.get_device() < 0:
-        raise ValueError("expected a CUDA tensor")
+    device = t.get_device()
+    if device < 0 or (here is not None and device != here):
+        _elsewhere(t, here)
     return t.data_ptr(), stride if many else H * d
 
 
-def _same_device(*tensors):
-    """The launch goes to the current device: every tensor must live there."""
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() not in (here, -1):  # -1, the CPU: refused by _ptr
-            raise ValueError(f"a tensor of {t.device} in a call on cuda:{here}")
+def _elsewhere(t, here):
+    if t.get_device() < 0:
+        raise ValueError("expected a CUDA tensor")
+    raise ValueError(f"tensors of {t.device} and cuda:{here} in one call")
+
+
+def _at(t, here):
+    """The pointer of a contiguous tensor on device `here`."""
+    if t is None:
+        return None
+    if t.get_device() != here:
+        _elsewhere(t, here)
+    if not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _launch_device(t):
+    """The device of t, which has to be the current one: the launch goes there."""
+    here = t.get_device()
+    if here < 0:
+        raise ValueError("expected a CUDA tensor")
+    if here != torch.cuda.current_device():
+        raise ValueError(f"a tensor of {t.device} in a call on cuda:{torch.cuda.current_device()}")
+    return here
 
 
 def dattn_rope(rotation: Rotation, x, out, positions, inverse: bool = False, stream=None):
@@ -474,15 +500,16 @@ def dattn_rope(rotation: Rotation, x, out, positions, inverse: bool = False, str
     if out.shape != size:
         raise ValueError("out must have the shape of x")
     _i32(positions, "positions")
-    xp, xs = _tokens(x, "x")
-    op, os_ = _tokens(out, "out")
+    here = x.get_device()
+    xp, xs = _tokens(x, "x", here)
+    op, os_ = _tokens(out, "out", here)
     H, d = size[-2], size[-1]
     N = size[0] if len(size) == 3 else size[0] * size[1]
     _size(positions, N, "positions")
-    _same_device(x, out, positions)
+    _launch_device(x)
     _check(load_library().dattn_rope(
-        ctypes.byref(rotation.c), xp, xs, op, os_, N, H, d, f32, _ptr(positions), bool(inverse),
-        _stream(stream)), "dattn_rope")
+        ctypes.byref(rotation.c), xp, xs, op, os_, N, H, d, f32, _at(positions, here),
+        bool(inverse), _stream_on(stream, here)), "dattn_rope")
 
 
 def dattn_rope_append(layout: KVLayout, k_pool, v_pool, stats, rotation: Rotation | None, q, k_new,
@@ -510,21 +537,22 @@ def dattn_rope_append(layout: KVLayout, k_pool, v_pool, stats, rotation: Rotatio
             raise ValueError("q must be bf16 [B][T][Hq][d]")
         Hq = qsize[2]
         _size(q_out, B * T * Hq * d, "q_out")
-        qp, qs = _tokens(q, "q")
     elif q_out is not None:
         raise ValueError("q and q_out come together")
     _layout_sizes(layout, B, k_pool, v_pool, stats)
     _size(seq_lens, B, "seq_lens"); _size(new_lens, B, "new_lens")
     _size(positions, B * T, "positions")
-    _same_device(k_pool, v_pool, stats, q, k_new, v_new, q_out, seq_lens, positions, new_lens,
-                 layout.block_table, layout.kv_scale, dev_err)
-    kp, ks = _tokens(k_new, "k_new")
-    vp, vs = _tokens(v_new, "v_new")
+    here = _launch_device(k_new)
+    if q is not None:
+        qp, qs = _tokens(q, "q", here)
+    kp, ks = _tokens(k_new, "k_new", here)
+    vp, vs = _tokens(v_new, "v_new", here)
+    _at(layout.block_table, here); _at(layout.kv_scale, here)
     _check(load_library().dattn_rope_append(
-        ctypes.byref(layout.c), _ptr(k_pool), _ptr(v_pool), _ptr(stats),
+        ctypes.byref(layout.c), _at(k_pool, here), _at(v_pool, here), _at(stats, here),
         ctypes.byref(rotation.c) if rotation is not None else None, qp, qs, kp, ks, vp, vs, B, T,
-        Hq, _ptr(q_out), _ptr(seq_lens), _ptr(positions), _ptr(new_lens), bool(advance),
-        _ptr(dev_err), _stream(stream)), "dattn_rope_append")
+        Hq, _at(q_out, here), _at(seq_lens, here), _at(positions, here), _at(new_lens, here),
+        bool(advance), _at(dev_err, here), _stream_on(stream, here)), "dattn_rope_append")
 
 
 def dattn_partial(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_lens, chunk_req,
