@@ -24,7 +24,11 @@
 // A CTA: 256 rows as four quarters of 64 tokens: one query block of four heads of a KV head (g a
 // multiple of 4), two query blocks of two heads (even g), or four query blocks of one head. A tile
 // (two quarters) takes part in a key block only if one of its quarters keeps it. Where the last
-// wave of CTAs would fill less than half of the SMs, its tiles get a CTA each. 15 warps:
+// wave of CTAs would fill less than half of the SMs, its tiles get a CTA each. A chunk of few tiles
+// (its blocks run one after another, 0.8-1.1 us each) gives each tile a cluster of up to eight CTAs,
+// which share its key blocks and join their sums through shared memory: 64 tokens of 32 heads over 8
+// KV heads of 128 after 32K tokens 562 -> 143 us (clusters of 4), 64 of 8 heads over one KV head after
+// 100K tokens 1597 -> 211 us (8), 39 of 16 heads after 1284 21.4 -> 16.4 us. 15 warps:
 //   0-3, 4-7  one query row per thread of tile 0, 1: the softmax. (Two threads per row took 11% longer:
 //             the second's share of the fixed work costs more than its latency saves.)
 //   8-11      load codes, widen them and write the K and V stages in the 128-byte-swizzled layout
@@ -34,6 +38,7 @@
 //   14        walks the key blocks, eight at a time, one lane per 16-key tile, and leaves each
 //             block's place, lengths and scales in a ring in shared memory for the others.
 // Tensor memory: O of the two tiles, then two score buffers for each, all 512 columns.
+#include <atomic>
 #include <mutex>
 
 #include "common.cuh"
@@ -56,6 +61,8 @@ constexpr int kPbRing = 2 * kPbGroup;       // the blocks' ring
 // Key blocks between two emptyings of an accumulator: 256 products that each lose up to 2^-24 of the
 // sum, 4.4e-6 of the result measured. (16: 2.2e-6 for 11% more time on a 32K prompt.)
 constexpr int kPbWindow = 32;
+constexpr int kPbSplitBlocks = 3;           // key blocks of a CTA at least, where a cluster shares
+                                            // a tile (2 cost more where it would, 4 gave 2 us less)
 constexpr uint32_t kPbCols = 512;           // O: [0, 128), [128, 256); S: 256 + 128 tile + 64 buffer
 
 // mbarriers
@@ -104,6 +111,7 @@ struct PbParams {
     PfParams f;
     int32_t hp, nq;    // heads and query blocks of a CTA: hp * nq = 4
     int32_t whole;     // CTAs of two tiles; the others hold one tile each
+    int32_t split;     // CTAs of a cluster, which share a tile's key blocks (1: no cluster)
     const uint8_t* k_pool;
     const uint8_t* v_pool;
     const float2* scale;  // [num_pages][Hkv][P/16] (K, V)
@@ -189,7 +197,9 @@ __device__ __forceinline__ float max16(const float* x) {
 }
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) << 23); }
 
-template <int D>
+// SPLIT: a cluster of pp.split CTAs holds one tile, each CTA a run of its key blocks; their sums and
+// maxima meet in shared memory.
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kPbThreads, 1)
 prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
     constexpr uint32_t kHalf = 64u * 128u;  // a 128-byte half of a key block's rows
@@ -208,9 +218,11 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
     const int hp = pp.hp, nq = pp.nq;
     const int32_t spk = p.g / hp;
     const int32_t ngrp = p.Hkv / p.kv_group;
-    const int32_t extra = max((int32_t)blockIdx.x - pp.whole, 0);
-    const uint32_t tmask = (int32_t)blockIdx.x < pp.whole ? 3u : 1u << (extra & 1);
-    int32_t c = (int32_t)blockIdx.x < pp.whole ? (int32_t)blockIdx.x : pp.whole + (extra >> 1);
+    const int32_t cta = SPLIT ? (int32_t)blockIdx.x / pp.split : (int32_t)blockIdx.x;
+    const int32_t rank = SPLIT ? (int32_t)cluster_rank() : 0;
+    const int32_t extra = max(cta - pp.whole, 0);
+    const uint32_t tmask = cta < pp.whole ? 3u : 1u << (extra & 1);
+    int32_t c = cta < pp.whole ? cta : pp.whole + (extra >> 1);
     const int32_t sk = c % spk;
     c /= spk;
     const int32_t hg = c % p.kv_group;
@@ -224,6 +236,11 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
     auto bar = [&](int i) { return bars + 8u * i; };
     PbBlock* ring = reinterpret_cast<PbBlock*>(base + L.ring);
     uint32_t* bm = reinterpret_cast<uint32_t*>(base + L.bm);
+    // SPLIT: the tile's sums (rows of D + 4 floats, for the banks) and (m_used, rexp, l, m_true) of its
+    // rows, where the K and V stages were
+    float* part = reinterpret_cast<float*>(base + L.kst);
+    float4* stat = reinterpret_cast<float4*>(part + 128 * (D + 4));
+    static_assert(128 * (D + 4) * 4 + 128 * 16 <= 2 * kPbStages * 64 * D * 2, "the parts' place");
     float* qscale = reinterpret_cast<float*>(base + L.qscale);
     volatile int* abort_p = reinterpret_cast<volatile int*>(base + L.abort);
     if (tid == 0) {
@@ -261,7 +278,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
     // ---- the CTA's query rows and key blocks (uniform over the CTA) ---------------------------
     const int32_t Ln = p.seq_lens[b];
     bool active = Ln >= p.Tq && Ln <= p.max_pages * p.P;
-    if (!active && tid == 0 && h0 == 0 && J == 0) set_err(p.dev_err, DATTN_DEVERR_LEN_OOB);
+    if (!active && tid == 0 && h0 == 0 && J == 0 && rank == 0) set_err(p.dev_err, DATTN_DEVERR_LEN_OOB);
     const int32_t c0 = Ln - p.Tq;
     const int32_t qa = (active ? c0 : 0) / kPfBlock + J * nq;  // the first query block
     int kind = p.head_kind ? p.head_kind[kvh] : DATTN_HEAD_DENSE;
@@ -348,6 +365,14 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
         uint32_t q[4];
         n += __popc(held_word(bm, nq, nwords, tmask, w, q));
     }
+    // the CTA's run of them: [first, first + n)
+    int32_t first_block = 0, use = 1;
+    if constexpr (SPLIT) {
+        use = max(1, min(pp.split, n / kPbSplitBlocks));
+        const int32_t all = n;
+        first_block = rank < use ? all * rank / use : all;
+        n = rank < use ? all * (rank + 1) / use - first_block : 0;
+    }
     // The ring: block i in slot i % 16, ready with its group of eight; a reader's warp gives a group
     // back after its last block.
     auto wait = [&](uint32_t bar_addr, uint32_t parity) {  // by a whole warp, one answer
@@ -368,6 +393,14 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
         const int blk = lane >> 2, u = lane & 3;  // this lane: tile u of the group's block blk
         int32_t w = 0;
         uint32_t q[4], word = held_word(bm, nq, nwords, tmask, 0, q);
+        if constexpr (SPLIT) {  // past the blocks of the CTAs before
+            int32_t skip = first_block;
+            while (n > 0 && skip >= __popc(word)) {  // (n > 0: more than skip blocks in all)
+                skip -= __popc(word);
+                word = held_word(bm, nq, nwords, tmask, ++w, q);
+            }
+            for (; n > 0 && skip > 0; --skip) word &= word - 1u;
+        }
         int r = -126;
         bool ok = true;
         for (int32_t i = 0; i < n && ok; i += kPbGroup) {
@@ -583,6 +616,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
         const int t = warp >> 2, r = tid, z = r >> 6;  // tile, row and quarter
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ocol = tbase + lanes + 128u * t;
+        const uint32_t ecol = tbase + lanes + 128u * (t ^ 1);  // SPLIT: the sums of earlier windows
         const int qi = q_block(z);
         const int32_t pos = (qa + qi) * kPfBlock + (r & 63);
         const bool rowok = ((has >> qi) & 1u) && ((tmask >> t) & 1u) && pos >= c0 && pos < Ln;
@@ -629,41 +663,69 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                 // one phase behind, which its parity can tell.)
                 mbar_wait(bar(kBarPv + t), (j - 1) & 1, abort_p, p.dev_err);
                 tc_fence_after();
-                const bool some = rowok && m_used != kPfNegInf;
                 const float at = m_used + (float)rexp;
-                const bool first = some && ref == kPfNegInf;
-                // far above the row's reference, what it holds moves to the new one first
-                const bool move = some && !first && at > ref + 60.f;
-                const float down = move ? exp2f(ref - at) : 1.f;
-                if (first || move) ref = at;
-                const float f = some ? exp2f(at - ref) : 0.f;
+                if constexpr (SPLIT) {
+                    // (to the other tile's columns, which this CTA does not use: the output row is
+                    // the cluster's)
+                    const float down = ref == kPfNegInf ? 0.f : exp2f(ref - at);
+                    ref = at;
 #pragma unroll 1
-                for (int cc = 0; cc < D / 16; ++cc) {
-                    float v[16];
-                    tc_ld16(ocol + 16u * cc, v);
-                    tc_wait_ld();
-                    float* to = orow + 16 * cc;
-                    if (move) {
-                        __threadfence();
+                    for (int cc = 0; cc < D / 16; ++cc) {
+                        float v[16];
+                        tc_ld16(ocol + 16u * cc, v);
+                        tc_wait_ld();
+                        uint32_t o[16];
+                        if (j > kPbWindow) {
+                            float e16[16];
+                            tc_ld16(ecol + 16u * cc, e16);
+                            tc_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            const float4 o = __ldcg(reinterpret_cast<const float4*>(to + e));
-                            *reinterpret_cast<float4*>(to + e) =
-                                make_float4(fmaf(o.x, down, v[e]), fmaf(o.y, down, v[e + 1]),
-                                            fmaf(o.z, down, v[e + 2]), fmaf(o.w, down, v[e + 3]));
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(fmaf(e16[e], down, v[e]));
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(v[e]);
                         }
-                    } else if (first) {
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4)
-                            *reinterpret_cast<float4*>(to + e) =
-                                make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-                    } else if (some) {
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4)
-                            red_add4(to + e, v[e] * f, v[e + 1] * f, v[e + 2] * f, v[e + 3] * f);
+                        tc_st16(ecol + 16u * cc, o);
                     }
+                    tc_wait_st();
+                    tc_fence_before();
+                } else {
+                    const bool some = rowok && m_used != kPfNegInf;
+                    const bool first = some && ref == kPfNegInf;
+                    // far above the row's reference, what it holds moves to the new one first
+                    const bool move = some && !first && at > ref + 60.f;
+                    const float down = move ? exp2f(ref - at) : 1.f;
+                    if (first || move) ref = at;
+                    const float f = some ? exp2f(at - ref) : 0.f;
+#pragma unroll 1
+                    for (int cc = 0; cc < D / 16; ++cc) {
+                        float v[16];
+                        tc_ld16(ocol + 16u * cc, v);
+                        tc_wait_ld();
+                        float* to = orow + 16 * cc;
+                        if (move) {
+                            __threadfence();
+#pragma unroll
+                            for (int e = 0; e < 16; e += 4) {
+                                const float4 o = __ldcg(reinterpret_cast<const float4*>(to + e));
+                                *reinterpret_cast<float4*>(to + e) =
+                                    make_float4(fmaf(o.x, down, v[e]), fmaf(o.y, down, v[e + 1]),
+                                                fmaf(o.z, down, v[e + 2]), fmaf(o.w, down, v[e + 3]));
+                            }
+                        } else if (first) {
+#pragma unroll
+                            for (int e = 0; e < 16; e += 4)
+                                *reinterpret_cast<float4*>(to + e) =
+                                    make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                        } else if (some) {
+#pragma unroll
+                            for (int e = 0; e < 16; e += 4)
+                                red_add4(to + e, v[e] * f, v[e + 1] * f, v[e + 2] * f, v[e + 3] * f);
+                        }
+                    }
+                    tc_fence_before();
                 }
-                tc_fence_before();
             }
             const uint32_t sbuf = tbase + lanes + 256u + 128u * t + 64u * buf;
             float x[64];
@@ -762,44 +824,123 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
         }
         ok = __all_sync(0xffffffffu, ok);
         const bool any = j > 0 && ok;
-        // out = (O + earlier windows) 2^rexp / l, the exponent and 1 / l multiplied in turn (either
-        // may be far from 1)
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const float up = pow2i(rexp);
-        const bool more = ref != kPfNegInf && ok;
-        const float down = more ? exp2f(ref - (m_used + (float)rexp)) : 0.f;
-        if (more) __threadfence();  // the row's earlier additions
+        if (SPLIT && use > 1) {
+            // the row's sum, relative to 2^(m_used + rexp), and what it is relative to
+            if ((tmask >> t) & 1u) {
+                const bool more = j > kPbWindow;  // (at a multiple of it the last window is still in O)
+                const float down =
+                    more && ref != kPfNegInf ? exp2f(ref - (m_used + (float)rexp)) : 0.f;
+                float* to = part + (r & 127) * (D + 4);
 #pragma unroll 1
-        for (int cc = 0; cc < D / 16; ++cc) {
-            float v[16];
-            if (any) {
-                tc_ld16(ocol + 16u * cc, v);
-                tc_wait_ld();
-            } else {
+                for (int cc = 0; cc < D / 16; ++cc) {
+                    float v[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = 0.f;
-            }
-            if (rowok) {
-                float* to = orow + 16 * cc;
+                    for (int e = 0; e < 16; ++e) v[e] = 0.f;
+                    if (any) {
+                        tc_ld16(ocol + 16u * cc, v);
+                        tc_wait_ld();
+                        if (more) {
+                            float e16[16];
+                            tc_ld16(ecol + 16u * cc, e16);
+                            tc_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                    float4 o = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-                    if (more) {
-                        const float4 a = __ldcg(reinterpret_cast<const float4*>(to + e));
-                        o.x = fmaf(a.x, down, o.x);
-                        o.y = fmaf(a.y, down, o.y);
-                        o.z = fmaf(a.z, down, o.z);
-                        o.w = fmaf(a.w, down, o.w);
+                            for (int e = 0; e < 16; ++e) v[e] = fmaf(e16[e], down, v[e]);
+                        }
                     }
-                    *reinterpret_cast<float4*>(to + e) =
-                        make_float4(o.x * inv * up, o.y * inv * up, o.z * inv * up, o.w * inv * up);
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4)
+                        *reinterpret_cast<float4*>(to + 16 * cc + e) =
+                            make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                }
+                stat[r & 127] = make_float4(m_used, (float)rexp, l, m_true);
+            }
+        } else if (!SPLIT || rank == 0) {
+            // out = (O + earlier windows) 2^rexp / l, the exponent and 1 / l multiplied in turn (either
+            // may be far from 1)
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float up = pow2i(rexp);
+            const bool more = !SPLIT && ref != kPfNegInf && ok;  // (SPLIT: fewer blocks than a window)
+            const float down = more ? exp2f(ref - (m_used + (float)rexp)) : 0.f;
+            if (more) __threadfence();  // the row's earlier additions
+#pragma unroll 1
+            for (int cc = 0; cc < D / 16; ++cc) {
+                float v[16];
+                if (any) {
+                    tc_ld16(ocol + 16u * cc, v);
+                    tc_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = 0.f;
+                }
+                if (rowok) {
+                    float* to = orow + 16 * cc;
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) {
+                        float4 o = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                        if (more) {
+                            const float4 a = __ldcg(reinterpret_cast<const float4*>(to + e));
+                            o.x = fmaf(a.x, down, o.x);
+                            o.y = fmaf(a.y, down, o.y);
+                            o.z = fmaf(a.z, down, o.z);
+                            o.w = fmaf(a.w, down, o.w);
+                        }
+                        *reinterpret_cast<float4*>(to + e) =
+                            make_float4(o.x * inv * up, o.y * inv * up, o.z * inv * up, o.w * inv * up);
+                    }
                 }
             }
+            if (rowok) {
+                // report the true row max and the sum relative to it
+                if (p.m_out) p.m_out[row] = m_true == kPfNegInf ? kPfNegInf : m_true * kLn2;
+                if (p.e_out) p.e_out[row] = m_true == kPfNegInf ? 0.f : l * exp2f(m_used - m_true);
+            }
         }
-        if (rowok) {
-            // report the true row max and the sum relative to it
-            if (p.m_out) p.m_out[row] = m_true == kPfNegInf ? kPfNegInf : m_true * kLn2;
-            if (p.e_out) p.e_out[row] = m_true == kPfNegInf ? 0.f : l * exp2f(m_used - m_true);
+    }
+    if constexpr (SPLIT) {
+        if (use > 1) {  // (one answer in the whole cluster)
+            // ---- the rows' parts meet: each CTA of the cluster joins its share of the 128 rows ----
+            __syncthreads();
+            cluster_arrive();
+            cluster_wait();
+            const int t = tmask >> 1;  // the CTA's tile
+            const int rows = 128 / pp.split;
+            for (int x = tid; x < rows * (D / 4); x += kPbThreads) {
+                const int rl = rank * rows + x / (D / 4), c4 = x % (D / 4);
+                const int r = 128 * t + rl, z = r >> 6, qi = q_block(z);
+                const int32_t pos = (qa + qi) * kPfBlock + (r & 63);
+                if (!(((has >> qi) & 1u) && pos >= c0 && pos < Ln)) continue;
+                float m = kPfNegInf, top = kPfNegInf;  // the row's maximum; the parts' largest exponent
+                for (int y = 0; y < use; ++y) {
+                    const float4 st = ld_cluster4(smem_u32(stat + rl), y);
+                    m = fmaxf(m, st.w);
+                    if (st.x != kPfNegInf) top = fmaxf(top, st.x + st.y);
+                }
+                float l = 0.f;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int y = 0; y < use && m != kPfNegInf; ++y) {
+                    const float4 st = ld_cluster4(smem_u32(stat + rl), y);
+                    if (st.x == kPfNegInf) continue;
+                    const float4 v = ld_cluster4(smem_u32(part + rl * (D + 4) + 4 * c4), y);
+                    const float f = exp2f(st.x + st.y - top);
+                    l = fmaf(st.z, exp2f(st.x - m), l);
+                    o.x = fmaf(v.x, f, o.x);
+                    o.y = fmaf(v.y, f, o.y);
+                    o.z = fmaf(v.z, f, o.z);
+                    o.w = fmaf(v.w, f, o.w);
+                }
+                // out = sum 2^top / (l 2^m), in turns as above
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const float up = m == kPfNegInf ? 0.f : exp2f(top - m);
+                const int64_t row = ((int64_t)b * p.Tq + (pos - c0)) * p.Hq + h0 + q_head(z);
+                *reinterpret_cast<float4*>(p.out + row * D + 4 * c4) =
+                    make_float4(o.x * inv * up, o.y * inv * up, o.z * inv * up, o.w * inv * up);
+                if (c4 == 0) {
+                    if (p.m_out) p.m_out[row] = m == kPfNegInf ? kPfNegInf : m * kLn2;
+                    if (p.e_out) p.e_out[row] = l;
+                }
+            }
+            cluster_arrive();  // no CTA leaves while another reads its parts
+            cluster_wait();
         }
     }
     // ---- teardown: the allocating warp frees the tensor memory --------------------------------
@@ -812,7 +953,48 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
 }
 
 std::mutex g_pb_mutex;
-int g_pb_smem_set[2][kMaxDevices] = {};  // a function attribute belongs to a device
+
+template <int D, bool SPLIT>
+dattn_status_t ensure_smem(uint32_t bytes) {
+    static int set[kMaxDevices] = {};  // a function attribute belongs to a device
+    std::lock_guard<std::mutex> lock(g_pb_mutex);
+    int& mine = set[device_index()];
+    if ((int)bytes > mine) {
+        if (cudaFuncSetAttribute(prefill_block_kernel<D, SPLIT>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)bytes) != cudaSuccess)
+            return DATTN_ERR_CUDA;
+        mine = (int)bytes;
+    }
+    return DATTN_OK;
+}
+
+// Clusters of s CTAs that the device holds at once (15 of 8, 36 of 4 and 76 of 2 on 152 SMs, one CTA
+// per SM whatever its shared memory); asked once per device and size.
+template <int D>
+int32_t clusters_at_once(int32_t s, uint32_t bytes) {
+    static std::atomic<int32_t> known[kMaxDevices][9] = {};
+    std::atomic<int32_t>& mine = known[device_index()][s];
+    int32_t n = mine.load(std::memory_order_relaxed);
+    if (n > 0) return n - 1;
+    if (ensure_smem<D, true>(bytes) != DATTN_OK) return 0;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)s);
+    cfg.blockDim = dim3(kPbThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cudaLaunchAttribute attr[1]{};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)s, 1u, 1u};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int at_once = 0;
+    if (cudaOccupancyMaxActiveClusters(&at_once, prefill_block_kernel<D, true>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        at_once = 0;
+    }
+    mine.store(at_once + 1, std::memory_order_relaxed);
+    return at_once;
+}
 
 }  // namespace
 
@@ -827,6 +1009,9 @@ static dattn_status_t launch_d(const PfParams& p0, const void* k_pool, const voi
     pp.k_pool = static_cast<const uint8_t*>(k_pool);
     pp.v_pool = static_cast<const uint8_t*>(v_pool);
     pp.scale = reinterpret_cast<const float2*>(kv_scale);
+    const int32_t nwords = (p.max_pages * p.P / kPfBlock + 1 + 4 + 31) / 32;
+    const PbSmem L = pb_smem_layout(D, pp.nq, nwords);
+    if (L.total > 227u * 1024u) return DATTN_ERR_UNSUPPORTED;
     const int32_t blocks = (p.Tq + kPfBlock - 1) / kPfBlock + 1;  // query blocks a chunk can touch
     p.nqb = (blocks + pp.nq - 1) / pp.nq;
     const int64_t per_head = (int64_t)p.nqb * (p.g / pp.hp);
@@ -835,7 +1020,18 @@ static dattn_status_t launch_d(const PfParams& p0, const void* k_pool, const voi
     // a last wave of tile pairs for at most half of the SMs: a CTA for each tile instead
     const int64_t rest = pairs % sms;
     pp.whole = (int32_t)(2 * rest <= sms ? pairs - rest : pairs);
-    const int64_t ctas = pp.whole + 2 * (pairs - pp.whole);
+    // Few tiles with rows (of a chunk that begins on a block): the largest cluster for each with which
+    // all run at once, where the block table has room for blocks to share.
+    const int64_t tiles = (int64_t)p.B * p.Hkv * (p.g / pp.hp) * (((blocks - 1) * pp.hp + 1) / 2);
+    pp.split = 1;
+    for (int32_t s = 8; s > 1 && pp.split == 1; s /= 2)
+        if (tiles * s <= sms &&
+            (int64_t)p.max_pages * p.P >= (int64_t)s * kPbSplitBlocks * kPfBlock &&
+            tiles <= clusters_at_once<D>(s, L.total)) {
+            pp.split = s;
+            pp.whole = 0;
+        }
+    const int64_t ctas = (pp.whole + 2 * (pairs - pp.whole)) * pp.split;
     if (pairs >= (1ll << 31) - sms) return DATTN_ERR_UNSUPPORTED;
     // as in prefill.cu: the smallest group of KV heads whose CTAs fill three waves
     p.kv_group = p.Hkv;
@@ -844,24 +1040,23 @@ static dattn_status_t launch_d(const PfParams& p0, const void* k_pool, const voi
             p.kv_group = G;
             break;
         }
-    const int32_t nwords = (p.max_pages * p.P / kPfBlock + 1 + 4 + 31) / 32;
-    const PbSmem L = pb_smem_layout(D, pp.nq, nwords);
-    if (L.total > 227u * 1024u) return DATTN_ERR_UNSUPPORTED;
-    {
-        std::lock_guard<std::mutex> lock(g_pb_mutex);
-        int& set = g_pb_smem_set[D == 128 ? 1 : 0][device_index()];
-        if ((int)L.total > set) {
-            if (cudaFuncSetAttribute(prefill_block_kernel<D>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)L.total) != cudaSuccess)
-                return DATTN_ERR_CUDA;
-            set = (int)L.total;
-        }
-    }
-    return launch_pdl(prefill_block_kernel<D>, dim3((unsigned)ctas), dim3(kPbThreads), L.total,
-                      stream, pp, nwords) == cudaSuccess
-               ? DATTN_OK
-               : DATTN_ERR_CUDA;
+    auto kern = pp.split > 1 ? prefill_block_kernel<D, true> : prefill_block_kernel<D, false>;
+    const dattn_status_t st =
+        pp.split > 1 ? ensure_smem<D, true>(L.total) : ensure_smem<D, false>(L.total);
+    if (st != DATTN_OK) return st;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kPbThreads);
+    cfg.dynamicSmemBytes = L.total;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)pp.split, 1u, 1u};
+    cfg.attrs = attr;
+    cfg.numAttrs = pp.split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, pp, nwords) == cudaSuccess ? DATTN_OK : DATTN_ERR_CUDA;
 }
 
 dattn_status_t launch_prefill_block(const PfParams& p, const void* k_pool, const void* v_pool,

@@ -288,13 +288,6 @@ struct RopeAppendParams {
     RotArgs rot;
 };
 
-__device__ __forceinline__ void cluster_arrive() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // New tokens of request b: new_lens[b] inside [0, T]; another value is flagged and clamped.
 __device__ __forceinline__ int32_t new_count(const int32_t* new_lens, int32_t b, int32_t T,
                                              int32_t* dev_err) {

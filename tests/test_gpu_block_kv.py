@@ -541,6 +541,59 @@ def test_long_prefill_of_many_tiles(Hq, Hkv, d, Tq, L):
     assert int(cache.dev_err.item()) == 0
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,Tq,L", [(32, 8, 128, 64, 9000), (8, 1, 64, 1, 20001),
+                                           (16, 16, 128, 33, 5000), (6, 3, 128, 130, 3001),
+                                           (12, 4, 64, 100, 4097), (4, 1, 128, 300, 300)])
+def test_prefill_of_few_rows_over_a_long_context(Hq, Hkv, d, Tq, L):
+    """Few tiles: clusters of CTAs share a tile's key blocks (more than 32 each in the first two, so
+    that accumulators are emptied). Errors as above; repeated and captured calls give the same bits."""
+    case = W.Case("pff", B=1, Hq=Hq, Hkv=Hkv, d=d, P=16, lens=[L], seed=6)
+    cache, K, V = _filled_fast(case, 33)
+    q = _rows((1, Tq, Hq, d), 88)
+    out, m, e = _prefill(cache, q)
+    want = _attention64(q[0], K, V, case.scale)
+    err = (out[0] - want).norm(dim=2) / want.norm(dim=2)
+    assert err.max().item() <= 2.0 ** -14 and ((out[0] - want).norm() / want.norm()) <= 2.0 ** -15
+    # m + ln e is the logarithm of the sum: scores of a few units, 2^-18 of them and of the sum
+    see = torch.arange(L, device=DEV)[None] <= (L - Tq + torch.arange(Tq, device=DEV))[:, None]
+    for h in (0, Hq - 1):
+        w = (q[0, :, h].double() @ K[h * Hkv // Hq].T * case.scale).masked_fill_(~see, -np.inf)
+        top, lse = w.max(1).values, torch.logsumexp(w, 1)
+        assert ((m[0, :, h] - top).abs() <= 2.0 ** -18 * (1 + top.abs())).all()
+        assert ((m[0, :, h] + e[0, :, h].double().log() - lse).abs() <= 2.0 ** -16).all()
+    again = torch.empty_like(out)
+    call = lambda: dattn.dattn_prefill(cache.layout, cache.k_pool, cache.v_pool, q,  # noqa: E731
+                                       case.scale, cache.seq_lens, again, dev_err=cache.dev_err)
+    call()
+    torch.cuda.synchronize()
+    assert torch.equal(again, out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+        call()
+    again.fill_(float("nan"))
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(again, out) and int(cache.dev_err.item()) == 0
+
+
+def test_prefill_of_few_rows_beside_empty_and_bad_requests():
+    """Short, zero-length and over-long requests beside a long one in clusters of four; rows of
+    a request that the call refuses stay as they were."""
+    lens = [1500, 9, 40, 700]
+    case = W.Case("pfb", B=4, Hq=4, Hkv=1, d=64, P=16, lens=lens, seed=6)
+    cache, kp, vp = _filled(case, 24)
+    q = _rows((4, 9, 4, 64), 89)
+    want, m, e = _prefill(cache, q)
+    _check(case, q, want, m, e, kp, vp, weights=PREFILL)
+    cache.seq_lens[1], cache.seq_lens[3] = 0, 16 * case.max_pages + 1
+    out = torch.full_like(want, 7.0)
+    out, _, _ = _prefill(cache, q, out=out)
+    assert torch.equal(out[0], want[0]) and torch.equal(out[2], want[2])
+    assert (out[1] == 7.0).all() and (out[3] == 7.0).all()
+    assert int(cache.dev_err.item()) != 0
+
+
 def test_prefill_whose_row_maxima_climb():
     """Keys whose scores climb by 2^9 and more from window to window and block to block: what the
     output row holds of earlier windows is moved to the new reference, or vanishes beside it."""
@@ -551,6 +604,22 @@ def test_prefill_whose_row_maxima_climb():
     q = torch.zeros(1, Tq, 4, d, dtype=torch.bfloat16, device=DEV)
     q[..., 0] = torch.tensor([1.0, 0.02, 3.0, -1.0], device=DEV).to(torch.bfloat16)
     k[0, :, 0, 0] = (torch.arange(L, device=DEV) // 64 * 8).to(torch.bfloat16)
+    cache.append(k, v)
+    kp.append(case.block_table[0], 0, k[0].double().cpu().numpy())
+    vp.append(case.block_table[0], 0, v[0].double().cpu().numpy())
+    out, m, e = _prefill(cache, q)
+    _check(case, q, out, m, e, kp, vp, weights=PREFILL)
+
+
+def test_prefill_of_many_tiles_whose_row_maxima_climb():
+    """As above with a CTA for each tile pair or tile, and no clusters."""
+    d, L, Tq, Hkv = 64, 64 * 70, 128, 20
+    case = W.Case("pfm", B=1, Hq=4 * Hkv, Hkv=Hkv, d=d, P=64, lens=[L], seed=6, scale=1.0)
+    cache, kp, vp = _cache(case), *_pools(case)
+    k, v = _rows((1, L, Hkv, d), 43), _rows((1, L, Hkv, d), 44)
+    q = torch.zeros(1, Tq, 4 * Hkv, d, dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = torch.tensor([1.0, 0.02, 3.0, -1.0], device=DEV).to(torch.bfloat16).repeat(Hkv)
+    k[0, :, :, 0] = (torch.arange(L, device=DEV) // 64 * 8).to(torch.bfloat16)[:, None]
     cache.append(k, v)
     kp.append(case.block_table[0], 0, k[0].double().cpu().numpy())
     vp.append(case.block_table[0], 0, v[0].double().cpu().numpy())
