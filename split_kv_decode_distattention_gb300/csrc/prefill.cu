@@ -205,6 +205,7 @@ prefill_tc_kernel(const __grid_constant__ PfParams p, const __grid_constant__ CU
         prefetch_tmap(&tmap_k);
         prefetch_tmap(&tmap_v);
     }
+    __syncwarp();  // (tcgen05 instructions take whole, converged warps)
     if (warp == 0) {  // the whole warp allocates the CTA's tensor memory
         tc_alloc(smem_u32(base + L.taddr), kTcCols);
         tc_relinquish();
@@ -516,7 +517,9 @@ prefill_tc_kernel(const __grid_constant__ PfParams p, const __grid_constant__ CU
                 const float f = need && m_used != kPfNegInf ? exp2f(m_used - mx) : 1.f;
                 if (__any_sync(0xffffffffu, f != 1.f) && j > 0) {
                     // O holds the blocks before this one: wait for them, then scale it
-                    mbar_wait(pv_done, (j - 1) & 1, abort_p, p.dev_err);
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(pv_done, (j - 1) & 1, abort_p, p.dev_err)) != 0;
+                    if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
                     for (int cc = 0; cc < D / 32; ++cc) {
@@ -582,6 +585,7 @@ prefill_tc_kernel(const __grid_constant__ PfParams p, const __grid_constant__ CU
                     }
                     fence_proxy_async_smem();
                 }
+                __syncwarp();
                 tc_fence_before();
                 mbar_arrive(p_full(s));
                 ++j;
@@ -601,6 +605,7 @@ prefill_tc_kernel(const __grid_constant__ PfParams p, const __grid_constant__ CU
         const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
         for (int cc = 0; cc < D / 32; ++cc) {
+            __syncwarp();
             float t[32];
             if (nblk > 0 && ok) {
                 tc_ld32(tbase + lanes + 32u * cc, t);

@@ -264,6 +264,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
         *abort_p = 0;
         fence_mbar_init();
     }
+    __syncwarp();  // (tcgen05 and cluster-barrier instructions take whole, converged warps)
     if (warp == 0) {  // the whole warp allocates the CTA's tensor memory
         tc_alloc(smem_u32(base + L.taddr), kPbCols);
         tc_relinquish();
@@ -661,7 +662,8 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                 // A window is over: its sum goes to the output row, the next one begins at zero.
                 // (P V of block j - 2 ended before these scores were made, so the barrier is at most
                 // one phase behind, which its parity can tell.)
-                mbar_wait(bar(kBarPv + t), (j - 1) & 1, abort_p, p.dev_err);
+                ok = wait(bar(kBarPv + t), (j - 1) & 1);
+                if (!ok) break;
                 tc_fence_after();
                 const float at = m_used + (float)rexp;
                 if constexpr (SPLIT) {
@@ -700,6 +702,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                     const float f = some ? exp2f(at - ref) : 0.f;
 #pragma unroll 1
                     for (int cc = 0; cc < D / 16; ++cc) {
+                        __syncwarp();
                         float v[16];
                         tc_ld16(ocol + 16u * cc, v);
                         tc_wait_ld();
@@ -724,6 +727,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                                 red_add4(to + e, v[e] * f, v[e + 1] * f, v[e + 2] * f, v[e + 3] * f);
                         }
                     }
+                    __syncwarp();
                     tc_fence_before();
                 }
             }
@@ -759,7 +763,8 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                 l *= f;
                 if ((j & (kPbWindow - 1)) != 0 && __any_sync(0xffffffffu, fo != 1.f)) {
                     // O holds the window's blocks before this one: wait for them, then scale it
-                    mbar_wait(bar(kBarPv + t), (j - 1) & 1, abort_p, p.dev_err);
+                    ok = wait(bar(kBarPv + t), (j - 1) & 1);
+                    if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
                     for (int cc = 0; cc < D / 16; ++cc) {  // (16 columns: the scores stay in registers)
@@ -864,6 +869,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
             if (more) __threadfence();  // the row's earlier additions
 #pragma unroll 1
             for (int cc = 0; cc < D / 16; ++cc) {
+                __syncwarp();
                 float v[16];
                 if (any) {
                     tc_ld16(ocol + 16u * cc, v);
@@ -939,6 +945,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                     if (p.e_out) p.e_out[row] = l;
                 }
             }
+            __syncwarp();
             cluster_arrive();  // no CTA leaves while another reads its parts
             cluster_wait();
         }
