@@ -7,9 +7,11 @@
 // row is scaled by a power of two 2^a that brings its largest element to [2^14, 2^15) and rounded
 // to fp16: exact for every element within 2^28 of the largest. The K scale of a 16-key tile
 // multiplies its scores; the V scale, a power of two, goes into the exponent of its weights,
-// w = 2^(s - m + log2(scale / r)), where 2^r is a power of two that the scales seen so far exceed
-// by 2^7 at most (raised, and the accumulators rescaled, when a larger one comes), so that w stays
-// below 2^15. w enters the product as two fp16 terms, 22 bits together.
+// w = 2^(s - m + log2(scale) - x). The reference m + x is the row's own: it follows the largest
+// s + log2(scale) of the keys that the row sees and whose V is not all zeros (w = 2^9 when it is set;
+// raised, and the row's accumulator rescaled, when a key exceeds 2^15), so that a V scale which the
+// row does not see, or whose keys weigh nothing in it, takes no bits from the others. w enters the
+// product as two fp16 terms: 22 bits together, and to 2^-33 of the largest w where it is small.
 // The tensor cores add into their fp32 accumulators rounding towards zero, which over a long
 // context shrinks the result (5.6e-5 after 4096 products of a 32K context), so a row's accumulator is
 // emptied into its output row every kPbWindow key blocks, by fp32 additions.
@@ -63,6 +65,10 @@ constexpr int kPbRing = 2 * kPbGroup;       // the blocks' ring
 constexpr int kPbWindow = 32;
 constexpr int kPbSplitBlocks = 3;           // key blocks of a CTA at least, where a cluster shares
                                             // a tile (2 cost more where it would, 4 gave 2 us less)
+// A row's reference m + x (log2 units): its largest weight is 2^kPbTop when the reference is set, and a
+// weight above 2^kPbMost sets it anew (both terms are fp16: below 2^16). With 12 more keys set it anew:
+// 4096 tokens after 28K took 2580 us, 2405 with 9.
+constexpr float kPbTop = 9.f, kPbMost = 15.f;
 constexpr uint32_t kPbCols = 512;           // O: [0, 128), [128, 256); S: 256 + 128 tile + 64 buffer
 
 // mbarriers
@@ -73,13 +79,16 @@ constexpr int kBarRingFull = 22, kBarRingEmpty = 24, kBarDrain = 26, kPbBars = 2
 constexpr int kRingReaders = 14;            // warps 0-13
 
 // A key block in the ring: its 16-key tiles as the widening reads them (place in the pool, in tiles,
-// and tokens) and as the softmax does (K scale, -, log2 of the V scale over 2^r, 2 to minus that), its
-// index, the quarters of rows that keep it (bits 0-3; bit 4: all its keys are written) and r.
+// and tokens) and as the softmax does (K scale, -, log2 of the V scale, 1 / V scale; kPbNoScale and 1
+// for a scale of 0), its index, the quarters of rows that keep it (bits 0-3; bit 4: all its keys are
+// written), and the smallest and largest log2 of a V scale of its written tiles.
 struct __align__(16) PbBlock {
     int2 rows[kPfTiles];
     float4 scale[kPfTiles];
-    int32_t kb, act, r, pad;
+    int32_t kb, act;
+    float low, high;
 };
+constexpr float kPbNoScale = -1000.f;
 constexpr int32_t kPbFull = 16;
 // the tiles (bits) of the quarters that keep a block
 __device__ __forceinline__ uint32_t tiles_of(uint32_t act) {
@@ -236,7 +245,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
     auto bar = [&](int i) { return bars + 8u * i; };
     PbBlock* ring = reinterpret_cast<PbBlock*>(base + L.ring);
     uint32_t* bm = reinterpret_cast<uint32_t*>(base + L.bm);
-    // SPLIT: the tile's sums (rows of D + 4 floats, for the banks) and (m_used, rexp, l, m_true) of its
+    // SPLIT: the tile's sums (rows of D + 4 floats, for the banks) and (m_used, xref, l, m_true) of its
     // rows, where the K and V stages were
     float* part = reinterpret_cast<float*>(base + L.kst);
     float4* stat = reinterpret_cast<float4*>(part + 128 * (D + 4));
@@ -402,7 +411,6 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
             }
             for (; n > 0 && skip > 0; --skip) word &= word - 1u;
         }
-        int r = -126;
         bool ok = true;
         for (int32_t i = 0; i < n && ok; i += kPbGroup) {
             const int32_t cnt = min(kPbGroup, n - i);
@@ -433,19 +441,13 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                     sc = __ldg(pp.scale + (y >> 4));
                 }
             }
-            // 2^r: what the V scales up to each block exceed by 2^7 at most
-            const int ve = sc.y > 0.f ? (__float_as_int(sc.y) >> 23) - 127 : -1000;
-            int vm = max(ve, __shfl_xor_sync(0xffffffffu, ve, 1));
-            vm = max(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
-            int mine = r;
-            for (int x = 0; x < kPbGroup; ++x) {
-                const int v = __shfl_sync(0xffffffffu, vm, 4 * x);
-                if (v > r + 7) r = v;
-                if (x == blk) mine = r;
-            }
-            // (far below 2^r a scale counts as 2^(r - 64): nothing beside the others; codes with
-            // scale 0 are zeros)
-            const int lv = sc.y > 0.f ? max(ve - mine, -64) : 0;
+            const int ve = (__float_as_int(sc.y) >> 23) - 127;
+            float high = sc.y > 0.f ? (float)ve : kPbNoScale;
+            float low = hi > 0 ? high : -kPbNoScale;
+            low = fminf(low, __shfl_xor_sync(0xffffffffu, low, 1));
+            low = fminf(low, __shfl_xor_sync(0xffffffffu, low, 2));
+            high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 1));
+            high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 2));
             int full = hi == 16 ? 1 : 0;
             full &= __shfl_xor_sync(0xffffffffu, full, 1);
             full &= __shfl_xor_sync(0xffffffffu, full, 2);
@@ -454,11 +456,13 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
             if (ok && blk < cnt) {
                 PbBlock& to = ring[(i + blk) & (kPbRing - 1)];
                 to.rows[u] = make_int2(y >> 4, hi);
-                to.scale[u] = make_float4(sc.x, 0.f, (float)lv, pow2i(-lv));
+                to.scale[u] = sc.y > 0.f ? make_float4(sc.x, 0.f, (float)ve, pow2i(-ve))
+                                         : make_float4(sc.x, 0.f, kPbNoScale, 1.f);
                 if (u == 0) {
                     to.kb = kb;
                     to.act = act | (full ? kPbFull : 0);
-                    to.r = mine;
+                    to.low = low;
+                    to.high = high;
                 }
             }
             __syncwarp();
@@ -625,16 +629,17 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
         const int64_t row = ((int64_t)b * p.Tq + (rowok ? pos - c0 : 0)) * p.Hq + h0 + q_head(z);
         float* orow = p.out + row * D;
         float m_used = kPfNegInf, m_true = kPfNegInf, l = 0.f;  // l is relative to m_used
-        int rexp = -126;  // O is relative to m_used and to 2^rexp
-        // what the output row holds of earlier windows is relative to 2^ref (-inf: nothing)
-        float ref = kPfNegInf;
+        // O is relative to 2^mref, mref = m_used + xref; xfac is 2^xref
+        float xref = -126.f, xfac = pow2i(-126), mref = kPfNegInf;
+        // what the output row holds of earlier windows is relative to 2^(ref_m + ref_x) (-inf: nothing)
+        float ref_m = kPfNegInf, ref_x = 0.f;
         int32_t j = 0;  // this tile's blocks
         bool ok = true;
         for (int32_t i = 0; i < n; ++i) {
             ok = ring_ready(i);
             if (!ok) break;
             const PbBlock& blk = ring[i & (kPbRing - 1)];
-            const int32_t act = blk.act, kb = blk.kb, rnew = blk.r;
+            const int32_t act = blk.act, kb = blk.kb;
             if (!(act & (3 << (2 * t)))) {
                 ring_release(i);
                 continue;
@@ -665,12 +670,14 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                 ok = wait(bar(kBarPv + t), (j - 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
-                const float at = m_used + (float)rexp;
+                // log2 of the present reference over that of the earlier windows
+                const float rise = (m_used - ref_m) + (xref - ref_x);
                 if constexpr (SPLIT) {
                     // (to the other tile's columns, which this CTA does not use: the output row is
                     // the cluster's)
-                    const float down = ref == kPfNegInf ? 0.f : exp2f(ref - at);
-                    ref = at;
+                    const float down = ref_m == kPfNegInf ? 0.f : exp2f(-rise);
+                    ref_m = m_used;
+                    ref_x = xref;
 #pragma unroll 1
                     for (int cc = 0; cc < D / 16; ++cc) {
                         float v[16];
@@ -694,12 +701,15 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                     tc_fence_before();
                 } else {
                     const bool some = rowok && m_used != kPfNegInf;
-                    const bool first = some && ref == kPfNegInf;
+                    const bool first = some && ref_m == kPfNegInf;
                     // far above the row's reference, what it holds moves to the new one first
-                    const bool move = some && !first && at > ref + 60.f;
-                    const float down = move ? exp2f(ref - at) : 1.f;
-                    if (first || move) ref = at;
-                    const float f = some ? exp2f(at - ref) : 0.f;
+                    const bool move = some && !first && rise > 60.f;
+                    const float down = move ? exp2f(-rise) : 1.f;
+                    const float f = some && !first && !move ? exp2f(rise) : 1.f;
+                    if (first || move) {
+                        ref_m = m_used;
+                        ref_x = xref;
+                    }
 #pragma unroll 1
                     for (int cc = 0; cc < D / 16; ++cc) {
                         __syncwarp();
@@ -752,15 +762,60 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
             const float mx = fmaxf(fmaxf(max16(x) * fu[0], max16(x + 16) * fu[1]),
                                    fmaxf(max16(x + 32) * fu[2], max16(x + 48) * fu[3]));
             m_true = fmaxf(m_true, mx);
-            // lazy rescale of O and l when the row maximum grows by more than 2^8, and of O when r
-            // is raised; the tensor-memory traffic is warp-collective, so a warp rescales when any
-            // of its rows must
-            const bool need = mx > m_used + kTcRescale || (m_used == kPfNegInf && mx != kPfNegInf);
-            if (__any_sync(0xffffffffu, need) || rnew != rexp) {
-                const float f = need && m_used != kPfNegInf ? exp2f(m_used - mx) : 1.f;
-                const float fo = f * (rexp - rnew < -126 ? 0.f : pow2i(rexp - rnew));
-                rexp = rnew;
-                l *= f;
+            // Lazy rescale of l when the row maximum grows by more than 2^8, and of O then and when a
+            // weight may exceed 2^kPbMost. The tensor-memory traffic is warp-collective, so a warp
+            // rescales when any of its rows must. A tile far below the reference comes here too.
+            if (__any_sync(0xffffffffu, mx > m_used + kTcRescale || mx + blk.high > mref + kPbMost ||
+                                            blk.low < xref - 64.f)) {
+                // Keys whose V is all zeros count in the sum, but not for O's reference (a token of the
+                // same tile, whose scale it is, may be one that the row does not see): a lane looks at
+                // two rows of the V stage. P V of this block, and so the stage's next use, waits for the
+                // weights made below.
+                ok = wait(bar(kBarVFull + i % kPbStages), (i / kPbStages) & 1);
+                if (!ok) break;
+                uint32_t z0 = 0xffffffffu, z1 = 0xffffffffu;
+                const uint8_t* vst = base + L.vst + (uint32_t)(i % kPbStages) * L.blk_bytes;
+#pragma unroll 1
+                for (uint32_t ch = 0; ch < D / 8 && (z0 | z1) != 0u; ++ch) {  // (most often once)
+                    const uint8_t* at = vst + (ch >> 3) * kHalf;
+                    const uint4 a = *reinterpret_cast<const uint4*>(at + swz128(lane, ch & 7u));
+                    const uint4 c = *reinterpret_cast<const uint4*>(at + swz128(lane + 32u, ch & 7u));
+                    z0 &= __ballot_sync(0xffffffffu, ((a.x | a.y | a.z | a.w) & 0x7fff7fffu) == 0u);
+                    z1 &= __ballot_sync(0xffffffffu, ((c.x | c.y | c.z | c.w) & 0x7fff7fffu) == 0u);
+                }
+                // the row's largest weight times V scale
+                float top = kPfNegInf;
+#pragma unroll
+                for (int u = 0; u < kPfTiles; ++u) {
+                    const uint32_t z = (u < 2 ? z0 : z1) >> (16 * (u & 1));
+                    float t;
+                    if ((z & 0xffffu) == 0u) {
+                        t = max16(x + 16 * u);
+                    } else {
+                        float y[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) y[e] = (z >> e) & 1u ? kPfNegInf : x[16 * u + e];
+                        t = max16(y);
+                    }
+                    top = fmaxf(top, fmaf(t, fu[u], blk.scale[u].z));
+                }
+                float fo = 1.f;
+                if (mx > m_used + kTcRescale || top > mref + kPbMost) {
+                    const float m_new = fmaxf(m_used, mx);
+                    const bool none = m_used == kPfNegInf;  // O and l are zeros
+                    // (an integer, so that 2^-xref is exact; the reference moves down by less than 1)
+                    float x_new = ceilf(top - m_new) - kPbTop;
+                    if (!none) x_new = fmaxf(x_new, floorf((m_used - m_new) + xref));
+                    x_new = fminf(fmaxf(x_new, -126.f), 127.f);
+                    if (!none) {
+                        l *= exp2f(m_used - m_new);
+                        fo = exp2f((m_used - m_new) + (xref - x_new));
+                    }
+                    m_used = m_new;
+                    xref = x_new;
+                    xfac = pow2i((int)x_new);
+                    mref = m_new + x_new;
+                }
                 if ((j & (kPbWindow - 1)) != 0 && __any_sync(0xffffffffu, fo != 1.f)) {
                     // O holds the window's blocks before this one: wait for them, then scale it
                     ok = wait(bar(kBarPv + t), (j - 1) & 1);
@@ -778,14 +833,30 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                     }
                     tc_wait_st();
                 }
-                if (need) m_used = mx;
+                // Keys with a V of zeros, whose weight for O may be of any size, and the tiles 2^64
+                // below the reference, whose weights may vanish, enter the sum here and weigh 0 in O.
+                const float mu = m_used == kPfNegInf ? 0.f : m_used;
+#pragma unroll
+                for (int u = 0; u < kPfTiles; ++u) {
+                    uint32_t z = ((u < 2 ? z0 : z1) >> (16 * (u & 1))) & 0xffffu;
+                    if (blk.scale[u].z < xref - 64.f) z = 0xffffu;
+                    if (z != 0u) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const bool out = (z >> e) & 1u;
+                            l += out ? ex2_approx(fmaf(x[16 * u + e], fu[u], -mu)) : 0.f;
+                            x[16 * u + e] = out ? kPfNegInf : x[16 * u + e];
+                        }
+                    }
+                }
+                __syncwarp();
             }
-            const float mu = m_used == kPfNegInf ? 0.f : m_used;
-            // w = 2^(x f - mu + lv) in pairs; a masked key (-inf) gives +0. w goes to the score
-            // buffer as two fp16 terms: hi (rounded) into columns [0, 32), lo (the exact rest,
+            // w = 2^(x f - mref + log2(V scale)) in pairs; a masked key (-inf) gives +0. w goes to the
+            // score buffer as two fp16 terms: hi (rounded) into columns [0, 32), lo (the exact rest,
             // rounded) into [32, 64). hi comes back from fp16 by a conversion, on the FMA pipe:
             // masking its word would load the ALU pipe, which is the fuller one. The sum takes w
-            // without its tile's 2^lv.
+            // times 2^xref over its tile's V scale.
+            const float base2 = m_used == kPfNegInf ? 0.f : mref;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 uint32_t ph[16], pl[16];
@@ -793,8 +864,9 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                 for (int uu = 0; uu < 2; ++uu) {
                     const int u = 2 * hf + uu;
                     const uint64_t f2 = pack_f32x2(fu[u], fu[u]);
-                    const float2 lv = *reinterpret_cast<const float2*>(&blk.scale[u].z);
-                    const float nm = lv.x - mu;
+                    const float2 vs = *reinterpret_cast<const float2*>(&blk.scale[u].z);
+                    const float nm = vs.x - base2;
+                    const float undo = fminf(vs.y * xfac, 1.8446744e19f);  // (at most 2^64 where w counts)
                     const uint64_t n2 = pack_f32x2(nm, nm);
                     float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
@@ -811,7 +883,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                         sub_f32x2(p0, p1, f16_lo(g), f16_hi(g), r0, r1);
                         pl[8 * uu + cc] = pack_f16(r0, r1);
                     }
-                    l = fmaf((s0 + s1) + (s2 + s3), lv.y, l);
+                    l = fmaf((s0 + s1) + (s2 + s3), undo, l);
                 }
                 tc_st16(sbuf + 16u * hf, ph);
                 tc_st16(sbuf + 32u + 16u * hf, pl);
@@ -830,11 +902,11 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
         ok = __all_sync(0xffffffffu, ok);
         const bool any = j > 0 && ok;
         if (SPLIT && use > 1) {
-            // the row's sum, relative to 2^(m_used + rexp), and what it is relative to
+            // the row's sum, relative to 2^(m_used + xref), and what it is relative to
             if ((tmask >> t) & 1u) {
                 const bool more = j > kPbWindow;  // (at a multiple of it the last window is still in O)
                 const float down =
-                    more && ref != kPfNegInf ? exp2f(ref - (m_used + (float)rexp)) : 0.f;
+                    more && ref_m != kPfNegInf ? exp2f((ref_m - m_used) + (ref_x - xref)) : 0.f;
                 float* to = part + (r & 127) * (D + 4);
 #pragma unroll 1
                 for (int cc = 0; cc < D / 16; ++cc) {
@@ -857,15 +929,16 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                         *reinterpret_cast<float4*>(to + 16 * cc + e) =
                             make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                 }
-                stat[r & 127] = make_float4(m_used, (float)rexp, l, m_true);
+                stat[r & 127] = make_float4(m_used, xref, l, m_true);
             }
         } else if (!SPLIT || rank == 0) {
-            // out = (O + earlier windows) 2^rexp / l, the exponent and 1 / l multiplied in turn (either
+            // out = (O + earlier windows) 2^xref / l, the exponent and 1 / l multiplied in turn (either
             // may be far from 1)
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            const float up = pow2i(rexp);
-            const bool more = !SPLIT && ref != kPfNegInf && ok;  // (SPLIT: fewer blocks than a window)
-            const float down = more ? exp2f(ref - (m_used + (float)rexp)) : 0.f;
+            const float up = xfac;
+            // (SPLIT: fewer blocks than a window)
+            const bool more = !SPLIT && ref_m != kPfNegInf && ok;
+            const float down = more ? exp2f((ref_m - m_used) + (ref_x - xref)) : 0.f;
             if (more) __threadfence();  // the row's earlier additions
 #pragma unroll 1
             for (int cc = 0; cc < D / 16; ++cc) {
@@ -915,11 +988,15 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                 const int r = 128 * t + rl, z = r >> 6, qi = q_block(z);
                 const int32_t pos = (qa + qi) * kPfBlock + (r & 63);
                 if (!(((has >> qi) & 1u) && pos >= c0 && pos < Ln)) continue;
-                float m = kPfNegInf, top = kPfNegInf;  // the row's maximum; the parts' largest exponent
+                // the row's maximum; the parts' largest reference, 2^(top_m + top_x)
+                float m = kPfNegInf, top_m = kPfNegInf, top_x = 0.f;
                 for (int y = 0; y < use; ++y) {
                     const float4 st = ld_cluster4(smem_u32(stat + rl), y);
                     m = fmaxf(m, st.w);
-                    if (st.x != kPfNegInf) top = fmaxf(top, st.x + st.y);
+                    if (st.x != kPfNegInf && (st.x - top_m) + (st.y - top_x) > 0.f) {
+                        top_m = st.x;
+                        top_x = st.y;
+                    }
                 }
                 float l = 0.f;
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -927,19 +1004,25 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                     const float4 st = ld_cluster4(smem_u32(stat + rl), y);
                     if (st.x == kPfNegInf) continue;
                     const float4 v = ld_cluster4(smem_u32(part + rl * (D + 4) + 4 * c4), y);
-                    const float f = exp2f(st.x + st.y - top);
+                    const float f = exp2f((st.x - top_m) + (st.y - top_x));
                     l = fmaf(st.z, exp2f(st.x - m), l);
                     o.x = fmaf(v.x, f, o.x);
                     o.y = fmaf(v.y, f, o.y);
                     o.z = fmaf(v.z, f, o.z);
                     o.w = fmaf(v.w, f, o.w);
                 }
-                // out = sum 2^top / (l 2^m), in turns as above
-                const float inv = l > 0.f ? 1.f / l : 0.f;
-                const float up = m == kPfNegInf ? 0.f : exp2f(top - m);
+                // out = sum 2^(top_m - m) 2^top_x / l, whole powers of two multiplied in turn as above
+                float inv = l > 0.f ? 1.f / l : 0.f, up = 0.f, up2 = 0.f;
+                if (m != kPfNegInf) {
+                    const float whole = fmaxf(rintf(top_m - m), -126.f);
+                    inv *= exp2f((top_m - m) - whole);
+                    up = pow2i((int)top_x);
+                    up2 = pow2i((int)whole);
+                }
                 const int64_t row = ((int64_t)b * p.Tq + (pos - c0)) * p.Hq + h0 + q_head(z);
                 *reinterpret_cast<float4*>(p.out + row * D + 4 * c4) =
-                    make_float4(o.x * inv * up, o.y * inv * up, o.z * inv * up, o.w * inv * up);
+                    make_float4(o.x * inv * up * up2, o.y * inv * up * up2, o.z * inv * up * up2,
+                                o.w * inv * up * up2);
                 if (c4 == 0) {
                     if (p.m_out) p.m_out[row] = m == kPfNegInf ? kPfNegInf : m * kLn2;
                     if (p.e_out) p.e_out[row] = l;
