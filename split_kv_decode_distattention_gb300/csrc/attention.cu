@@ -474,9 +474,15 @@ __device__ __forceinline__ void write_final(const AttnParams& p, int32_t s, int3
 // when a tile brings a larger one). So 0 <= w_i <= 2^15 always fits fp16, and w_i is
 // split into two fp16 terms (22 significant bits) as the bf16 path splits p_i. The
 // accumulator is multiplied by r * 2^-15 when the piece is published.
-// The block-scaled 8-bit pool takes the same path with one K and one V scale for the tile: the
-// scales are warp-uniform, so raising r needs no reduction, and a tile brings 16 bytes of
-// scales (a bulk copy's least) instead of 128.
+// The block-scaled 8-bit pool takes the same path with one K and one V scale for the tile: a tile
+// brings 16 bytes of scales (a bulk copy's least) instead of 128, and its weighted sum, which is
+// taken by itself (see tile_f8), is multiplied by the V scale as it is added to O in fp32. So its
+// weights are p_i * 2^15, without a scale and without r: a V scale that a query column does not
+// see, or whose tokens weigh nothing in it, takes no bits from the others. The first
+// tile of a warp, and a tile whose V scale is far above the smallest so far, may count by weights
+// far below 1: what two fp16 terms leave of its weights enters in further products, times 2^20 each
+// time, until nothing is left. (O is kept times 2^-8, so that the largest V scale
+// does not overflow before a larger score makes its weight small.)
 // PK: 2 or 4 query columns over the 4-bit pool, whose PV weights take one product per m-tile
 // (see tile_i4). (A mixed-pool instance would work the same way for its 4-bit heads.)
 template <int D, int FMT, bool PK>
@@ -500,6 +506,7 @@ struct Consumer {
                    // current piece's query
     int32_t rk;    // 8-bit pool: r = 2^rk bounds the V scales seen in this piece
     float rv, inv;  // 8-bit pool: r and 2^15 / r
+    float vlim;     // block-scaled pool: 2^12 times the smallest nonzero V scale of this piece so far
     bool i4 = I4;   // the current piece's KV head is 4-bit (set per piece in a mixed pool)
     // 4-bit pool: 8 * 2^-24 * (sum of the query) of this lane's columns 2tig, 2tig + 1, and
     // the running sums of this lane's PV weights of those columns (see tile_i4)
@@ -712,6 +719,7 @@ struct Consumer {
         rk = -112;
         rv = __int_as_float((127 - 112) << 23);
         inv = __int_as_float((142 + 112) << 23);
+        vlim = 0.f;
     }
 
     // Online softmax (base 2) over one tile's logits: rows g8 (s0, s1) and g8 + 8 (s2, s3),
@@ -849,19 +857,46 @@ struct Consumer {
         float s0 = (sa[0] + sb[0]) * kc0, s1 = (sa[1] + sb[1]) * kc0;
         float s2 = (sa[2] + sb[2]) * kc1, s3 = (sa[3] + sb[3]) * kc1;
         float vs0 = sc[BLK ? 1 : 16 + g8], vs1 = BLK ? vs0 : sc[24 + g8];
-        const float vtile = vs0;  // block-scaled pool: the tile's V scale
+        // block-scaled pool: the V scale times 2^-15 (the weights') and 2^-8 (O's), a power of two
+        const float vtile = vs0 * 1.1920928955078125e-07f;
         mask_tile(lo, hi, cut, s0, s1, s2, s3, vs0, vs1);
-        if constexpr (BLK) vs0 = vs1 = vtile;  // masked rows have weight 0
         float p0, p1, p2, p3;
         softmax(s0, s1, s2, s3, p0, p1, p2, p3);
         // ---- V scales: raise r to a power of two >= every V scale of the tile ---------
+        if constexpr (!BLK) raise_r(fmaxf(vs0, vs1));
+        // in [0, 2^15], exact
+        const float vn0 = BLK ? 32768.f : vs0 * inv, vn1 = BLK ? 32768.f : vs1 * inv;
+        float w0 = p0 * vn0, w1 = p1 * vn0, w2 = p2 * vn1, w3 = p3 * vn1;
         if constexpr (BLK) {
-            if (vtile > rv) raise_r_to(vtile);  // warp-uniform
-        } else {
-            raise_r(fmaxf(vs0, vs1));
+            const bool wide = vtile > vlim;  // warp-uniform
+            if (vtile > 0.f) vlim = vlim > 0.f ? fminf(vlim, 4096.f * vtile) : 4096.f * vtile;
+            if (wide) {
+                float vf = vtile;
+                for (int pass = 0; pass < 8; ++pass) {  // (8 x 20 bits: all of a weight)
+                    pv_f8(vbase, lo, hi, w0, w1, w2, w3, vf);
+                    vf *= 9.5367431640625e-07f;  // 2^-20
+                    w0 = rest_of(w0);
+                    w1 = rest_of(w1);
+                    w2 = rest_of(w2);
+                    w3 = rest_of(w3);
+                    // (false for NaN)
+                    if (!__any_sync(0xffffffffu, fmaxf(fmaxf(fabsf(w0), fabsf(w1)),
+                                                       fmaxf(fabsf(w2), fabsf(w3))) > 0.f))
+                        break;
+                }
+                return;
+            }
         }
-        const float vn0 = vs0 * inv, vn1 = vs1 * inv;  // in [0, 2^15], exact
-        const float w0 = p0 * vn0, w1 = p1 * vn0, w2 = p2 * vn1, w3 = p3 * vn1;
+        pv_f8(vbase, lo, hi, w0, w1, w2, w3, vtile);
+    }
+
+    // O^T += V^T W^T of an 8-bit tile with this lane's weights (rows g8: w0, w1; g8 + 8: w2, w3), the
+    // block-scaled pool's times vf.
+    __device__ __forceinline__ void pv_f8(uint32_t vbase, int lo, int hi, float w0, float w1, float w2,
+                                          float w3, float vf) {
+        const int tig = lane & 3;
+        const uint32_t row = (lane & 7) + ((lane >> 3) & 1) * 8;
+        const uint32_t csel = lane >> 4;
         // ---- W^T as the B operand: two fp16 terms, transposed with movmatrix ----------
         // (one query column: both terms in one operand, one product per m-tile)
         const bool g1 = p.gq == 1;
@@ -891,16 +926,17 @@ struct Consumer {
         }
         // The products add into their accumulators rounding towards zero. Over a long piece that
         // shrinks the result (3.9e-6 of it at 8 x 32K tokens of 32 heads), so the block-scaled pool's
-        // tile is summed by itself and added to O rounding to nearest (3.2e-7; 324 us for 318).
+        // tile is summed by itself and added to O, times its V scale, rounding to nearest (3.2e-7; 324
+        // us for 318).
         auto pv = [&](float (&acc)[4], uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3) {
             if constexpr (BLK) {
                 float t[4] = {0.f, 0.f, 0.f, 0.f};
                 mma_f16(t, x0, x1, x2, x3, bh0, bh1);
                 if (!g1) mma_f16(t, x0, x1, x2, x3, bl0, bl1);
-                acc[0] += t[0];
-                acc[1] += t[1];
-                acc[2] += t[2];
-                acc[3] += t[3];
+                acc[0] = fmaf(t[0], vf, acc[0]);
+                acc[1] = fmaf(t[1], vf, acc[1]);
+                acc[2] = fmaf(t[2], vf, acc[2]);
+                acc[3] = fmaf(t[3], vf, acc[3]);
             } else {
                 mma_f16(acc, x0, x1, x2, x3, bh0, bh1);
                 if (!g1) mma_f16(acc, x0, x1, x2, x3, bl0, bl1);
@@ -922,6 +958,12 @@ struct Consumer {
             e4m3x4_to_f16(r3, a2, a3);
             pv(o[2 * c + 1], a0, a1, a2, a3);
         }
+    }
+
+    // What the two fp16 terms of w leave of it (exact; 2^-7 at most for w in [0, 2^15]), times 2^20.
+    static __device__ __forceinline__ float rest_of(float w) {
+        const float r = w - __half2float(__float2half_rn(w));
+        return (r - __half2float(__float2half_rn(r))) * 1048576.f;
     }
 
     // ---- 4-bit pool ------------------------------------------------------------------
@@ -956,24 +998,22 @@ struct Consumer {
     // O (and the 4-bit weight sums). The maximum over the warp is taken only when some lane's
     // exceeds r.
     __device__ __forceinline__ void raise_r(float vl) {
-        if (__any_sync(0xffffffffu, vl > rv)) raise_r_to(warp_vmax(vl));
-    }
-
-    // The same for a warp-uniform vt > r (r >= 2^-112, so vt is a normal number).
-    __device__ __forceinline__ void raise_r_to(float vt) {
-        const int32_t bits = __float_as_int(vt);
-        const int32_t k = min(127, ((bits >> 23) & 0xff) - 127 + ((bits & 0x7fffff) != 0));
-        const int32_t dk = rk - k;
-        const float f = dk >= -126 ? __int_as_float((127 + dk) << 23) : 0.f;
+        if (__any_sync(0xffffffffu, vl > rv)) {
+            const float vt = warp_vmax(vl);  // > r >= 2^-112: a normal number
+            const int32_t bits = __float_as_int(vt);
+            const int32_t k = min(127, ((bits >> 23) & 0xff) - 127 + ((bits & 0x7fffff) != 0));
+            const int32_t dk = rk - k;
+            const float f = dk >= -126 ? __int_as_float((127 + dk) << 23) : 0.f;
 #pragma unroll
-        for (int mt = 0; mt < KS; ++mt) {
-            o[mt][0] *= f; o[mt][1] *= f; o[mt][2] *= f; o[mt][3] *= f;
+            for (int mt = 0; mt < KS; ++mt) {
+                o[mt][0] *= f; o[mt][1] *= f; o[mt][2] *= f; o[mt][3] *= f;
+            }
+            ws0 *= f;
+            ws1 *= f;
+            rk = k;
+            rv = __int_as_float((127 + k) << 23);
+            inv = __int_as_float((142 - k) << 23);
         }
-        ws0 *= f;
-        ws1 *= f;
-        rk = k;
-        rv = __int_as_float((127 + k) << 23);
-        inv = __int_as_float((142 - k) << 23);
     }
 
     // O^T += V^T W^T for one tile with this lane's weights (rows g8: w0, w1; g8 + 8: w2, w3).
@@ -1120,7 +1160,7 @@ struct Consumer {
                 if (hB < p.gq) { wo[hB * D + dd] = o[mt][1]; wo[hB * D + dd + 8] = o[mt][3]; }
             }
         } else {
-            const float rs = rv * 3.0517578125e-05f;  // r * 2^-15, exact
+            const float rs = BLK ? 256.f : rv * 3.0517578125e-05f;  // r * 2^-15, exact
             const bool f4 = MIX ? i4 : I4;
             // 4-bit: row g8 of an m-tile (an even nibble) holds 2^-24 (sum of w n), row g8 + 8
             // (an odd nibble) 16 times that; 8 * (sum of w) is the offset of n = code + 8

@@ -224,3 +224,75 @@ def test_prefill_after_a_taken_back_outlier(size):
     q = _rows((1, Tq, 4, d), 20)
     out, m, e = _prefill(cache, q)
     _check(cache, [L], q, out, m, e)
+
+
+# ---------------------------------------------------------------- decode
+# A weight is exact to 2^-40 of the largest of its warp, and to 24 bits where its tile's V scale is 2^12
+# times the smallest that the warp has taken in, or the first: in the bound's terms 2^-28 for 2^-33.
+DECODE = 2.0 ** -28
+
+
+@pytest.mark.parametrize("size", SIZES)
+def test_decode_after_a_taken_back_outlier(size):
+    d, L = 64, 84
+    case = W.Case("back", B=1, Hq=4, Hkv=1, d=d, P=16, lens=[0], seed=3, reserve_tokens=L + 8)
+    cache = _cache(case)
+    k, v = _rows((1, L, 1, d), 16), _rows((1, L, 1, d), 17)
+    cache.append(k[:, :70].contiguous(), v[:, :70].contiguous())
+    kx, vx = _rows((1, 3, 1, d), 18), _rows((1, 3, 1, d), 19)
+    _grow(vx[0], slice(1, 2), size)
+    cache.append(kx, vx)
+    cache.seq_lens.fill_(70)
+    cache.append(k[:, 70:].contiguous(), v[:, 70:].contiguous())
+    q = _rows((1, 1, 4, d), 20)
+    for splits in (0, 1):
+        out = torch.empty(1, 4, d, device=DEV)
+        cache.decode(q[:, 0].contiguous(), out, cache.workspace(num_splits=splits), num_splits=splits)
+        torch.cuda.synchronize()
+        _check(cache, [L], q, out[:, None], step=DECODE)
+
+
+@pytest.mark.parametrize("T,g,splits", [(2, 4, 0), (8, 1, 0), (4, 2, 1), (3, 2, 7)])
+def test_multi_query_decode_beside_a_large_value(T, g, splits):
+    """The last of T new tokens has the large V: the queries before it do not see it."""
+    d, L, B = 128, 1500, len(SIZES)
+    case = W.Case("draft", B=B, Hq=2 * g, Hkv=2, d=d, P=16, lens=[0] * B, seed=3, reserve_tokens=L)
+    cache = _cache(case)
+    k, v = _rows((B, L, 2, d), 21), _rows((B, L, 2, d), 22)
+    for b, size in enumerate(SIZES):
+        _grow(v[b], [L - 1], size)
+    cache.append(k, v)
+    q = _rows((B, T, 2 * g, d), 23)
+    out = torch.empty(B, T, 2 * g, d, device=DEV)
+    m, e = torch.empty(B, T, 2 * g, device=DEV), torch.empty(B, T, 2 * g, device=DEV)
+    cache.decode(q, out, cache.workspace(queries=T, num_splits=splits), m, e, num_splits=splits)
+    torch.cuda.synchronize()
+    assert int(cache.dev_err.item()) == 0
+    _check(cache, [L] * B, q, out, m, e, step=DECODE)
+
+
+@pytest.mark.parametrize("Hq,splits", [(2, 1), (16, 1), (16, 0)])
+@pytest.mark.parametrize("drop", [20.0, 45.0, 200.0])
+def test_decode_of_large_values_that_weigh_little(Hq, splits, drop):
+    """A visible tile of large values whose keys score `drop` below the others, and taken in before
+    them or after."""
+    d, L, B = 128, 700, 6
+    case = W.Case("dlight", B=B, Hq=Hq, Hkv=2, d=d, P=64, lens=[0] * B, seed=3, reserve_tokens=L,
+                  scale=1.0)
+    cache = _cache(case)
+    k, v = _rows((B, L, 2, d), 24) * 0.125, _rows((B, L, 2, d), 25)
+    k[..., 0] = 0.0
+    for b in range(B):
+        at = slice(0, 16) if b % 2 else slice(640, 660)
+        v[b, at] *= 2.0 ** [12, 30, 100][b // 2]
+        k[b, at, :, 0] = -drop / 2
+    cache.append(k, v)
+    q = _rows((B, 1, Hq, d), 26)
+    q[..., 0] = 2.0
+    out = torch.empty(B, Hq, d, device=DEV)
+    m, e = torch.empty(B, Hq, device=DEV), torch.empty(B, Hq, device=DEV)
+    cache.decode(q[:, 0].contiguous(), out, cache.workspace(num_splits=splits), m, e,
+                 num_splits=splits)
+    torch.cuda.synchronize()
+    assert int(cache.dev_err.item()) == 0
+    _check(cache, [L] * B, q, out[:, None], m[:, None], e[:, None], step=DECODE)
