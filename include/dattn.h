@@ -230,8 +230,8 @@ dattn_status_t dattn_kv_append(const dattn_kv_layout *layout, void *k_pool,
  *     y_a = A (x_a cos(p f_k) - x_b sin(p f_k)),  y_b = A (x_b cos(p f_k) + x_a sin(p f_k)),
  * with (a, b) = (k, k + rot_dim/2), or (2k, 2k + 1) when interleaved; channels from rot_dim on
  * are unchanged. Frequencies are given as turns per position, f_k / (2 pi) mod 1, in units of
- * 2^-64 (dattn_rope_turns), so that an angle is exact at any int32 position; arithmetic is
- * fp32, each result rounded once.
+ * 2^-64 (dattn_rope_turns), so that an angle is known to 2^-32 of a turn at any int32 position;
+ * arithmetic is fp32, each result rounded once.
  */
 typedef struct dattn_rotation {
     int32_t rot_dim;       /* channels [0, rot_dim) are rotated: a multiple of 16, 0 to d */
@@ -252,12 +252,15 @@ enum {
 };
 
 /* Fills inv_freq [rot_dim/2] (host) with the frequencies of a scaling (DATTN_ROPE_*). factor > 0;
- * original_len, low and high > low are read by DATTN_ROPE_BY_PARTS only. */
+ * original_len, low and high > low are read by DATTN_ROPE_BY_PARTS only. The parameters are fp32
+ * numbers, the frequencies fp64: where a base is not an fp32 number, pass frequencies of its own to
+ * dattn_rope_turns. */
 dattn_status_t dattn_rope_frequencies(int32_t rot_dim, float base, int32_t scaling, float factor,
                                       float original_len, float low, float high,
                                       double *inv_freq);
 
-/* turns[k] (host) = inv_freq[k] / (2 pi) mod 1 in units of 2^-64; the frequencies are finite. */
+/* turns[k] (host) = inv_freq[k] / (2 pi) mod 1 in units of 2^-64, rounded to nearest (|inv_freq[k]|
+ * below 2^32: within one unit); the frequencies are finite. */
 dattn_status_t dattn_rope_turns(int32_t n, const double *inv_freq, uint64_t *turns);
 
 /*

@@ -345,7 +345,8 @@ class Rotation:
     f_k comes from base and a scaling for long contexts: "none", "linear" (f_k / factor), "ntk"
     (the base raised) or "by-parts" (frequencies with fewer than `low` turns over original_len
     divided by factor, those with more than `high` kept, a ramp between); or is given as inv_freq,
-    rot_dim / 2 numbers. The frequencies are kept as host data: a Rotation belongs to no device.
+    rot_dim / 2 numbers. base, factor and the other parameters are taken as fp32 numbers, inv_freq as
+    fp64. The frequencies are kept as host data: a Rotation belongs to no device.
     """
 
     def __init__(self, rot_dim: int, interleaved: bool = False, base: float = 10000.0,

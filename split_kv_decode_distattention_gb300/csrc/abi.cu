@@ -284,10 +284,19 @@ dattn_status_t dattn_rope_turns(int32_t n, const double* inv_freq, uint64_t* tur
     if (!inv_freq || !turns) return DATTN_ERR_INVALID_ARG;
     for (int32_t k = 0; k < n; ++k)
         if (!std::isfinite(inv_freq[k])) return DATTN_ERR_INVALID_ARG;
+    // f / (2 pi) as a sum of two doubles, with 2 pi as one: about 105 bits together, so that the 64
+    // bits kept after the point are right for |f| < 2^32 (a single quotient is off by 2^-53 of f,
+    // which position 2^31 makes 2^-22 of it).
+    const double pi2 = 6.283185307179586477, pi2_lo = 2.449293598294706414e-16;
     for (int32_t k = 0; k < n; ++k) {
-        const double t = inv_freq[k] / 6.283185307179586476925;
-        const double frac = t - std::floor(t);  // [0, 1]
-        turns[k] = frac < 1.0 ? (uint64_t)std::ldexp(frac, 64) : 0u;
+        const double f = inv_freq[k];
+        const double q = f / pi2;
+        const double q_lo = (std::fma(-q, pi2, f) - q * pi2_lo) / pi2;
+        // the fractions in units of 2^-64, their whole parts taken off exactly
+        const double a = std::ldexp(q - std::trunc(q), 64), ai = std::trunc(a);
+        const double b = std::ldexp(q_lo - std::trunc(q_lo), 64), bi = std::trunc(b);
+        auto whole = [](double x) { return x < 0.0 ? -(uint64_t)-x : (uint64_t)x; };  // |x| < 2^64
+        turns[k] = whole(ai) + whole(bi) + whole(std::nearbyint((a - ai) + (b - bi)));
     }
     return DATTN_OK;
 }

@@ -6,10 +6,11 @@
 // the pair being channels (k, k + r/2) or (2k, 2k + 1) of the first r. Its transpose (the angle
 // negated) is the gradient.
 //
-// Angles: a frequency is kept as the fraction of a turn per position in units of 2^-64, so the
-// 64-bit integer product p * f_k wraps at whole turns and its upper 32 bits are the angle to
-// 2^-32 of a turn at any position, without a 64-bit floating-point operation; fp32 products lose
-// 0.06 rad at position 10^6. Sine and cosine of that fraction: sincos_turn.
+// Angles: a frequency is kept as the fraction of a turn per position in units of 2^-64 (rounded to
+// nearest), so the 64-bit integer product p * f_k wraps at whole turns, is within 2^-34 of a turn at
+// any int32 position, and its upper 32 bits are the angle to 2^-32 of a turn, without a 64-bit
+// floating-point operation; fp32 products lose 0.06 rad at position 10^6. Sine and cosine of that
+// fraction: sincos_turn.
 //
 // The kernels are bound by the bytes they move for long inputs (dattn_rope of 16384 tokens of 32
 // heads of 128 out of a fused projection: 41 us, 0.96 of the copy bandwidth) and by latency for
