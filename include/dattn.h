@@ -555,7 +555,8 @@ dattn_status_t dattn_page_select(const dattn_kv_layout *layout, const dattn_bf16
 /*
  * Workspace bytes for dattn_partial (items = C, top_k = 0), dattn_decode (items = B,
  * top_k = 0) and dattn_page_select (items = B, top_k > 0) with the given num_splits
- * (0 = the automatic choice on the current device). Returns 0 for invalid arguments.
+ * (0 = the automatic choice on the current device, for every pool format and length). Returns
+ * 0 for invalid arguments.
  */
 size_t dattn_workspace_size(int32_t items, int32_t Hq, int32_t Hkv, int32_t head_dim,
                             int32_t top_k, int32_t num_splits);
@@ -564,7 +565,10 @@ size_t dattn_workspace_size(int32_t items, int32_t Hq, int32_t Hkv, int32_t head
 dattn_status_t dattn_workspace_init(void *ws, size_t ws_bytes, void *stream);
 
 /* The automatic num_splits for a work size of total_tiles 16-token tiles on the current
- * device: SM count times resident CTAs per SM, capped so a CTA gets at least 16 tiles. */
+ * device: SM count times resident CTAs per SM, capped so a CTA gets at least 16 tiles. A launch
+ * with num_splits = 0 may take more CTAs: it counts each head's fixed cost in tiles too, and over
+ * the block-scaled pool a CTA gets at least 4. So the workspace of such a launch is the one that
+ * dattn_workspace_size gives for num_splits = 0, not for this number. */
 int32_t dattn_auto_splits(int64_t total_tiles);
 
 /* The balanced split: CTA c of G covers tiles [floor(c*W/G), floor((c+1)*W/G)). */

@@ -402,6 +402,9 @@ def dattn_workspace_init(ws: Workspace, stream=None):
 
 
 def dattn_auto_splits(total_tiles: int) -> int:
+    """The automatic split of total_tiles 16-token tiles, 16 to a CTA at least. A launch with
+    num_splits=0 may take more CTAs (KV_FP8_BLOCK: 4 tiles each); size its workspace with
+    num_splits=0."""
     return int(load_library().dattn_auto_splits(total_tiles))
 
 
