@@ -154,27 +154,46 @@ def _check(status: int, what: str):
         raise DattnError(f"{what} failed: {msg}")
 
 
-def _ptr(t):
+def _stream_on(stream, device):
+    """The launch stream's handle: the given stream's, else the device's current one (by the raw
+    getter: building a Stream object costs about as much as the launch)."""
+    return stream.cuda_stream if stream is not None else \
+        torch._C._cuda_getCurrentRawStream(device)
+
+
+def _elsewhere(t, here):
+    if t.get_device() < 0:
+        raise ValueError("expected a CUDA tensor")
+    raise ValueError(f"tensors of {t.device} and cuda:{here} in one call")
+
+
+def _at(t, here):
+    """The pointer of a contiguous tensor on device `here`."""
     if t is None:
         return None
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
+    if t.get_device() != here:
+        _elsewhere(t, here)
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
     return t.data_ptr()
 
 
-def _stream(stream):
-    """The launch stream's handle: the given stream's, else the current device's current one (by
-    the raw getter: building a Stream object costs about as much as the launch)."""
-    if stream is not None:
-        return stream.cuda_stream
-    return _stream_on(None, torch.cuda.current_device())
+def _launch_device(t):
+    """The device of t, which has to be the current one: the launch goes there."""
+    here = t.get_device()
+    if here < 0:
+        raise ValueError("expected a CUDA tensor")
+    if here != torch.cuda.current_device():
+        raise ValueError(f"a tensor of {t.device} in a call on cuda:{torch.cuda.current_device()}")
+    return here
 
 
-def _stream_on(stream, device):
-    return stream.cuda_stream if stream is not None else \
-        torch._C._cuda_getCurrentRawStream(device)
+def _layout_device(layout, t):
+    """The device of a call over `layout`, t's: the current one, with the layout's tensors on it."""
+    here = _launch_device(t)
+    if layout.device != here:
+        _elsewhere(layout.block_table, here)
+    return here
 
 
 def _bf16(t, name):
@@ -271,6 +290,10 @@ class KVLayout:
             self._head_format_c = (ctypes.c_int8 * num_kv_heads)(*self.head_format)
         self.block_table = block_table  # keeps the tensors alive
         self.kv_scale = kv_scale
+        self.device = block_table.get_device()  # (-1: the host's, which no call takes)
+        _at(block_table, self.device)
+        if kv_format in _QUANT:
+            _at(kv_scale, self.device)
         self.c = _Layout(num_pages, num_kv_heads, head_dim, page_size,
                          block_table.data_ptr(), block_table.shape[-1], kv_format,
                          kv_scale.data_ptr() if kv_scale is not None else None,
@@ -397,8 +420,11 @@ def dattn_workspace_size(items, Hq, Hkv, head_dim, top_k=0, num_splits=0) -> int
 
 
 def dattn_workspace_init(ws: Workspace, stream=None):
-    _check(load_library().dattn_workspace_init(_ptr(ws.buffer), ws.buffer.numel(),
-                                               _stream(stream)), "dattn_workspace_init")
+    if ws.buffer.get_device() < 0:
+        raise ValueError("expected a CUDA tensor")
+    _check(load_library().dattn_workspace_init(
+        ws.buffer.data_ptr(), ws.buffer.numel(), _stream_on(stream, torch.cuda.current_device())),
+        "dattn_workspace_init")
 
 
 def dattn_auto_splits(total_tiles: int) -> int:
@@ -437,9 +463,11 @@ def dattn_kv_append(layout: KVLayout, k_pool, v_pool, stats, k_new, v_new, seq_l
     _layout_sizes(layout, B, k_pool, v_pool, stats)
     _size(k_new, B * T * Hkv * d, "k_new"); _size(v_new, B * T * Hkv * d, "v_new")
     _size(seq_lens, B, "seq_lens")
+    here = _layout_device(layout, k_pool)
     _check(load_library().dattn_kv_append(
-        ctypes.byref(layout.c), _ptr(k_pool), _ptr(v_pool), _ptr(stats), _ptr(k_new),
-        _ptr(v_new), B, T, _ptr(seq_lens), _ptr(dev_err), _stream(stream)), "dattn_kv_append")
+        ctypes.byref(layout.c), _at(k_pool, here), _at(v_pool, here), _at(stats, here),
+        _at(k_new, here), _at(v_new, here), B, T, _at(seq_lens, here), _at(dev_err, here),
+        _stream_on(stream, here)), "dattn_kv_append")
 
 
 def _tokens(t, name, here=None):
@@ -464,33 +492,6 @@ def _tokens(t, name, here=None):
     if device < 0 or (here is not None and device != here):
         _elsewhere(t, here)
     return t.data_ptr(), stride if many else H * d
-
-
-def _elsewhere(t, here):
-    if t.get_device() < 0:
-        raise ValueError("expected a CUDA tensor")
-    raise ValueError(f"tensors of {t.device} and cuda:{here} in one call")
-
-
-def _at(t, here):
-    """The pointer of a contiguous tensor on device `here`."""
-    if t is None:
-        return None
-    if t.get_device() != here:
-        _elsewhere(t, here)
-    if not t.is_contiguous():
-        raise ValueError("expected a contiguous tensor")
-    return t.data_ptr()
-
-
-def _launch_device(t):
-    """The device of t, which has to be the current one: the launch goes there."""
-    here = t.get_device()
-    if here < 0:
-        raise ValueError("expected a CUDA tensor")
-    if here != torch.cuda.current_device():
-        raise ValueError(f"a tensor of {t.device} in a call on cuda:{torch.cuda.current_device()}")
-    return here
 
 
 def dattn_rope(rotation: Rotation, x, out, positions, inverse: bool = False, stream=None):
@@ -546,12 +547,11 @@ def dattn_rope_append(layout: KVLayout, k_pool, v_pool, stats, rotation: Rotatio
     _layout_sizes(layout, B, k_pool, v_pool, stats)
     _size(seq_lens, B, "seq_lens"); _size(new_lens, B, "new_lens")
     _size(positions, B * T, "positions")
-    here = _launch_device(k_new)
+    here = _layout_device(layout, k_new)
     if q is not None:
         qp, qs = _tokens(q, "q", here)
     kp, ks = _tokens(k_new, "k_new", here)
     vp, vs = _tokens(v_new, "v_new", here)
-    _at(layout.block_table, here); _at(layout.kv_scale, here)
     _check(load_library().dattn_rope_append(
         ctypes.byref(layout.c), _at(k_pool, here), _at(v_pool, here), _at(stats, here),
         ctypes.byref(rotation.c) if rotation is not None else None, qp, qs, kp, ks, vp, vs, B, T,
@@ -573,11 +573,13 @@ def dattn_partial(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_lens, c
     _size(q, B * Hq * d, "q"); _size(seq_lens, B, "seq_lens")
     _size(chunk_page_indptr, C + 1, "chunk_page_indptr")
     _size(m, C * Hq, "m"); _size(e, C * Hq, "e"); _size(MA, C * Hq * d, "MA")
+    here = _layout_device(layout, k_pool)
     _check(load_library().dattn_partial(
-        ctypes.byref(layout.c), _ptr(k_pool), _ptr(v_pool), _ptr(q), B, Hq, scale,
-        _ptr(seq_lens), C, _ptr(chunk_req), _ptr(chunk_page_indptr), _ptr(chunk_pages),
-        _ptr(m), _ptr(e), _ptr(MA), _ptr(ws.buffer), ws.buffer.numel(), num_splits,
-        _ptr(dev_err), _stream(stream)), "dattn_partial")
+        ctypes.byref(layout.c), _at(k_pool, here), _at(v_pool, here), _at(q, here), B, Hq, scale,
+        _at(seq_lens, here), C, _at(chunk_req, here), _at(chunk_page_indptr, here),
+        _at(chunk_pages, here), _at(m, here), _at(e, here), _at(MA, here), _at(ws.buffer, here),
+        ws.buffer.numel(), num_splits, _at(dev_err, here), _stream_on(stream, here)),
+        "dattn_partial")
 
 
 def dattn_merge(chunk_indptr, m, e, MA, out=None, m_g=None, e_g=None, MA_g=None, dev_err=None,
@@ -592,9 +594,11 @@ def dattn_merge(chunk_indptr, m, e, MA, out=None, m_g=None, e_g=None, MA_g=None,
     _size(m, C * Hq, "m"); _size(e, C * Hq, "e")
     _size(out, B * Hq * d, "out"); _size(m_g, B * Hq, "m_g"); _size(e_g, B * Hq, "e_g")
     _size(MA_g, B * Hq * d, "MA_g")
+    here = _launch_device(MA)
     _check(load_library().dattn_merge(
-        B, C, Hq, d, _ptr(chunk_indptr), _ptr(m), _ptr(e), _ptr(MA), _ptr(out), _ptr(m_g),
-        _ptr(e_g), _ptr(MA_g), _ptr(dev_err), _stream(stream)), "dattn_merge")
+        B, C, Hq, d, _at(chunk_indptr, here), _at(m, here), _at(e, here), _at(MA, here),
+        _at(out, here), _at(m_g, here), _at(e_g, here), _at(MA_g, here), _at(dev_err, here),
+        _stream_on(stream, here)), "dattn_merge")
 
 
 def dattn_merge_gathered(m, e, MA, out=None, m_g=None, e_g=None, MA_g=None, dev_err=None,
@@ -610,9 +614,11 @@ def dattn_merge_gathered(m, e, MA, out=None, m_g=None, e_g=None, MA_g=None, dev_
     _size(m, R * B * Hq, "m"); _size(e, R * B * Hq, "e")
     _size(out, B * Hq * d, "out"); _size(m_g, B * Hq, "m_g"); _size(e_g, B * Hq, "e_g")
     _size(MA_g, B * Hq * d, "MA_g")
+    here = _launch_device(MA)
     _check(load_library().dattn_merge_gathered(
-        B, R, Hq, d, _ptr(m), _ptr(e), _ptr(MA), _ptr(out), _ptr(m_g), _ptr(e_g), _ptr(MA_g),
-        _ptr(dev_err), _stream(stream)), "dattn_merge_gathered")
+        B, R, Hq, d, _at(m, here), _at(e, here), _at(MA, here), _at(out, here), _at(m_g, here),
+        _at(e_g, here), _at(MA_g, here), _at(dev_err, here), _stream_on(stream, here)),
+        "dattn_merge_gathered")
 
 
 def _decode_sizes(layout, B, T, Hq, k_pool, v_pool, q, seq_lens, out, m_g, e_g, sparse):
@@ -633,10 +639,14 @@ def dattn_decode(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_lens, ou
     B, Hq = q.shape[0], q.shape[1]
     _decode_sizes(layout, B, 1, Hq, k_pool, v_pool, q, seq_lens, out, m_g, e_g, sparse)
     sp = ctypes.byref(sparse.c) if sparse is not None else None
+    here = _layout_device(layout, k_pool)
+    if sparse is not None:
+        _at(sparse.head_kind, here); _at(sparse.selected, here); _at(sparse.selected_phys, here)
     _check(load_library().dattn_decode(
-        ctypes.byref(layout.c), _ptr(k_pool), _ptr(v_pool), _ptr(q), B, Hq, scale,
-        _ptr(seq_lens), sp, num_splits, _ptr(ws.buffer), ws.buffer.numel(), _ptr(out),
-        _ptr(m_g), _ptr(e_g), _ptr(dev_err), _stream(stream)), "dattn_decode")
+        ctypes.byref(layout.c), _at(k_pool, here), _at(v_pool, here), _at(q, here), B, Hq, scale,
+        _at(seq_lens, here), sp, num_splits, _at(ws.buffer, here), ws.buffer.numel(),
+        _at(out, here), _at(m_g, here), _at(e_g, here), _at(dev_err, here),
+        _stream_on(stream, here)), "dattn_decode")
 
 
 def dattn_append_decode(layout: KVLayout, k_pool, v_pool, stats, k_new, v_new, q, scale: float,
@@ -658,11 +668,14 @@ def dattn_append_decode(layout: KVLayout, k_pool, v_pool, stats, k_new, v_new, q
     _size(k_new, B * Hkv * d, "k_new"); _size(v_new, B * Hkv * d, "v_new")
     _decode_sizes(layout, B, 1, Hq, k_pool, v_pool, q, seq_lens, out, m_g, e_g, sparse)
     sp = ctypes.byref(sparse.c) if sparse is not None else None
+    here = _layout_device(layout, k_pool)
+    if sparse is not None:
+        _at(sparse.head_kind, here); _at(sparse.selected, here); _at(sparse.selected_phys, here)
     _check(load_library().dattn_append_decode(
-        ctypes.byref(layout.c), _ptr(k_pool), _ptr(v_pool), _ptr(stats), _ptr(k_new),
-        _ptr(v_new), _ptr(q), B, Hq, scale, _ptr(seq_lens), sp, num_splits, _ptr(ws.buffer),
-        ws.buffer.numel(), _ptr(out), _ptr(m_g), _ptr(e_g), _ptr(dev_err), _stream(stream)),
-        "dattn_append_decode")
+        ctypes.byref(layout.c), _at(k_pool, here), _at(v_pool, here), _at(stats, here),
+        _at(k_new, here), _at(v_new, here), _at(q, here), B, Hq, scale, _at(seq_lens, here), sp,
+        num_splits, _at(ws.buffer, here), ws.buffer.numel(), _at(out, here), _at(m_g, here),
+        _at(e_g, here), _at(dev_err, here), _stream_on(stream, here)), "dattn_append_decode")
 
 
 def dattn_decode_multi(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_lens, out,
@@ -674,10 +687,12 @@ def dattn_decode_multi(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_le
     _i32(seq_lens, "seq_lens"); _f32(out, "out")
     B, T, Hq = q.shape[0], q.shape[1], q.shape[2]
     _decode_sizes(layout, B, T, Hq, k_pool, v_pool, q, seq_lens, out, m_g, e_g, None)
+    here = _layout_device(layout, k_pool)
     _check(load_library().dattn_decode_multi(
-        ctypes.byref(layout.c), _ptr(k_pool), _ptr(v_pool), _ptr(q), B, T, Hq, scale,
-        _ptr(seq_lens), num_splits, _ptr(ws.buffer), ws.buffer.numel(), _ptr(out), _ptr(m_g),
-        _ptr(e_g), _ptr(dev_err), _stream(stream)), "dattn_decode_multi")
+        ctypes.byref(layout.c), _at(k_pool, here), _at(v_pool, here), _at(q, here), B, T, Hq,
+        scale, _at(seq_lens, here), num_splits, _at(ws.buffer, here), ws.buffer.numel(),
+        _at(out, here), _at(m_g, here), _at(e_g, here), _at(dev_err, here),
+        _stream_on(stream, here)), "dattn_decode_multi")
 
 
 def dattn_prefill(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_lens, out, m=None,
@@ -695,10 +710,13 @@ def dattn_prefill(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_lens, o
                                                sparse.block_lists.shape[1] < layout.num_kv_heads):
             raise ValueError("block_lists must be int32 [B][Hkv][qblock_stride][max_sel]")
     sp = ctypes.byref(sparse.c) if sparse is not None else None
+    here = _layout_device(layout, k_pool)
+    if sparse is not None:
+        _at(sparse.head_kind, here); _at(sparse.block_lists, here)
     _check(load_library().dattn_prefill(
-        ctypes.byref(layout.c), _ptr(k_pool), _ptr(v_pool), _ptr(q), B, Tq, Hq, scale,
-        _ptr(seq_lens), sp, _ptr(out), _ptr(m), _ptr(e), _ptr(dev_err), _stream(stream)),
-        "dattn_prefill")
+        ctypes.byref(layout.c), _at(k_pool, here), _at(v_pool, here), _at(q, here), B, Tq, Hq,
+        scale, _at(seq_lens, here), sp, _at(out, here), _at(m, here), _at(e, here),
+        _at(dev_err, here), _stream_on(stream, here)), "dattn_prefill")
 
 
 def dattn_decode_noalloc(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_lens, out,
@@ -714,10 +732,13 @@ def dattn_decode_noalloc(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_
     B, Hq = q.shape[0], q.shape[1]
     _decode_sizes(layout, B, 1, Hq, k_pool, v_pool, q, seq_lens, out, m_g, e_g, sparse)
     sp = ctypes.byref(sparse.c) if sparse is not None else None
+    here = _layout_device(layout, k_pool)
+    if sparse is not None:
+        _at(sparse.head_kind, here); _at(sparse.selected, here); _at(sparse.selected_phys, here)
     _check(load_library().dattn_decode_noalloc(
-        ctypes.byref(layout.c), _ptr(k_pool), _ptr(v_pool), _ptr(q), B, Hq, scale,
-        _ptr(seq_lens), sp, num_splits, _ptr(out), _ptr(m_g), _ptr(e_g), _ptr(dev_err),
-        _stream(stream)), "dattn_decode_noalloc")
+        ctypes.byref(layout.c), _at(k_pool, here), _at(v_pool, here), _at(q, here), B, Hq, scale,
+        _at(seq_lens, here), sp, num_splits, _at(out, here), _at(m_g, here), _at(e_g, here),
+        _at(dev_err, here), _stream_on(stream, here)), "dattn_decode_noalloc")
 
 
 def dattn_page_select(layout: KVLayout, stats, q, seq_lens, head_kind, top_k: int, selected,
@@ -735,7 +756,9 @@ def dattn_page_select(layout: KVLayout, stats, q, seq_lens, head_kind, top_k: in
     _size(selected, B * c.num_kv_heads * top_k, "selected")
     if selected_phys is not None:
         _size(selected_phys, B * c.num_kv_heads * top_k, "selected_phys")
+    here = _layout_device(layout, q)
     _check(load_library().dattn_page_select(
-        ctypes.byref(layout.c), _ptr(stats), _ptr(q), B, Hq, _ptr(seq_lens), _ptr(head_kind),
-        top_k, _ptr(selected), _ptr(selected_phys), _ptr(ws.buffer), ws.buffer.numel(),
-        num_splits, _ptr(dev_err), _stream(stream)), "dattn_page_select")
+        ctypes.byref(layout.c), _at(stats, here), _at(q, here), B, Hq, _at(seq_lens, here),
+        _at(head_kind, here), top_k, _at(selected, here), _at(selected_phys, here),
+        _at(ws.buffer, here), ws.buffer.numel(), num_splits, _at(dev_err, here),
+        _stream_on(stream, here)), "dattn_page_select")
