@@ -480,8 +480,8 @@ __device__ __forceinline__ void write_final(const AttnParams& p, int32_t s, int3
 // weights are p_i * 2^15, without a scale and without r: a V scale that a query column does not
 // see, or whose tokens weigh nothing in it, takes no bits from the others. The first
 // tile of a warp, and a tile whose V scale is far above the smallest so far, may count by weights
-// far below 1: what two fp16 terms leave of its weights enters in further products, times 2^20 each
-// time, until nothing is left. (O is kept times 2^-8, so that the largest V scale
+// far below 1: where it has some below 2^-12, what two fp16 terms leave of its weights enters in
+// further products, times 2^20 each time, until nothing is left. (O is kept times 2^-8, so that the largest V scale
 // does not overflow before a larger score makes its weight small.)
 // PK: 2 or 4 query columns over the 4-bit pool, whose PV weights take one product per m-tile
 // (see tile_i4). (A mixed-pool instance would work the same way for its 4-bit heads.)
@@ -870,7 +870,9 @@ struct Consumer {
         if constexpr (BLK) {
             const bool wide = vtile > vlim;  // warp-uniform
             if (vtile > 0.f) vlim = vlim > 0.f ? fminf(vlim, 4096.f * vtile) : 4096.f * vtile;
-            if (wide) {
+            if (wide && __any_sync(0xffffffffu, (w0 > 0.f && w0 < 8.f) || (w1 > 0.f && w1 < 8.f) ||
+                                                    (w2 > 0.f && w2 < 8.f) ||
+                                                    (w3 > 0.f && w3 < 8.f))) {
                 float vf = vtile;
                 for (int pass = 0; pass < 8; ++pass) {  // (8 x 20 bits: all of a weight)
                     pv_f8(vbase, lo, hi, w0, w1, w2, w3, vf);
