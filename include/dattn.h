@@ -93,6 +93,12 @@
  *    So tokens appended in one call and one by one are stored alike but for such codes. A
  *    logical page that holds tokens of a request is that request's alone: pages are shared
  *    between requests only where they are full.
+ *    Taking tokens back (setting seq_lens back, as after rejected draft tokens) leaves what they
+ *    did to a logical page that keeps tokens: its scale stays as they raised it, the earlier
+ *    codes stay rounded to it, and later appends into the page take no smaller one. A page
+ *    whose first token is taken back starts anew. So a rejected token far larger than the others
+ *    of its page leaves them in steps of 2^-9 of its scale; where that matters, append the page's
+ *    tokens again from its first slot.
  *    Compared with a scale per row, a tile carries 8 bytes of scales instead of 128, and a
  *    prefill can read the pool (dattn_prefill). dattn_append_decode does not take this format:
  *    an append may rewrite rows that the same launch reads; call dattn_rope_append or
@@ -500,7 +506,8 @@ typedef struct dattn_prefill_sparse {
  *   DATTN_HEAD_STREAMING: kb < sink_blocks, or qb - local_blocks < kb <= qb;
  *   DATTN_HEAD_RETRIEVAL: the blocks listed in row qb of block_lists (blocks after qb add
  *                         nothing); a query that keeps no key gives out = 0, m = -inf, e = 0.
- * One CTA computes its query blocks over all their key blocks, so no workspace is needed.
+ * A CTA computes its query blocks over all their key blocks, or, for a few tokens over a long
+ * block-scaled context, a cluster of CTAs does through its shared memory: no workspace is needed.
  *
  *   k_pool, v_pool (device) the pool: bf16 or DATTN_KV_FP8_BLOCK (DATTN_ERR_UNSUPPORTED for
  *            the other quantized formats)

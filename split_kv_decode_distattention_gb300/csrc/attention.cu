@@ -481,8 +481,8 @@ __device__ __forceinline__ void write_final(const AttnParams& p, int32_t s, int3
 // see, or whose tokens weigh nothing in it, takes no bits from the others. The first
 // tile of a warp, and a tile whose V scale is far above the smallest so far, may count by weights
 // far below 1: where it has some below 2^-12, what two fp16 terms leave of its weights enters in
-// further products, times 2^20 each time, until nothing is left. (O is kept times 2^-8, so that the largest V scale
-// does not overflow before a larger score makes its weight small.)
+// further products, times 2^20 each time, until nothing is left. (O is kept times 2^-8, so that the
+// largest V scale does not overflow before a larger score makes its weight small.)
 // PK: 2 or 4 query columns over the 4-bit pool, whose PV weights take one product per m-tile
 // (see tile_i4). (A mixed-pool instance would work the same way for its 4-bit heads.)
 template <int D, int FMT, bool PK>
@@ -928,8 +928,8 @@ struct Consumer {
         }
         // The products add into their accumulators rounding towards zero. Over a long piece that
         // shrinks the result (3.9e-6 of it at 8 x 32K tokens of 32 heads), so the block-scaled pool's
-        // tile is summed by itself and added to O, times its V scale, rounding to nearest (3.2e-7; 324
-        // us for 318).
+        // tile is summed by itself and added to O, times its V scale, rounding to nearest (3.2e-7, for
+        // 2% of the time).
         auto pv = [&](float (&acc)[4], uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3) {
             if constexpr (BLK) {
                 float t[4] = {0.f, 0.f, 0.f, 0.f};

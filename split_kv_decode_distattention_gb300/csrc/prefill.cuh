@@ -133,7 +133,7 @@ __device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&r)[32])
         : "memory");
 }
 
-// Packed fp32 pairs (Blackwell's two-wide fp32 FMA and add)
+// Two-wide fp32 arithmetic (pairs as pack_f32x2 of common.cuh makes them)
 // (r0, r1) = (x0, x1) * m + c, m and c packed pairs, each lane rounded once
 __device__ __forceinline__ void fma_f32x2(float x0, float x1, uint64_t m, uint64_t c, float& r0,
                                           float& r1) {

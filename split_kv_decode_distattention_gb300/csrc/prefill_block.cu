@@ -19,7 +19,7 @@
 // What bounds it: the tensor cores, then the softmax's latency. A 64-key block of 128 query rows
 // takes one product S = Q K^T and two products O += P V, 3 x 2 x 128 x 64 x d operations for the
 // 2 x 2 x 128 x 64 x d that count: 2/3 of the dense 16-bit rate at most. Measured: a causal prompt of
-// 32K tokens, 32 query and 8 KV heads of 128, 9.39 ms (939 TFLOP/s counted, 0.49 of the bf16 rate);
+// 32K tokens, 32 query and 8 KV heads of 128, 9.45 ms (933 TFLOP/s counted, 0.48 of the bf16 rate);
 // without the softmax's arithmetic 6.94 ms. A key block is widened once for 256 query rows: one CTA
 // per SM holds two tiles of 128 rows, which work past each other.
 //
@@ -30,7 +30,7 @@
 // (its blocks run one after another, 0.8-1.1 us each) gives each tile a cluster of up to eight CTAs,
 // which share its key blocks and join their sums through shared memory: 64 tokens of 32 heads over 8
 // KV heads of 128 after 32K tokens 562 -> 143 us (clusters of 4), 64 of 8 heads over one KV head after
-// 100K tokens 1597 -> 211 us (8), 39 of 16 heads after 1284 21.4 -> 16.4 us. 15 warps:
+// 100K tokens 1593 -> 211 us (8), 39 of 16 heads after 1284 21.6 -> 17.2 us. 15 warps:
 //   0-3, 4-7  one query row per thread of tile 0, 1: the softmax. (Two threads per row took 11% longer:
 //             the second's share of the fixed work costs more than its latency saves.)
 //   8-11      load codes, widen them and write the K and V stages in the 128-byte-swizzled layout
@@ -61,10 +61,12 @@ constexpr int kPbStages = 3;                // K stages, and V stages
 constexpr int kPbGroup = 8;                 // key blocks that warp 14 resolves at once
 constexpr int kPbRing = 2 * kPbGroup;       // the blocks' ring
 // Key blocks between two emptyings of an accumulator: 256 products that each lose up to 2^-24 of the
-// sum, 4.4e-6 of the result measured. (16: 2.2e-6 for 11% more time on a 32K prompt.)
+// sum, 4.3e-6 of the result measured after 28K tokens. (16: 2.2e-6 for 11% more time on a 32K prompt.)
 constexpr int kPbWindow = 32;
-constexpr int kPbSplitBlocks = 3;           // key blocks of a CTA at least, where a cluster shares
-                                            // a tile (2 cost more where it would, 4 gave 2 us less)
+// Key blocks of a CTA at least, where a cluster shares a tile. With 2, 3 and 4: 17.6, 14.3 and 14.2 us
+// for 4 x 75 tokens after 90-700 (d = 64), 17.2, 17.2 and 19.5 for 39 after 1284, 10.9, 12.6 and 12.6
+// for 9 after 882.
+constexpr int kPbSplitBlocks = 3;
 // A row's reference m + x (log2 units): its largest weight is 2^kPbTop when the reference is set, and a
 // weight above 2^kPbMost sets it anew (both terms are fp16: below 2^16). With 12 more keys set it anew:
 // 4096 tokens after 28K took 2580 us, 2405 with 9.

@@ -791,10 +791,10 @@ RotArgs rot_args(const dattn_rotation* rot) {
     return r;
 }
 
-// CTAs that share the heads of a window: about eight CTAs per SM in all (near three waves; 2 to 12
-// measured: 44.1 us at 4, 42.3 at 8 and 12 for 16384 tokens of 32 heads, 38.1, 38.7 and 41.0 us
-// for an append of 2 x 4093 tokens, where a window makes its table once per slice), a head each
-// at least.
+// CTAs that share the heads of a window: about eight CTAs per SM in all (near three waves), a head
+// each at least. 2, 4, 8 and 12 per SM measured: 42.9, 42.9, 41.5 and 41.5 us for 16384 tokens of 32
+// heads; 39.0, 34.6, 33.9 and 35.5 us for an append of 2 x 4093 tokens, where a window makes its
+// table once per slice.
 int32_t head_slices(int64_t windows, int32_t heads) {
     const int64_t want = (8 * (int64_t)sm_count_current() + windows - 1) / windows;
     const int64_t most = (heads + kRopeWarps - 1) / kRopeWarps;
