@@ -478,11 +478,11 @@ __device__ __forceinline__ void write_final(const AttnParams& p, int32_t s, int3
 // brings 16 bytes of scales (a bulk copy's least) instead of 128, and its weighted sum, which is
 // taken by itself (see tile_f8), is multiplied by the V scale as it is added to O in fp32. So its
 // weights are p_i * 2^15, without a scale and without r: a V scale that a query column does not
-// see, or whose tokens weigh nothing in it, takes no bits from the others. The first
-// tile of a warp, and a tile whose V scale is far above the smallest so far, may count by weights
-// far below 1: where it has some below 2^-12, what two fp16 terms leave of its weights enters in
-// further products, times 2^20 each time, until nothing is left. (O is kept times 2^-8, so that the
-// largest V scale does not overflow before a larger score makes its weight small.)
+// see, or whose tokens weigh nothing in it, takes no bits from the others. The two terms hold a
+// weight below 2^-12 to 2^-40 only. Where that could show beside the sums so far (the heavier tokens'
+// V is zeros or far smaller), what they leave of the tile's weights enters in further products, times
+// 2^20 each time, until nothing is left. (O is kept times 2^-8, so that the largest V scale does not
+// overflow before a larger score makes its weight small.)
 // PK: 2 or 4 query columns over the 4-bit pool, whose PV weights take one product per m-tile
 // (see tile_i4). (A mixed-pool instance would work the same way for its 4-bit heads.)
 template <int D, int FMT, bool PK>
@@ -506,7 +506,9 @@ struct Consumer {
                    // current piece's query
     int32_t rk;    // 8-bit pool: r = 2^rk bounds the V scales seen in this piece
     float rv, inv;  // 8-bit pool: r and 2^15 / r
-    float vlim;     // block-scaled pool: 2^12 times the smallest nonzero V scale of this piece so far
+    // block-scaled pool: what the largest element of every column of O was at least, since the maxima
+    // were last raised (terms_show)
+    float olow;
     bool i4 = I4;   // the current piece's KV head is 4-bit (set per piece in a mixed pool)
     // 4-bit pool: 8 * 2^-24 * (sum of the query) of this lane's columns 2tig, 2tig + 1, and
     // the running sums of this lane's PV weights of those columns (see tile_i4)
@@ -719,7 +721,7 @@ struct Consumer {
         rk = -112;
         rv = __int_as_float((127 - 112) << 23);
         inv = __int_as_float((142 + 112) << 23);
-        vlim = 0.f;
+        olow = 0.f;
     }
 
     // Online softmax (base 2) over one tile's logits: rows g8 (s0, s1) and g8 + 8 (s2, s3),
@@ -754,6 +756,7 @@ struct Consumer {
                 ws0 *= al0;
                 ws1 *= al1;
             }
+            if constexpr (BLK) olow = 0.f;
             if constexpr (Q) {
                 if (p.gq == 1) alo = al0;  // column 1 holds column 0's lo terms (g1_weights)
             }
@@ -868,14 +871,15 @@ struct Consumer {
         const float vn0 = BLK ? 32768.f : vs0 * inv, vn1 = BLK ? 32768.f : vs1 * inv;
         float w0 = p0 * vn0, w1 = p1 * vn0, w2 = p2 * vn1, w3 = p3 * vn1;
         if constexpr (BLK) {
-            const bool wide = vtile > vlim;  // warp-uniform
-            if (vtile > 0.f) vlim = vlim > 0.f ? fminf(vlim, 4096.f * vtile) : 4096.f * vtile;
-            if (wide && __any_sync(0xffffffffu, (w0 > 0.f && w0 < 8.f) || (w1 > 0.f && w1 < 8.f) ||
-                                                    (w2 > 0.f && w2 < 8.f) ||
-                                                    (w3 > 0.f && w3 < 8.f))) {
+            // the smallest weight but 0 (as bits, less one) against 2^3, 2^-12 of the largest
+            const uint32_t low = min(min(__float_as_uint(w0) - 1u, __float_as_uint(w1) - 1u),
+                                     min(__float_as_uint(w2) - 1u, __float_as_uint(w3) - 1u));
+            if (__any_sync(0xffffffffu, low < 0x40ffffffu) && 1024.f * vtile > olow &&
+                terms_show(vtile)) {
                 float vf = vtile;
                 for (int pass = 0; pass < 8; ++pass) {  // (8 x 20 bits: all of a weight)
                     pv_f8(vbase, lo, hi, w0, w1, w2, w3, vf);
+                    if (!terms_show(vf)) break;
                     vf *= 9.5367431640625e-07f;  // 2^-20
                     w0 = rest_of(w0);
                     w1 = rest_of(w1);
@@ -960,6 +964,24 @@ struct Consumer {
             e4m3x4_to_f16(r3, a2, a3);
             pv(o[2 * c + 1], a0, a1, a2, a3);
         }
+    }
+
+    // Whether what two fp16 terms leave of 16 weights, 2^-25 each, times the largest code and vf could
+    // exceed 2^-22 of the largest element of a column of O (16 * 2^-25 * 448 < 2^-12).
+    __device__ __forceinline__ bool terms_show(float vf) {
+        float a = 0.f, b = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < KS; ++mt) {
+            a = fmaxf(a, fmaxf(fabsf(o[mt][0]), fabsf(o[mt][2])));
+            b = fmaxf(b, fmaxf(fabsf(o[mt][1]), fabsf(o[mt][3])));
+        }
+        a = warp_vmax(a);
+        b = warp_vmax(b);
+        const int c = 2 * (lane & 3);
+        olow = fminf(c < p.gq ? a : -kNegInf, c + 1 < p.gq ? b : -kNegInf);
+        olow = fminf(olow, __shfl_xor_sync(0xffffffffu, olow, 1));
+        olow = fminf(olow, __shfl_xor_sync(0xffffffffu, olow, 2));
+        return 1024.f * vf > olow;
     }
 
     // What the two fp16 terms of w leave of it (exact; 2^-7 at most for w in [0, 2^15]), times 2^20.

@@ -227,8 +227,9 @@ def test_prefill_after_a_taken_back_outlier(size):
 
 
 # ---------------------------------------------------------------- decode
-# A weight is exact to 2^-40 of the largest of its warp, and to 24 bits where its tile's V scale is 2^12
-# times the smallest that the warp has taken in, or the first: in the bound's terms 2^-28 for 2^-33.
+# A weight is right to 22 bits, or to 2^-40 of the largest of its warp where the tile's part of that
+# cannot exceed 2^-22 of the sums so far: the t of 16 keys, 2^-23 and 2^-23, holds it for the products
+# of a tile. (In the bound's terms 2^-28 for 2^-33, where V scales are within 2^12 of each other.)
 DECODE = 2.0 ** -28
 
 
@@ -296,3 +297,35 @@ def test_decode_of_large_values_that_weigh_little(Hq, splits, drop):
     torch.cuda.synchronize()
     assert int(cache.dev_err.item()) == 0
     _check(cache, [L] * B, q, out[:, None], m[:, None], e[:, None], step=DECODE)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,d,splits", [(1, 2, 2, 128, 1), (1, 16, 2, 128, 0), (2, 8, 2, 64, 1),
+                                               (8, 2, 2, 128, 3)])
+@pytest.mark.parametrize("every,size", [(5, 0.0), (1, 0.0), (5, 2.0 ** -30), (16, 2.0 ** -30)])
+def test_heavy_tokens_without_values(T, Hq, Hkv, d, splits, every, size):
+    """Every fifth token, one of each tile, or only the first (every = 1) scores 20 above the others and
+    has a V of zeros or of 2^-30 of theirs: the others' small weights make the result."""
+    L, B = 1500, 2
+    case = W.Case("heavy", B=B, Hq=Hq, Hkv=Hkv, d=d, P=32, lens=[0] * B, seed=3, reserve_tokens=L,
+                  scale=1.0)
+    cache = _cache(case)
+    k, v = _rows((B, L, Hkv, d), 31) * 0.125, _rows((B, L, Hkv, d), 32)
+    k[..., 0] = 0.0
+    heavy = slice(0, 1) if every == 1 else slice(0, L, every)
+    k[:, heavy, :, 0] = 10.0
+    v[:, heavy] *= size
+    cache.append(k, v)
+    q = _rows((B, T, Hq, d), 33)
+    q[..., 0] = 2.0
+    out = torch.empty(B, T, Hq, d, device=DEV)
+    m, e = torch.empty(B, T, Hq, device=DEV), torch.empty(B, T, Hq, device=DEV)
+    ws = cache.workspace(queries=T, num_splits=splits)
+    if T == 1:
+        cache.decode(q[:, 0].contiguous(), out, ws, m, e, num_splits=splits)
+    else:
+        cache.decode(q, out, ws, m, e, num_splits=splits)
+    torch.cuda.synchronize()
+    assert int(cache.dev_err.item()) == 0
+    _check(cache, [L] * B, q, out, m, e, step=DECODE)
+    out, m, e = _prefill(cache, q)
+    _check(cache, [L] * B, q, out, m, e)
