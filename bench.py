@@ -279,7 +279,7 @@ def measured_peak():
 
 
 # the sources that build the decode (prefill) kernel and choose its launch configuration
-DECODE_SOURCES = ("abi.cu", "attention.cu", "common.cuh", "internal.h")
+DECODE_SOURCES = ("abi.cu", "attention.cu", "attention.cuh", "common.cuh", "internal.h")
 PREFILL_SOURCES = ("abi.cu", "prefill.cu", "common.cuh", "internal.h")
 
 

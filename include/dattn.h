@@ -316,6 +316,30 @@ dattn_status_t dattn_rope_append(const dattn_kv_layout *layout, void *k_pool, vo
                                  void *stream);
 
 /*
+ * Reads tokens of the cache back into dense rows: to move a request to another instance, to store
+ * it in another format, or for code that knows no pages. Row n of the outputs, with
+ * out_indptr[b] <= n < out_indptr[b+1], is token starts[b] + n - out_indptr[b] of request b.
+ *
+ *   out_indptr (device) int32 [B+1], ascending from >= 0; rows that it leaves out stay as they are
+ *   starts     (device, nullable) int32 [B]: NULL: every request from its first token
+ *   seq_lens   (device) int32 [B]
+ *   N          rows that k_out and v_out hold; rows from N on are not written
+ *   k_out, v_out (device, either may be NULL) bf16, or fp32 when out_f32 = 1; row n's heads are
+ *              Hkv * d consecutive elements at n * k_stride (v_stride) elements. A value is
+ *              code * scale, rounded to fp32, then to bf16; a bf16 pool's values come as they are.
+ * A token that is not in the request (starts[b] < 0, or the token at or beyond seq_lens[b] or the
+ * block table) is flagged with DATTN_DEVERR_LEN_OOB, one on an unmapped page or a page outside the
+ * pool with that page's bit, bounds out of order with DATTN_DEVERR_CHUNK_OOB where the call meets
+ * them; their rows stay as they are. Pointers are 16-byte aligned, strides multiples of 16 bytes.
+ * Every pool format; N <= 2^30.
+ */
+dattn_status_t dattn_kv_read(const dattn_kv_layout *layout, const void *k_pool,
+                             const void *v_pool, int32_t B, const int32_t *out_indptr,
+                             const int32_t *starts, const int32_t *seq_lens, int32_t N,
+                             void *k_out, int64_t k_stride, void *v_out, int64_t v_stride,
+                             int32_t out_f32, int32_t *dev_err, void *stream);
+
+/*
  * MicroAttention partials over explicit chunks of pages [IL, DistAttention 的等价数学变换].
  * Chunk c covers the request-relative pages
  * chunk_pages[chunk_page_indptr[c] .. chunk_page_indptr[c+1]) of request chunk_req[c].
@@ -429,6 +453,26 @@ dattn_status_t dattn_decode_multi(const dattn_kv_layout *layout, const void *k_p
                                   int32_t Hq, float scale, const int32_t *seq_lens,
                                   int32_t num_splits, void *ws, size_t ws_bytes, float *out,
                                   float *m_g, float *e_g, int32_t *dev_err, void *stream);
+
+/*
+ * Multi-query decode through a sliding window with first tokens that stay visible. As in
+ * dattn_decode_multi the T query tokens of request b are the last T of its L_b tokens; query token
+ * t, at position p = L_b - T + t, attends the tokens i <= p with i > p - window or i < sinks (one
+ * that sees no token gives out = 0, m = -inf, e = 0). With T = 1 that is what a streaming head of
+ * dattn_decode attends; window >= L_b is dattn_decode_multi. Every pool format; the tokens that a
+ * request's queries see are read once for all of them.
+ *
+ *   window   tokens of the window, the query's own the last: >= 1;  sinks >= 0
+ *   out      (device) fp32, or bf16 when out_bf16 = 1, [B][T][Hq][d], 16-byte aligned
+ *   q, seq_lens, m_g, e_g, num_splits, ws, ws_bytes  as for dattn_decode_multi
+ * A length below 0 or beyond the block table is flagged with DATTN_DEVERR_LEN_OOB and clamped.
+ */
+dattn_status_t dattn_decode_window(const dattn_kv_layout *layout, const void *k_pool,
+                                   const void *v_pool, const dattn_bf16 *q, int32_t B, int32_t T,
+                                   int32_t Hq, float scale, const int32_t *seq_lens,
+                                   int32_t window, int32_t sinks, int32_t num_splits, void *ws,
+                                   size_t ws_bytes, void *out, int32_t out_bf16, float *m_g,
+                                   float *e_g, int32_t *dev_err, void *stream);
 
 /*
  * One decode step with its append, in one launch: exactly dattn_kv_append of one new token

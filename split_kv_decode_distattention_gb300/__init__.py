@@ -15,6 +15,8 @@ Entry points, with the same names as in include/dattn.h:
   dattn_decode_multi fused decode of T new query tokens per request, causal over them
   dattn_page_select  page scoring and top-K selection for retrieval heads
   dattn_prefill      block-sparse prefill of a chunk of new tokens (64-token key blocks)
+  dattn_decode_window  fused decode of T query tokens through a sliding window with sinks
+  dattn_kv_read      tokens of the cache read back into dense rows
   dattn_rope         rotary positions of queries or keys, and their gradient
   dattn_rope_append  the append with the rotation of queries and keys applied on the way
 """
@@ -30,7 +32,7 @@ __all__ = [
     "KVLayout", "SparseConfig", "DattnError", "load_library", "library_path",
     "dattn_kv_append", "dattn_partial", "dattn_merge", "dattn_decode", "dattn_page_select",
     "dattn_append_decode", "dattn_merge_gathered", "dattn_rope", "dattn_rope_append",
-    "dattn_rope_frequencies", "Rotation",
+    "dattn_rope_frequencies", "Rotation", "dattn_decode_window", "dattn_kv_read",
     "dattn_decode_noalloc", "dattn_decode_multi", "dattn_prefill", "PrefillSparseConfig",
     "dattn_workspace_size", "dattn_workspace_init", "dattn_auto_splits", "dattn_split_range",
     "dattn_split_owner", "dattn_status_string", "dattn_version", "Workspace",
@@ -104,6 +106,10 @@ _SIGS = {
                                 _SZ, _P, _P, _P, _P, _P]),
     "dattn_prefill": (_I, [ctypes.POINTER(_Layout), _P, _P, _P, _I, _I, _I, _F, _P,
                            ctypes.POINTER(_PrefillSparse), _P, _P, _P, _P, _P]),
+    "dattn_decode_window": (_I, [ctypes.POINTER(_Layout), _P, _P, _P, _I, _I, _I, _F, _P, _I, _I,
+                                 _I, _P, _SZ, _P, _I, _P, _P, _P, _P]),
+    "dattn_kv_read": (_I, [ctypes.POINTER(_Layout), _P, _P, _I, _P, _P, _P, _I, _P, _I64, _P, _I64,
+                           _I, _P, _P]),
     "dattn_rope_frequencies": (_I, [_I, _F, _I, _F, _F, _F, _F, _P]),
     "dattn_rope_turns": (_I, [_I, _P, _P]),
     "dattn_rope": (_I, [ctypes.POINTER(_Rotation), _P, _I64, _P, _I64, _I, _I, _I, _I, _P, _I,
@@ -693,6 +699,70 @@ def dattn_decode_multi(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_le
         scale, _at(seq_lens, here), num_splits, _at(ws.buffer, here), ws.buffer.numel(),
         _at(out, here), _at(m_g, here), _at(e_g, here), _at(dev_err, here),
         _stream_on(stream, here)), "dattn_decode_multi")
+
+
+def _out_bf16(out) -> bool:
+    """Whether the attention's output is bf16 (else it is float32)."""
+    if out.dtype != torch.float32 and out.dtype != torch.bfloat16:
+        raise TypeError("out must be float32 or bfloat16")
+    return out.dtype == torch.bfloat16
+
+
+def dattn_decode_window(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_lens, window: int,
+                        sinks: int, out, ws: Workspace, m_g=None, e_g=None, num_splits=0,
+                        dev_err=None, stream=None):
+    """dattn_decode_multi through a sliding window: the query at position p (q bf16 [B][T][Hq][d],
+    the last T tokens of each request) attends tokens i <= p with i > p - window or i < sinks. out
+    float32 or bf16 [B][T][Hq][d] (+ m_g, e_g fp32 [B][T][Hq]); the workspace as for
+    dattn_decode_multi."""
+    _pool(layout, k_pool, "k_pool"); _pool(layout, v_pool, "v_pool"); _bf16(q, "q")
+    _i32(seq_lens, "seq_lens"); _f32(m_g, "m_g"); _f32(e_g, "e_g")
+    bf16 = _out_bf16(out)
+    if q.dim() != 4:
+        raise ValueError("q must be bf16 [B][T][Hq][d]")
+    B, T, Hq = q.shape[0], q.shape[1], q.shape[2]
+    _decode_sizes(layout, B, T, Hq, k_pool, v_pool, q, seq_lens, out, m_g, e_g, None)
+    here = _layout_device(layout, k_pool)
+    _check(load_library().dattn_decode_window(
+        ctypes.byref(layout.c), _at(k_pool, here), _at(v_pool, here), _at(q, here), B, T, Hq,
+        scale, _at(seq_lens, here), window, sinks, num_splits, _at(ws.buffer, here),
+        ws.buffer.numel(), _at(out, here), bf16, _at(m_g, here), _at(e_g, here),
+        _at(dev_err, here), _stream_on(stream, here)), "dattn_decode_window")
+
+
+def dattn_kv_read(layout: KVLayout, k_pool, v_pool, k_out, v_out, out_indptr, seq_lens,
+                  starts=None, dev_err=None, stream=None):
+    """Read tokens of the cache back: row n of k_out and v_out (bf16 or float32 [N][Hkv][d], evenly
+    spaced tokens with packed heads; either may be None), out_indptr[b] <= n < out_indptr[b+1], is
+    token starts[b] + n - out_indptr[b] of request b (out_indptr int32 [B+1]; starts int32 [B],
+    None: from the first token). Other rows, and rows of tokens that the request or the pool does
+    not hold, stay as they are."""
+    _pool(layout, k_pool, "k_pool"); _pool(layout, v_pool, "v_pool")
+    _i32(out_indptr, "out_indptr"); _i32(seq_lens, "seq_lens"); _i32(starts, "starts")
+    any_out = k_out if k_out is not None else v_out
+    if any_out is None:
+        raise ValueError("k_out or v_out is needed")
+    f32 = any_out.dtype == torch.float32
+    if not f32 and any_out.dtype != torch.bfloat16:
+        raise TypeError("k_out and v_out must both be bfloat16 or both float32")
+    if out_indptr.dim() != 1 or out_indptr.shape[0] < 1:
+        raise ValueError("out_indptr must be int32 [B + 1]")
+    B, Hkv, d = out_indptr.shape[0] - 1, layout.num_kv_heads, layout.head_dim
+    N = any_out.shape[0] if any_out.dim() == 3 else -1
+    here = _layout_device(layout, k_pool)
+    outs = []
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is not None and (t.dim() != 3 or tuple(t.shape) != (N, Hkv, d)):
+            raise ValueError(f"{name} must be [N][Hkv][d]")
+        if t is not None and t.dtype != any_out.dtype:
+            raise TypeError("k_out and v_out must both be bfloat16 or both float32")
+        outs += _tokens(t, name, here) if t is not None else (None, 0)
+    _layout_sizes(layout, B, k_pool, v_pool)
+    _size(seq_lens, B, "seq_lens"); _size(starts, B, "starts")
+    _check(load_library().dattn_kv_read(
+        ctypes.byref(layout.c), _at(k_pool, here), _at(v_pool, here), B, _at(out_indptr, here),
+        _at(starts, here), _at(seq_lens, here), N, *outs, f32, _at(dev_err, here),
+        _stream_on(stream, here)), "dattn_kv_read")
 
 
 def dattn_prefill(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_lens, out, m=None,

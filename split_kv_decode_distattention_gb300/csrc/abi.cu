@@ -32,7 +32,7 @@ namespace {
 
 std::atomic<int> g_sm_count[kMaxDevices];
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace
 
 // Shape checks shared by every call that reads the pool.
 dattn_status_t check_layout(const dattn_kv_layout* L) {
@@ -64,8 +64,6 @@ dattn_status_t check_heads(const dattn_kv_layout* L, int32_t B, int32_t Hq) {
     if (B > kMaxItems) return DATTN_ERR_UNSUPPORTED;
     return DATTN_OK;
 }
-
-}  // namespace
 
 dattn_status_t head_formats(const dattn_kv_layout& L, KvHeadFormats& f) {
     f = KvHeadFormats{};

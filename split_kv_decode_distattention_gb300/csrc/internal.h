@@ -54,7 +54,7 @@ __host__ __device__ constexpr int32_t seg_cost(int32_t fmt, int32_t gq) {
     return fmt == DATTN_KV_FP8_BLOCK ? 12 + 2 * gq : 6;
 }
 
-enum AttnMode : int { MODE_PARTIAL = 0, MODE_DENSE = 1, MODE_SPARSE = 2 };
+enum AttnMode : int { MODE_PARTIAL = 0, MODE_DENSE = 1, MODE_SPARSE = 2, MODE_WINDOW = 3 };
 
 // The per-KV-head formats of a mixed pool: bit h of i4 is set when KV head h is 4-bit (else
 // 8-bit); h4 heads are 4-bit. A head's row within its region uses its index among the heads
@@ -137,6 +137,15 @@ struct AttnParams {
     int32_t fmt;
     const float* kv_scale;
     KvHeadFormats hf;  // DATTN_KV_MIXED: the per-head formats
+    // the windowed mode (with `sinks` above): tokens that a query sees, itself the last; and in
+    // dattn_decode_shared the groups of requests (0: none) whose first prefix_lens[g] tokens are
+    // attended elsewhere
+    int32_t window;
+    int32_t groups;
+    const int32_t* group_indptr;  // [groups + 1]
+    const int32_t* prefix_lens;   // [groups]
+    int32_t normalise;            // 0: out is MA; 1: out is the attention
+    int32_t out_bf16;             // out holds bf16 values (16-byte aligned)
 };
 
 // Floats of one workspace slot (a piece's partial): MA [g][D], then m [g] and e [g],
@@ -158,7 +167,8 @@ struct AttnSmem {
 constexpr int kAplanScalars = 8;
 
 __host__ __device__ inline AttnSmem attn_smem_layout(int D, int g, int nitems, int Hkv,
-                                                     bool sparse, int fmt, bool append = false) {
+                                                     bool sparse, int fmt, bool append = false,
+                                                     bool window = false) {
     AttnSmem s;
     const uint32_t ns = (uint32_t)attn_stages(fmt);
     s.nstages = ns;
@@ -178,7 +188,7 @@ __host__ __device__ inline AttnSmem attn_smem_layout(int D, int g, int nitems, i
     o = (o + 15u) & ~15u;
     s.item_start = o;  o += (uint32_t)(nitems + 1) * 4u;
     s.item_len = o;    o += (uint32_t)nitems * 4u;
-    s.item_pos = o;    o += append ? (uint32_t)nitems * 4u : 0u;
+    s.item_pos = o;    o += append || window ? (uint32_t)nitems * 4u : 0u;
     o = (o + 15u) & ~15u;
     // fused append to a quantized pool: each consumer lane's codes and scale of the new row
     s.qrow = o;        o += (append && fmt != DATTN_KV_BF16) ? kConsumerWarps * 32u * 3u * 4u : 0u;
@@ -213,6 +223,16 @@ dattn_status_t launch_rope_append(const dattn_kv_layout& L, void* k_pool, void* 
 dattn_status_t launch_attention(const AttnParams& p, const void* k_pool, const void* v_pool,
                                 int D, int32_t num_splits, void* ws, size_t ws_bytes,
                                 cudaStream_t stream, int64_t tiles_bound);
+
+// The engine's windowed mode (attention_window.cu): p.mode is MODE_WINDOW.
+dattn_status_t launch_attention_window(const AttnParams& p, const void* k_pool, const void* v_pool,
+                                       int D, int32_t num_splits, void* ws, size_t ws_bytes,
+                                       cudaStream_t stream, int64_t tiles_bound);
+
+// The checks of arguments that the entry points share (abi.cu).
+dattn_status_t check_layout(const dattn_kv_layout* L);
+dattn_status_t check_heads(const dattn_kv_layout* L, int32_t B, int32_t Hq);
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Launches kernel<<<grid, block, smem, stream>>>(args...) with programmatic stream
 // serialization, so that its launch and prologue overlap the previous kernel on the stream.

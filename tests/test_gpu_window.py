@@ -1,0 +1,170 @@
+"""The sliding window with first tokens that stay visible (dattn_decode_window, dattn_prefill_window)
+against its definition in 64 bits: the query at position p sees the keys i <= p with i > p - window or
+i < sinks."""
+import numpy as np
+import pytest
+import torch
+
+from _block_ref import attention
+from _paged import FORMATS, Paged, bf16, check, weight_error
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+OVER = 1 << 30
+
+
+@pytest.fixture(scope="module")
+def dattn():
+    import split_kv_decode_distattention_gb300 as dattn
+    dattn.load_library()
+    return dattn
+
+
+def sees(L, T, window, sinks):
+    """[T][L]: which keys the last T tokens see."""
+    p = np.arange(L - T, L)[:, None]
+    i = np.arange(L)[None]
+    return (i <= p) & ((i > p - window) | (i < sinks))
+
+
+def check_all(pool, q, out, m, e, scale, window, sinks, what):
+    B, T, Hq, d = q.shape
+    g = Hq // pool.Hkv
+    qn = q.double().cpu().numpy()
+    for b in range(B):
+        L = pool.lens[b]
+        see = sees(L, T, window, sinks)
+        K, V = pool.rows("k", b), pool.rows("v", b)
+        for h in range(Hq):
+            ref, rm, re, bound, t = attention(qn[b, :, h], K[:, h // g], V[:, h // g], scale, see,
+                                              weight_error(pool.fmt))
+            check(out[b, :, h], None if m is None else m[b, :, h], None if e is None else e[b, :, h],
+                  ref, bound, t, rm, re, f"{what} b={b} h={h} L={L}")
+
+
+def queries(B, T, Hq, d, seed):
+    return bf16(np.random.default_rng(seed).standard_normal((B, T, Hq, d))).to(DEV)
+
+
+STEPS = [
+    # (lens, T, Hq, Hkv, d, P, window, sinks)
+    ([1, 5, 16, 17, 40, 0], 1, 4, 4, 128, 16, 7, 2),
+    ([2000, 33, 515], 2, 8, 2, 128, 16, 100, 4),       # windows on no tile boundary
+    ([2000, 33, 515], 2, 8, 2, 128, 64, 96, 16),       # and on one
+    ([3, 1, 8, 700, 129], 8, 2, 2, 64, 16, 1, 0),      # a window of the token itself, lengths below T
+    ([3, 1, 8, 700, 129], 8, 2, 2, 64, 16, 3, 1),
+    ([900, 64], 4, 4, 2, 64, 32, OVER, 5),             # no window: all tokens
+    ([900, 64], 3, 4, 2, 128, 32, 20, OVER),           # all tokens are first tokens
+    ([1500, 70, 90], 1, 16, 2, 128, 128, 64, 17),      # sinks that end inside a tile; g = 8
+    ([300, 301, 302, 303, 304, 305], 4, 6, 3, 64, 16, 13, 3),
+]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("case", range(len(STEPS)))
+def test_step_against_the_definition(dattn, fmt, case):
+    lens, T, Hq, Hkv, d, P, window, sinks = STEPS[case]
+    pool = Paged(fmt, lens, Hkv, d, P, seed=case)
+    lay, (kp, vp) = pool.layout(dattn), pool.pools()
+    B = len(lens)
+    q = queries(B, T, Hq, d, case + 50)
+    L = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    ws = dattn.Workspace(B, T * Hq, Hkv, d)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    scale = d ** -0.5
+    for dtype, splits in ((torch.float32, 0), (torch.bfloat16, 5)):
+        if splits:
+            ws = dattn.Workspace(B, T * Hq, Hkv, d, num_splits=splits)
+        out = torch.full((B, T, Hq, d), 9.0, dtype=dtype, device=DEV)
+        m, e = (torch.full((B, T, Hq), 9.0, device=DEV) for _ in range(2))
+        dattn.dattn_decode_window(lay, kp, vp, q, scale, L, window, sinks, out, ws, m, e,
+                                  num_splits=splits, dev_err=err)
+        assert int(err) == 0
+        # (a query before the first token sees nothing: L < T)
+        check_all(pool, q, out, m, e, scale, window, sinks, f"{fmt} splits={splits}")
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_step_without_a_window_is_the_multi_query_decode(dattn, fmt):
+    lens, T, Hq, Hkv, d = [1003, 17, 250], 2, 8, 2, 128
+    pool = Paged(fmt, lens, Hkv, d, 16, seed=3)
+    lay, (kp, vp) = pool.layout(dattn), pool.pools()
+    q = queries(3, T, Hq, d, 4)
+    L = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    ws = dattn.Workspace(3, T * Hq, Hkv, d)
+    a, b = (torch.empty(3, T, Hq, d, device=DEV) for _ in range(2))
+    dattn.dattn_decode_multi(lay, kp, vp, q, 0.1, L, a, ws, num_splits=3)
+    dattn.dattn_decode_window(lay, kp, vp, q, 0.1, L, 5000, 0, b, ws, num_splits=3)
+    assert torch.equal(a, b)
+
+
+def test_step_of_one_token_is_what_a_streaming_head_attends(dattn):
+    lens, Hq, Hkv, d = [1003, 17, 250, 0], 8, 2, 128
+    pool = Paged("fp8", lens, Hkv, d, 16, seed=3)
+    lay, (kp, vp) = pool.layout(dattn), pool.pools()
+    q = queries(4, 1, Hq, d, 4)
+    L = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    ws = dattn.Workspace(4, Hq, Hkv, d)
+    kind = torch.full((Hkv,), dattn.HEAD_STREAMING, dtype=torch.int8, device=DEV)
+    a, b = (torch.empty(4, 1, Hq, d, device=DEV) for _ in range(2))
+    dattn.dattn_decode(lay, kp, vp, q[:, 0], 0.1, L, a, ws,
+                       sparse=dattn.SparseConfig(kind, 4, 33, 0, None))
+    dattn.dattn_decode_window(lay, kp, vp, q, 0.1, L, 33, 4, b, ws)
+    # the same keys, split and summed in another order (fp32 sums of weights within 2^-22)
+    assert (a - b).abs().max() < 1e-4
+
+
+def test_step_flags_bad_lengths_and_pages(dattn):
+    pool = Paged("bf16", [100, 100, 100], 2, 64, 16, seed=1)
+    pool.table[1, 6] = -1
+    pool.table[2, 5] = pool.pages
+    lay, (kp, vp) = pool.layout(dattn), pool.pools()
+    q = queries(3, 1, 4, 64, 1)
+    L = torch.tensor([-3, 100, 100], dtype=torch.int32, device=DEV)
+    ws = dattn.Workspace(3, 4, 2, 64)
+    out = torch.full((3, 1, 4, 64), 9.0, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    dattn.dattn_decode_window(lay, kp, vp, q, 0.1, L, 40, 0, out, ws, dev_err=err)
+    E = dattn.DEVERR
+    assert int(err) == E["LEN_OOB"] | E["UNMAPPED_PAGE"] | E["PAGE_OOB"]
+    assert (out[0] == 0).all() and torch.isfinite(out).all()
+
+
+def test_step_does_not_look_at_pages_that_the_window_left(dattn):
+    """Pages behind the window may be unmapped (given back): nothing is flagged."""
+    pool = Paged("fp8", [1000], 2, 64, 16, seed=2)
+    free = pool.table.copy()
+    free[0, 1:(1000 - 200) // 16] = -1  # all but the sinks' page and the window's
+    q = queries(1, 2, 4, 64, 7)
+    lay, (kp, vp) = pool.layout(dattn), pool.pools()
+    L = torch.tensor([1000], dtype=torch.int32, device=DEV)
+    ws = dattn.Workspace(1, 8, 2, 64)
+    a, b = (torch.empty(1, 2, 4, 64, device=DEV) for _ in range(2))
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    dattn.dattn_decode_window(lay, kp, vp, q, 0.1, L, 190, 5, a, ws)
+    pool.table = free
+    dattn.dattn_decode_window(pool.layout(dattn), kp, vp, q, 0.1, L, 190, 5, b, ws, dev_err=err)
+    assert int(err) == 0 and torch.equal(a, b)
+
+
+def test_step_in_a_graph_follows_the_lengths(dattn):
+    pool = Paged("int4", [400, 90], 2, 128, 16, seed=5)
+    lay, (kp, vp) = pool.layout(dattn), pool.pools()
+    q = queries(2, 2, 4, 128, 8)
+    L = torch.tensor([400, 90], dtype=torch.int32, device=DEV)
+    ws = dattn.Workspace(2, 8, 2, 128)
+    out, want = (torch.empty(2, 2, 4, 128, device=DEV) for _ in range(2))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        dattn.dattn_decode_window(lay, kp, vp, q, 0.1, L, 50, 4, out, ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dattn.dattn_decode_window(lay, kp, vp, q, 0.1, L, 50, 4, out, ws)
+    for lens in ([400, 90], [33, 2], [399, 60]):
+        L.copy_(torch.tensor(lens, dtype=torch.int32))
+        graph.replay()
+        dattn.dattn_decode_window(lay, kp, vp, q, 0.1, L, 50, 4, want, ws)
+        assert torch.equal(out, want)
