@@ -575,6 +575,28 @@ dattn_status_t dattn_prefill(const dattn_kv_layout *layout, const void *k_pool,
                              int32_t *dev_err, void *stream);
 
 /*
+ * Prefill of a chunk through a sliding window with first tokens that stay visible: the query at
+ * position p = L_b - Tq + t attends the tokens i <= p with i > p - window or i < sinks, token by
+ * token (dattn_prefill's streaming heads keep whole 64-token blocks). Otherwise as dattn_prefill
+ * with sparse == NULL: the chunk is the last Tq of the L_b tokens of request b, the pool is bf16 or
+ * DATTN_KV_FP8_BLOCK, and no workspace is needed. Only the key blocks that a window or the first
+ * tokens touch are read; pages of others may be unmapped.
+ *
+ *   window   tokens of the window, the query's own the last: >= 1;  sinks >= 0
+ *   out      (device) fp32, or bf16 when out_bf16 = 1, [B][Tq][Hq][d]
+ *   m, e     (device, nullable) fp32 [B][Tq][Hq], as for dattn_prefill
+ * A seq_len below Tq is flagged with DATTN_DEVERR_LEN_OOB, and that request's outputs are left
+ * untouched. The precision is dattn_prefill's; over the block-scaled pool with a bf16 output the sums
+ * are not emptied on the way, so that window + sinks above 2^17 needs an fp32 output there
+ * (DATTN_ERR_UNSUPPORTED, unless the block table holds no more tokens than that).
+ */
+dattn_status_t dattn_prefill_window(const dattn_kv_layout *layout, const void *k_pool,
+                                    const void *v_pool, const dattn_bf16 *q, int32_t B,
+                                    int32_t Tq, int32_t Hq, float scale, const int32_t *seq_lens,
+                                    int32_t window, int32_t sinks, void *out, int32_t out_bf16,
+                                    float *m, float *e, int32_t *dev_err, void *stream);
+
+/*
  * Page scoring and top-K selection for retrieval heads [LV §2.2.2, §3.1.2]. For every
  * request b and KV head h of kind DATTN_HEAD_RETRIEVAL:
  *   logical score  sigma(lp) = max over the g query heads j of

@@ -16,6 +16,7 @@ Entry points, with the same names as in include/dattn.h:
   dattn_page_select  page scoring and top-K selection for retrieval heads
   dattn_prefill      block-sparse prefill of a chunk of new tokens (64-token key blocks)
   dattn_decode_window  fused decode of T query tokens through a sliding window with sinks
+  dattn_prefill_window prefill of a chunk through a sliding window with sinks
   dattn_kv_read      tokens of the cache read back into dense rows
   dattn_rope         rotary positions of queries or keys, and their gradient
   dattn_rope_append  the append with the rotation of queries and keys applied on the way
@@ -32,7 +33,8 @@ __all__ = [
     "KVLayout", "SparseConfig", "DattnError", "load_library", "library_path",
     "dattn_kv_append", "dattn_partial", "dattn_merge", "dattn_decode", "dattn_page_select",
     "dattn_append_decode", "dattn_merge_gathered", "dattn_rope", "dattn_rope_append",
-    "dattn_rope_frequencies", "Rotation", "dattn_decode_window", "dattn_kv_read",
+    "dattn_rope_frequencies", "Rotation", "dattn_decode_window", "dattn_prefill_window",
+    "dattn_kv_read",
     "dattn_decode_noalloc", "dattn_decode_multi", "dattn_prefill", "PrefillSparseConfig",
     "dattn_workspace_size", "dattn_workspace_init", "dattn_auto_splits", "dattn_split_range",
     "dattn_split_owner", "dattn_status_string", "dattn_version", "Workspace",
@@ -108,6 +110,8 @@ _SIGS = {
                            ctypes.POINTER(_PrefillSparse), _P, _P, _P, _P, _P]),
     "dattn_decode_window": (_I, [ctypes.POINTER(_Layout), _P, _P, _P, _I, _I, _I, _F, _P, _I, _I,
                                  _I, _P, _SZ, _P, _I, _P, _P, _P, _P]),
+    "dattn_prefill_window": (_I, [ctypes.POINTER(_Layout), _P, _P, _P, _I, _I, _I, _F, _P, _I, _I,
+                                  _P, _I, _P, _P, _P, _P]),
     "dattn_kv_read": (_I, [ctypes.POINTER(_Layout), _P, _P, _I, _P, _P, _P, _I, _P, _I64, _P, _I64,
                            _I, _P, _P]),
     "dattn_rope_frequencies": (_I, [_I, _F, _I, _F, _F, _F, _F, _P]),
@@ -787,6 +791,25 @@ def dattn_prefill(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_lens, o
         ctypes.byref(layout.c), _at(k_pool, here), _at(v_pool, here), _at(q, here), B, Tq, Hq,
         scale, _at(seq_lens, here), sp, _at(out, here), _at(m, here), _at(e, here),
         _at(dev_err, here), _stream_on(stream, here)), "dattn_prefill")
+
+
+def dattn_prefill_window(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_lens, window: int,
+                         sinks: int, out, m=None, e=None, dev_err=None, stream=None):
+    """Prefill of q bf16 [B][Tq][Hq][d], the last Tq tokens of each request, through a sliding
+    window: the query at position p attends tokens i <= p with i > p - window or i < sinks. out
+    float32 or bf16 [B][Tq][Hq][d] (+ m, e fp32 [B][Tq][Hq]); bf16 or KV_FP8_BLOCK pools."""
+    _pool(layout, k_pool, "k_pool"); _pool(layout, v_pool, "v_pool"); _bf16(q, "q")
+    _i32(seq_lens, "seq_lens"); _f32(m, "m"); _f32(e, "e")
+    bf16 = _out_bf16(out)
+    if q.dim() != 4:
+        raise ValueError("q must be bf16 [B][Tq][Hq][d]")
+    B, Tq, Hq = q.shape[0], q.shape[1], q.shape[2]
+    _decode_sizes(layout, B, Tq, Hq, k_pool, v_pool, q, seq_lens, out, m, e, None)
+    here = _layout_device(layout, k_pool)
+    _check(load_library().dattn_prefill_window(
+        ctypes.byref(layout.c), _at(k_pool, here), _at(v_pool, here), _at(q, here), B, Tq, Hq,
+        scale, _at(seq_lens, here), window, sinks, _at(out, here), bf16, _at(m, here), _at(e, here),
+        _at(dev_err, here), _stream_on(stream, here)), "dattn_prefill_window")
 
 
 def dattn_decode_noalloc(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_lens, out,

@@ -137,7 +137,10 @@ __device__ __forceinline__ void tc_build_bitmaps(const PfParams& p, int32_t b, i
     }
 }
 
-template <int D>
+// WIN: dattn_prefill_window. The bitmaps are over the blocks that the CTA's windows and the first
+// tokens touch (PfWindow); in a block at a window's edge, or with the last of the first tokens, each
+// row masks its keys.
+template <int D, bool WIN>
 __global__ void __launch_bounds__(kTcThreads, 2)
 prefill_tc_kernel(const __grid_constant__ PfParams p, const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v, int32_t nwords) {
@@ -242,9 +245,26 @@ prefill_tc_kernel(const __grid_constant__ PfParams p, const __grid_constant__ CU
         if (tid == 0) set_err(p.dev_err, DATTN_DEVERR_LEN_OOB);
         active = false;
     }
-    const int32_t nw = active ? (qa + 1 + 1 + 31) / 32 : 0;  // words over blocks 0 .. qa + 1
+    int32_t nw = active ? (qa + 1 + 1 + 31) / 32 : 0;  // words over blocks 0 .. qa + 1
+    const PfWindow win(p, p_lo, qa + (hasB ? 1 : 0));
+    if constexpr (WIN) nw = active ? (win.count + 31) / 32 : 0;
     if (active) {
-        tc_build_bitmaps(p, b, kvh, qa, hasB, bmA, bmB, nw, tid);
+        if constexpr (WIN) {
+            for (int32_t w = tid; w < nw; w += kTcThreads) {
+                uint32_t a = 0u, bb = 0u;
+                for (int bit = 0; bit < 32; ++bit) {
+                    const int32_t j = 32 * w + bit, kb = win.block(j);
+                    if (j >= win.count) break;
+                    a |= (pf_window_keeps(p, kb, qa, p_lo) ? 1u : 0u) << bit;
+                    bb |= (hasB && pf_window_keeps(p, kb, qa + 1, max(p_lo, (qa + 1) * kPfBlock))
+                               ? 1u : 0u) << bit;
+                }
+                bmA[w] = a;
+                bmB[w] = bb;
+            }
+        } else {
+            tc_build_bitmaps(p, b, kvh, qa, hasB, bmA, bmB, nw, tid);
+        }
         if (hp) {  // both halves keep query block qa's key blocks
             __syncthreads();
             for (int32_t w = tid; w < nw; w += kTcThreads) bmB[w] = bmA[w];
@@ -299,7 +319,7 @@ prefill_tc_kernel(const __grid_constant__ PfParams p, const __grid_constant__ CU
                 const int bit = __ffs(word) - 1;
                 word &= word - 1u;
                 if (grp == i) {
-                    kb_o = 32 * w + bit;
+                    kb_o = WIN ? win.block(32 * w + bit) : 32 * w + bit;
                     fl_o = ((bmA[w] >> bit) & 1u) | (((bmB[w] >> bit) & 1u) << 1);
                 }
                 ++n;
@@ -497,7 +517,11 @@ prefill_tc_kernel(const __grid_constant__ PfParams p, const __grid_constant__ CU
                 const bool keep = rowok && (flags & rbit) != 0u;
                 const int32_t cut = keep ? pos - kb * kPfBlock + 1 : 0;
                 float mxr;  // the row maximum of the raw scores
-                if (__all_sync(0xffffffffu, cut >= kPfBlock && his == kFullTiles)) {
+                // windowed: key i is seen only from `low` on, or below `sk`
+                const int32_t low = WIN ? pos - p.window + 1 - kb * kPfBlock : 0;
+                const int32_t sk = WIN ? p.sinks - kb * kPfBlock : 0;
+                if (__all_sync(0xffffffffu, cut >= kPfBlock && his == kFullTiles &&
+                                                (!WIN || low <= 0 || sk >= kPfBlock))) {
                     mxr = row_max64(x);
                 } else {
                     int32_t lim[kPfTiles];
@@ -505,7 +529,8 @@ prefill_tc_kernel(const __grid_constant__ PfParams p, const __grid_constant__ CU
                     for (int u = 0; u < kPfTiles; ++u)
                         lim[u] = min(16 * u + ((his >> (5 * u)) & 31), cut);
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) x[i] = i < lim[i >> 4] ? x[i] : kPfNegInf;
+                    for (int i = 0; i < 64; ++i)
+                        x[i] = i < lim[i >> 4] && (!WIN || i >= low || i < sk) ? x[i] : kPfNegInf;
                     mxr = row_max64(x);
                 }
                 const float mx = mxr * sl2a;  // scaled (log2 units); -inf stays -inf
@@ -614,7 +639,16 @@ prefill_tc_kernel(const __grid_constant__ PfParams p, const __grid_constant__ CU
 #pragma unroll
                 for (int i = 0; i < 32; ++i) t[i] = 0.f;
             }
-            if (rowok) {
+            if (WIN && rowok && p.out_bf16 != 0) {
+                uint16_t* to = reinterpret_cast<uint16_t*>(p.out) + row * D + 32 * cc;
+#pragma unroll
+                for (int i = 0; i < 32; i += 8)
+                    *reinterpret_cast<uint4*>(to + i) = make_uint4(
+                        pack_bf16(t[i] * inv, t[i + 1] * inv),
+                        pack_bf16(t[i + 2] * inv, t[i + 3] * inv),
+                        pack_bf16(t[i + 4] * inv, t[i + 5] * inv),
+                        pack_bf16(t[i + 6] * inv, t[i + 7] * inv));
+            } else if (rowok) {
 #pragma unroll
                 for (int i = 0; i < 32; i += 4)
                     *reinterpret_cast<float4*>(orow + 32 * cc + i) =
@@ -669,9 +703,22 @@ dattn_status_t make_half_tensor_map(void* tmap_out, const void* pool, int64_t ro
     return r == CUDA_SUCCESS ? DATTN_OK : DATTN_ERR_CUDA;
 }
 
-int g_tc_smem_set[2] = {0, 0};
+template <int D, bool WIN>
+dattn_status_t ensure_tc_smem(int bytes) {
+    static int set[kMaxDevices] = {};  // a function attribute belongs to a device
+    std::lock_guard<std::mutex> lock(g_pf_mutex);
+    int& mine = set[device_index()];
+    if (bytes > mine) {
+        if (cudaFuncSetAttribute(prefill_tc_kernel<D, WIN>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 bytes) != cudaSuccess)
+            return DATTN_ERR_CUDA;
+        mine = bytes;
+    }
+    return DATTN_OK;
+}
 
-template <int D>
+template <int D, bool WIN>
 dattn_status_t launch_prefill_tc_d(const PfParams& p0, const void* k_pool, const void* v_pool,
                                    cudaStream_t stream) {
     PfParams p = p0;
@@ -697,27 +744,17 @@ dattn_status_t launch_prefill_tc_d(const PfParams& p0, const void* k_pool, const
                 break;
             }
     }
-    const int32_t nwords = (p.max_pages * p.P / kPfBlock + 2 + 31) / 32;
+    const int32_t nwords = (int32_t)((pf_bitmap_blocks(p, 1) + 31) / 32);
     const TcSmem L = tc_smem_layout(D, nwords);
     if (L.total > 227u * 1024u) return DATTN_ERR_UNSUPPORTED;
-    {
-        std::lock_guard<std::mutex> lock(g_pf_mutex);
-        int& set = g_tc_smem_set[D == 128 ? 1 : 0];
-        if ((int)L.total > set) {
-            if (cudaFuncSetAttribute(prefill_tc_kernel<D>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)L.total) != cudaSuccess)
-                return DATTN_ERR_CUDA;
-            set = (int)L.total;
-        }
-    }
+    dattn_status_t st = ensure_tc_smem<D, WIN>((int)L.total);
+    if (st != DATTN_OK) return st;
     alignas(64) CUtensorMap tk;
     alignas(64) CUtensorMap tv;
     const int64_t rows = (int64_t)p.num_pages * p.Hkv * p.P;
-    dattn_status_t st;
     if ((st = make_half_tensor_map(&tk, k_pool, rows, D)) != DATTN_OK) return st;
     if ((st = make_half_tensor_map(&tv, v_pool, rows, D)) != DATTN_OK) return st;
-    if (launch_pdl(prefill_tc_kernel<D>, dim3((unsigned)ctas), dim3(kTcThreads), L.total, stream,
+    if (launch_pdl(prefill_tc_kernel<D, WIN>, dim3((unsigned)ctas), dim3(kTcThreads), L.total, stream,
                    p, tk, tv, nwords) != cudaSuccess)
         return DATTN_ERR_CUDA;
     return DATTN_OK;
@@ -730,12 +767,14 @@ bool pf_aligned16(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u)
 
 using namespace dattn;
 
-extern "C" dattn_status_t dattn_prefill(const dattn_kv_layout* layout, const void* k_pool,
-                                        const void* v_pool, const dattn_bf16* q, int32_t B,
-                                        int32_t Tq, int32_t Hq, float scale,
-                                        const int32_t* seq_lens,
-                                        const dattn_prefill_sparse* sparse, float* out, float* m,
-                                        float* e, int32_t* dev_err, void* stream) {
+namespace {
+
+// dattn_prefill (window 0) and dattn_prefill_window.
+dattn_status_t prefill_impl(const dattn_kv_layout* layout, const void* k_pool, const void* v_pool,
+                            const dattn_bf16* q, int32_t B, int32_t Tq, int32_t Hq, float scale,
+                            const int32_t* seq_lens, const dattn_prefill_sparse* sparse,
+                            int32_t window, int32_t sinks, void* out, int32_t out_bf16, float* m,
+                            float* e, int32_t* dev_err, void* stream) {
     // the layout checks every pool-reading call makes
     if (layout == nullptr || layout->block_table == nullptr) return DATTN_ERR_INVALID_ARG;
     if (layout->num_pages <= 0 || layout->num_kv_heads <= 0 || layout->max_pages_per_req <= 0 ||
@@ -797,7 +836,10 @@ extern "C" dattn_status_t dattn_prefill(const dattn_kv_layout* layout, const voi
     p.sl2 = scale * kLog2e;
     p.seq_lens = seq_lens;
     p.nqb = (Tq + kPfBlock - 1) / kPfBlock + 1;  // a chunk spans at most this many blocks
-    p.out = out;
+    p.out = static_cast<float*>(out);
+    p.out_bf16 = out_bf16;
+    p.window = window;
+    p.sinks = sinks;
     p.m_out = m;
     p.e_out = e;
     p.dev_err = dev_err;
@@ -806,6 +848,34 @@ extern "C" dattn_status_t dattn_prefill(const dattn_kv_layout* layout, const voi
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (block)
         return launch_prefill_block(p, k_pool, v_pool, layout->kv_scale, layout->head_dim, s);
-    return layout->head_dim == 64 ? launch_prefill_tc_d<64>(p, k_pool, v_pool, s)
-                                  : launch_prefill_tc_d<128>(p, k_pool, v_pool, s);
+    if (window > 0)
+        return layout->head_dim == 64 ? launch_prefill_tc_d<64, true>(p, k_pool, v_pool, s)
+                                      : launch_prefill_tc_d<128, true>(p, k_pool, v_pool, s);
+    return layout->head_dim == 64 ? launch_prefill_tc_d<64, false>(p, k_pool, v_pool, s)
+                                  : launch_prefill_tc_d<128, false>(p, k_pool, v_pool, s);
+}
+
+}  // namespace
+
+extern "C" dattn_status_t dattn_prefill(const dattn_kv_layout* layout, const void* k_pool,
+                                        const void* v_pool, const dattn_bf16* q, int32_t B,
+                                        int32_t Tq, int32_t Hq, float scale,
+                                        const int32_t* seq_lens,
+                                        const dattn_prefill_sparse* sparse, float* out, float* m,
+                                        float* e, int32_t* dev_err, void* stream) {
+    return prefill_impl(layout, k_pool, v_pool, q, B, Tq, Hq, scale, seq_lens, sparse, 0, 0, out,
+                        0, m, e, dev_err, stream);
+}
+
+extern "C" dattn_status_t dattn_prefill_window(
+    const dattn_kv_layout* layout, const void* k_pool, const void* v_pool, const dattn_bf16* q,
+    int32_t B, int32_t Tq, int32_t Hq, float scale, const int32_t* seq_lens, int32_t window,
+    int32_t sinks, void* out, int32_t out_bf16, float* m, float* e, int32_t* dev_err,
+    void* stream) {
+    if (window < 1 || sinks < 0 || (out_bf16 & ~1)) return DATTN_ERR_INVALID_ARG;
+    // (no length reaches 2^30, so that a window or sinks beyond it see the same)
+    window = window < (1 << 30) ? window : 1 << 30;
+    sinks = sinks < (1 << 30) ? sinks : 1 << 30;
+    return prefill_impl(layout, k_pool, v_pool, q, B, Tq, Hq, scale, seq_lens, nullptr, window,
+                        sinks, out, out_bf16, m, e, dev_err, stream);
 }

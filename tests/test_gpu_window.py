@@ -168,3 +168,109 @@ def test_step_in_a_graph_follows_the_lengths(dattn):
         graph.replay()
         dattn.dattn_decode_window(lay, kp, vp, q, 0.1, L, 50, 4, want, ws)
         assert torch.equal(out, want)
+
+
+# ---- the prefill
+
+CHUNKS = [
+    # (lens, Tq, Hq, Hkv, d, P, window, sinks)
+    ([70, 200, 641], 64, 4, 2, 128, 16, 100, 4),      # even groups: two heads to a tile
+    ([70, 200, 641], 37, 4, 2, 128, 16, 64, 0),       # a window of one block
+    ([130, 333], 130, 3, 3, 64, 32, 1, 0),            # the token itself alone; odd groups
+    ([130, 333], 130, 3, 1, 64, 16, 1, 1),
+    ([600, 601, 700], 129, 8, 2, 128, 64, 65, 64),    # sinks of one block; g = 4
+    ([600, 601, 700], 129, 5, 1, 128, 64, 63, 65),
+    ([1030, 900], 900, 8, 1, 64, 16, 200, 130),       # g = 8; sinks past two blocks
+    ([500], 300, 4, 2, 128, 16, OVER, 3),             # no window
+    ([500], 300, 4, 2, 128, 16, 5, OVER),             # all tokens are first tokens
+    ([3000], 1, 8, 2, 128, 128, 777, 10),             # one token
+    ([4200], 70, 4, 4, 64, 16, 3000, 5),              # more than 32 blocks seen by a row
+]
+
+
+@pytest.mark.parametrize("fmt", ("bf16", "fp8-block"))
+@pytest.mark.parametrize("case", range(len(CHUNKS)))
+def test_chunk_against_the_definition(dattn, fmt, case):
+    lens, T, Hq, Hkv, d, P, window, sinks = CHUNKS[case]
+    pool = Paged(fmt, lens, Hkv, d, P, seed=case)
+    lay, (kp, vp) = pool.layout(dattn), pool.pools()
+    B = len(lens)
+    q = queries(B, T, Hq, d, case + 150)
+    L = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for dtype in (torch.float32, torch.bfloat16):
+        out = torch.full((B + 1, T, Hq, d), 9.0, dtype=dtype, device=DEV)
+        m, e = (torch.full((B, T, Hq), 9.0, device=DEV) for _ in range(2))
+        dattn.dattn_prefill_window(lay, kp, vp, q, d ** -0.5, L, window, sinks, out, m, e,
+                                   dev_err=err)
+        assert int(err) == 0 and (out[B] == 9).all()
+        check_all(pool, q, out, m, e, d ** -0.5, window, sinks, f"{fmt} {dtype}")
+
+
+@pytest.mark.parametrize("fmt", ("bf16", "fp8-block"))
+def test_chunk_without_a_window_is_the_causal_prefill(dattn, fmt):
+    pool = Paged(fmt, [700, 400], 2, 128, 16, seed=3)
+    lay, (kp, vp) = pool.layout(dattn), pool.pools()
+    q = queries(2, 300, 8, 128, 4)
+    L = torch.tensor([700, 400], dtype=torch.int32, device=DEV)
+    a, b = (torch.empty(2, 300, 8, 128, device=DEV) for _ in range(2))
+    dattn.dattn_prefill(lay, kp, vp, q, 0.1, L, a)
+    dattn.dattn_prefill_window(lay, kp, vp, q, 0.1, L, 700, 0, b)
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", ("bf16", "fp8-block"))
+def test_chunk_of_a_few_tokens_is_the_step(dattn, fmt):
+    pool = Paged(fmt, [700, 93], 2, 128, 16, seed=8)
+    lay, (kp, vp) = pool.layout(dattn), pool.pools()
+    q = queries(2, 4, 4, 128, 9)
+    L = torch.tensor([700, 93], dtype=torch.int32, device=DEV)
+    a, b = (torch.empty(2, 4, 4, 128, device=DEV) for _ in range(2))
+    dattn.dattn_prefill_window(lay, kp, vp, q, 0.1, L, 100, 7, a)
+    dattn.dattn_decode_window(lay, kp, vp, q, 0.1, L, 100, 7, b, dattn.Workspace(2, 16, 2, 128))
+    # weights within 2^-17 of theirs in both, values below 2^3
+    assert (a - b).abs().max() < 4 * 2.0 ** -17 * 8
+
+
+@pytest.mark.parametrize("fmt", ("bf16", "fp8-block"))
+def test_chunk_behind_a_long_context_reads_its_window_alone(dattn, fmt):
+    """70K tokens whose pages behind the sinks and before the window are unmapped."""
+    Hkv, d, P, T, W, S = 1, 64, 64, 90, 150, 70
+    lens = [70_001]
+    keep = Paged(fmt, [S + P + W + T + 2 * P], Hkv, d, P, seed=10)  # a pool of the pages in use
+    n = lens[0] // P + 1
+    first = (lens[0] - T - W + 1) // P
+    table = np.full((1, n), -1, np.int32)
+    used = [0, 1] + list(range(first, n))
+    table[0, used] = keep.table[0, :len(used)]
+    q = queries(1, T, 2, d, 11)
+    keep.k, keep.v = np.nan_to_num(keep.k), np.nan_to_num(keep.v)
+    near = Paged.__new__(Paged)
+    near.__dict__.update(keep.__dict__)
+    near.table, near.lens = table, lens
+    lay, (kp, vp) = near.layout(dattn), near.pools()
+    L = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = torch.empty(1, T, 2, d, device=DEV)
+    dattn.dattn_prefill_window(lay, kp, vp, q, 0.2, L, W, S, out, dev_err=err)
+    assert int(err) == 0
+    see = sees(lens[0], T, W, S)
+    seen = see.any(0)
+    tok = np.flatnonzero(seen)
+    K, V = (x[table[0][tok // P], 0, tok % P] for x in (near.k, near.v))
+    for h in range(2):
+        ref, _, _, bound, _ = attention(q[0, :, h].double().cpu().numpy(), K, V, 0.2, see[:, seen],
+                                        weight_error(fmt))
+        check(out[0, :, h], None, None, ref, bound, 0, 0, 0, f"{fmt} h={h}")
+
+
+def test_chunk_flags_a_length_below_it(dattn):
+    pool = Paged("bf16", [100, 100], 2, 64, 16, seed=1)
+    lay, (kp, vp) = pool.layout(dattn), pool.pools()
+    q = queries(2, 50, 4, 64, 1)
+    out = torch.full((2, 50, 4, 64), 9.0, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    dattn.dattn_prefill_window(lay, kp, vp, q, 0.1, torch.tensor([49, 100], dtype=torch.int32,
+                                                                 device=DEV), 20, 0, out, dev_err=err)
+    assert int(err) == dattn.DEVERR["LEN_OOB"]
+    assert (out[0] == 9).all() and (out[1] != 9).all()
