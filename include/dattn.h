@@ -475,6 +475,43 @@ dattn_status_t dattn_decode_window(const dattn_kv_layout *layout, const void *k_
                                    float *e_g, int32_t *dev_err, void *stream);
 
 /*
+ * Decode of a batch whose requests share long prefixes (a system prompt, a document that many ask
+ * about): dattn_decode_multi, with the tokens that a group of requests has in common read and computed
+ * once for all of them [IL: the prefix is a sub-block whose partials (m, e, MA) aggregate with those
+ * of each request's own tokens].
+ *
+ * Group i is the requests group_indptr[i] .. group_indptr[i+1] - 1. Their first prefix_lens[i] tokens
+ * are the same tokens in the same pages: the rows of the block table of all requests of the group
+ * agree on the pages that hold them (at any prefix length; a shorter one than the pages allow is
+ * right too, only slower). The pages are read from the row of the group's longest request; that the
+ * others agree is not checked. A request may be shorter than its group's prefix (it sees its own
+ * tokens only, e.g. none at length 0), and requests outside all groups share nothing.
+ *
+ *   num_groups    0 to B (and 1024); 0: as dattn_decode_multi
+ *   group_indptr  (device) int32 [num_groups + 1], ascending within [0, B]. Bounds out of order are
+ *                 flagged with DATTN_DEVERR_CHUNK_OOB, and every request is then attended by itself.
+ *   prefix_lens   (device) int32 [num_groups]; below 0 counts as 0
+ *   out           (device) fp32, or bf16 when out_bf16 = 1, [B][T][Hq][d], 16-byte aligned
+ *   q, seq_lens, m_g, e_g  as for dattn_decode_multi (g * T <= 8)
+ *   ws, ws_bytes  workspace of at least dattn_shared_workspace_size(B, T, Hq, Hkv, d)
+ * Three launches. Pools: bf16 and DATTN_KV_FP8_BLOCK (others DATTN_ERR_UNSUPPORTED). The products with
+ * a prefix take a key block of 64 tokens as a whole: a NaN among the values of a token (or an
+ * infinity) reaches every request of the group.
+ */
+dattn_status_t dattn_decode_shared(const dattn_kv_layout *layout, const void *k_pool,
+                                   const void *v_pool, const dattn_bf16 *q, int32_t B, int32_t T,
+                                   int32_t Hq, float scale, const int32_t *seq_lens,
+                                   int32_t num_groups, const int32_t *group_indptr,
+                                   const int32_t *prefix_lens, void *ws, size_t ws_bytes,
+                                   void *out, int32_t out_bf16, float *m_g, float *e_g,
+                                   int32_t *dev_err, void *stream);
+
+/* Workspace bytes of dattn_decode_shared on the current device, for any groups; 0 for invalid
+ * arguments. Its counters are zeroed once as for the other calls. */
+size_t dattn_shared_workspace_size(int32_t B, int32_t T, int32_t Hq, int32_t Hkv,
+                                   int32_t head_dim);
+
+/*
  * One decode step with its append, in one launch: exactly dattn_kv_append of one new token
  * per request (T = 1) followed by dattn_decode, for every pool format but
  * DATTN_KV_FP8_BLOCK (DATTN_ERR_UNSUPPORTED; see the layout notes). (A quantized pool

@@ -16,6 +16,7 @@ Entry points, with the same names as in include/dattn.h:
   dattn_page_select  page scoring and top-K selection for retrieval heads
   dattn_prefill      block-sparse prefill of a chunk of new tokens (64-token key blocks)
   dattn_decode_window  fused decode of T query tokens through a sliding window with sinks
+  dattn_decode_shared  fused decode of a batch whose requests share long prefixes
   dattn_prefill_window prefill of a chunk through a sliding window with sinks
   dattn_kv_read      tokens of the cache read back into dense rows
   dattn_rope         rotary positions of queries or keys, and their gradient
@@ -34,7 +35,7 @@ __all__ = [
     "dattn_kv_append", "dattn_partial", "dattn_merge", "dattn_decode", "dattn_page_select",
     "dattn_append_decode", "dattn_merge_gathered", "dattn_rope", "dattn_rope_append",
     "dattn_rope_frequencies", "Rotation", "dattn_decode_window", "dattn_prefill_window",
-    "dattn_kv_read",
+    "dattn_kv_read", "dattn_decode_shared", "dattn_shared_workspace_size", "SharedWorkspace",
     "dattn_decode_noalloc", "dattn_decode_multi", "dattn_prefill", "PrefillSparseConfig",
     "dattn_workspace_size", "dattn_workspace_init", "dattn_auto_splits", "dattn_split_range",
     "dattn_split_owner", "dattn_status_string", "dattn_version", "Workspace",
@@ -112,6 +113,9 @@ _SIGS = {
                                  _I, _P, _SZ, _P, _I, _P, _P, _P, _P]),
     "dattn_prefill_window": (_I, [ctypes.POINTER(_Layout), _P, _P, _P, _I, _I, _I, _F, _P, _I, _I,
                                   _P, _I, _P, _P, _P, _P]),
+    "dattn_decode_shared": (_I, [ctypes.POINTER(_Layout), _P, _P, _P, _I, _I, _I, _F, _P, _I, _P, _P,
+                                 _P, _SZ, _P, _I, _P, _P, _P, _P]),
+    "dattn_shared_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
     "dattn_kv_read": (_I, [ctypes.POINTER(_Layout), _P, _P, _I, _P, _P, _P, _I, _P, _I64, _P, _I64,
                            _I, _P, _P]),
     "dattn_rope_frequencies": (_I, [_I, _F, _I, _F, _F, _F, _F, _P]),
@@ -427,6 +431,18 @@ class Workspace:
 
 def dattn_workspace_size(items, Hq, Hkv, head_dim, top_k=0, num_splits=0) -> int:
     return int(load_library().dattn_workspace_size(items, Hq, Hkv, head_dim, top_k, num_splits))
+
+
+class SharedWorkspace:
+    """A zeroed device workspace of dattn_decode_shared (allocated by torch)."""
+
+    def __init__(self, B: int, T: int, Hq: int, Hkv: int, head_dim: int, device=None):
+        self.nbytes = dattn_shared_workspace_size(B, T, Hq, Hkv, head_dim)
+        self.buffer = torch.zeros(max(self.nbytes, 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def dattn_shared_workspace_size(B, T, Hq, Hkv, head_dim) -> int:
+    return int(load_library().dattn_shared_workspace_size(B, T, Hq, Hkv, head_dim))
 
 
 def dattn_workspace_init(ws: Workspace, stream=None):
@@ -791,6 +807,31 @@ def dattn_prefill(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_lens, o
         ctypes.byref(layout.c), _at(k_pool, here), _at(v_pool, here), _at(q, here), B, Tq, Hq,
         scale, _at(seq_lens, here), sp, _at(out, here), _at(m, here), _at(e, here),
         _at(dev_err, here), _stream_on(stream, here)), "dattn_prefill")
+
+
+def dattn_decode_shared(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_lens, group_indptr,
+                        prefix_lens, out, ws: SharedWorkspace, m_g=None, e_g=None, dev_err=None,
+                        stream=None):
+    """dattn_decode_multi (q bf16 [B][T][Hq][d]) of a batch whose requests share prefixes: requests
+    group_indptr[i] .. group_indptr[i+1] - 1 (int32 [groups + 1]) hold their first prefix_lens[i]
+    tokens (int32 [groups]) in the same pages, which are read once for the group. out float32 or bf16
+    [B][T][Hq][d] (+ m_g, e_g fp32 [B][T][Hq]); bf16 or KV_FP8_BLOCK pools."""
+    _pool(layout, k_pool, "k_pool"); _pool(layout, v_pool, "v_pool"); _bf16(q, "q")
+    _i32(seq_lens, "seq_lens"); _i32(group_indptr, "group_indptr"); _i32(prefix_lens, "prefix_lens")
+    _f32(m_g, "m_g"); _f32(e_g, "e_g")
+    bf16 = _out_bf16(out)
+    if q.dim() != 4:
+        raise ValueError("q must be bf16 [B][T][Hq][d]")
+    B, T, Hq = q.shape[0], q.shape[1], q.shape[2]
+    groups = prefix_lens.numel()
+    _decode_sizes(layout, B, T, Hq, k_pool, v_pool, q, seq_lens, out, m_g, e_g, None)
+    _size(group_indptr, groups + 1, "group_indptr")
+    here = _layout_device(layout, k_pool)
+    _check(load_library().dattn_decode_shared(
+        ctypes.byref(layout.c), _at(k_pool, here), _at(v_pool, here), _at(q, here), B, T, Hq,
+        scale, _at(seq_lens, here), groups, _at(group_indptr, here), _at(prefix_lens, here),
+        _at(ws.buffer, here), ws.buffer.numel(), _at(out, here), bf16, _at(m_g, here),
+        _at(e_g, here), _at(dev_err, here), _stream_on(stream, here)), "dattn_decode_shared")
 
 
 def dattn_prefill_window(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_lens, window: int,

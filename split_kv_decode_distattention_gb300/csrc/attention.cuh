@@ -509,7 +509,9 @@ __device__ __forceinline__ void write_final(const AttnParams& p, int32_t s, int3
         out[3] = ma.w;
     }
     if (d == 0) {
-        if (p.m_out) p.m_out[row] = m == kNegInf ? kNegInf : m * kLn2;
+        // (dattn_decode_shared joins its parts in log2 units)
+        const float ln2 = WIN && p.normalise == 0 ? 1.f : kLn2;
+        if (p.m_out) p.m_out[row] = m == kNegInf ? kNegInf : m * ln2;
         if (p.e_out) p.e_out[row] = e;
     }
 }

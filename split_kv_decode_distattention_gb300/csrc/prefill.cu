@@ -670,12 +670,12 @@ prefill_tc_kernel(const __grid_constant__ PfParams p, const __grid_constant__ CU
     }
 }
 
-std::mutex g_pf_mutex;
+}  // namespace
 
 // The pool as rows of d bf16 values split into 128-byte halves (dims {64, rows, d/64}), with
 // a box of one half of 16 rows: the tcgen05 operands keep each half of a key block as 64
 // contiguous 128-byte rows.
-PFN_cuTensorMapEncodeTiled_v12000 tc_encode_fn() {
+static PFN_cuTensorMapEncodeTiled_v12000 tc_encode_fn() {
     static std::once_flag once;
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     std::call_once(once, [] {
@@ -702,6 +702,10 @@ dattn_status_t make_half_tensor_map(void* tmap_out, const void* pool, int64_t ro
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? DATTN_OK : DATTN_ERR_CUDA;
 }
+
+namespace {
+
+std::mutex g_pf_mutex;
 
 template <int D, bool WIN>
 dattn_status_t ensure_tc_smem(int bytes) {

@@ -145,52 +145,6 @@ __device__ __forceinline__ uint32_t held_word(const uint32_t* bm, int nq, int nw
     return q[0] | q[1] | q[2] | q[3];
 }
 
-// Matrix descriptors as their lower words: the upper word (stride 1024 bytes, the descriptor version
-// and the 128-byte swizzle, see tc_sdesc) is the same for every operand here, and a step along an
-// operand adds its bytes / 16 to the lower word.
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
-    return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);
-}
-// The products are predicated on the issuing lane instead of branched around: the code around them
-// stays convergent, so that their operands can live in uniform registers, where tcgen05.mma takes
-// them from.
-template <bool ACC>
-__device__ __forceinline__ void pb_mma_ss(uint32_t lead, uint32_t d_tmem, uint32_t a_lo,
-                                          uint32_t b_lo, uint32_t idesc) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-        "setp.ne.b32 q, %6, 0;\n\tmov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(kDescHi), "n"(ACC ? 1 : 0), "r"(lead)
-        : "memory");
-}
-__device__ __forceinline__ void pb_mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem,
-                                          uint32_t b_lo, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-        "setp.ne.b32 q, %6, 0;\n\tmov.b64 b, {%2, %4};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "r"(b_lo), "r"(idesc), "n"(kDescHi), "r"(acc), "r"(lead)
-        : "memory");
-}
-// tc_commit by the issuing lane
-__device__ __forceinline__ void pb_commit(uint32_t lead, uint32_t bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
-            bar),
-        "r"(lead)
-        : "memory");
-}
-// 1 in one lane of the (convergent) warp
-__device__ __forceinline__ uint32_t elect_lane() {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r));
-    return r;
-}
 // kind::f16 with fp16 operands (tc_idesc's type fields cleared) and an fp32 accumulator
 __host__ __device__ constexpr uint32_t pb_idesc(uint32_t M, uint32_t N, uint32_t b_mn) {
     return tc_idesc(M, N, b_mn) & ~((7u << 7) | (7u << 10));

@@ -11,7 +11,7 @@ __device__ __forceinline__ bool shared_groups_ok(const int32_t* indptr, int32_t 
                                                  int tid, int nthreads) {
     bool ok = true;
     for (int32_t g = tid; g < groups; g += nthreads) {
-        const int32_t a = __ldg(indptr + g), b = __ldg(indptr + g + 1);
+        const int32_t a = __ldcg(indptr + g), b = __ldcg(indptr + g + 1);
         ok = ok && a >= 0 && a <= b && b <= B;
     }
     return __syncthreads_and(ok) != 0;
@@ -22,9 +22,9 @@ __device__ __forceinline__ int32_t shared_group(const int32_t* indptr, int32_t g
     int32_t lo = 0, hi = groups;  // the number of groups that end at or before i
     while (lo < hi) {
         const int32_t mid = (lo + hi) >> 1;
-        if (__ldg(indptr + mid + 1) <= i) lo = mid + 1; else hi = mid;
+        if (__ldcg(indptr + mid + 1) <= i) lo = mid + 1; else hi = mid;
     }
-    return lo < groups && __ldg(indptr + lo) <= i ? lo : -1;
+    return lo < groups && __ldcg(indptr + lo) <= i ? lo : -1;
 }
 
 }  // namespace dattn
