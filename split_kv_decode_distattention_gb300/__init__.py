@@ -825,7 +825,9 @@ def dattn_decode_shared(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_l
     B, T, Hq = q.shape[0], q.shape[1], q.shape[2]
     groups = prefix_lens.numel()
     _decode_sizes(layout, B, T, Hq, k_pool, v_pool, q, seq_lens, out, m_g, e_g, None)
-    _size(group_indptr, groups + 1, "group_indptr")
+    if group_indptr.numel() != groups + 1:
+        raise ValueError(f"group_indptr holds {group_indptr.numel()} elements; {groups} groups need "
+                         f"{groups + 1}")
     here = _layout_device(layout, k_pool)
     _check(load_library().dattn_decode_shared(
         ctypes.byref(layout.c), _at(k_pool, here), _at(v_pool, here), _at(q, here), B, T, Hq,
