@@ -197,7 +197,9 @@ def test_tensors_of_another_device_are_refused(current, name):
 
 @pytest.mark.parametrize("name", USES)
 def test_tensors_too_short_are_refused(current, name):
-    for other in set(USES[name].split()) - {"err", "ws", "k_out", "v_out", "q"}:
+    # (a shorter out_indptr is a read of fewer requests)
+    for other in set(USES[name].split()) - {"err", "ws", "k_out", "v_out", "q"} - \
+            ({"ind"} if name == "read" else set()):
         t = tensors()
         t[other] = t[other].reshape(-1)[:-1].reshape(1, -1) if other == "table" else \
             t[other].reshape(-1)[:-1]
