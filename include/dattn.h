@@ -487,7 +487,7 @@ dattn_status_t dattn_decode_window(const dattn_kv_layout *layout, const void *k_
  * others agree is not checked. A request may be shorter than its group's prefix (it sees its own
  * tokens only, e.g. none at length 0), and requests outside all groups share nothing.
  *
- *   num_groups    0 to B (and 1024); 0: as dattn_decode_multi
+ *   num_groups    0 to B (and 512); 0: as dattn_decode_multi
  *   group_indptr  (device) int32 [num_groups + 1], ascending within [0, B]. Bounds out of order are
  *                 flagged with DATTN_DEVERR_CHUNK_OOB, and every request is then attended by itself.
  *   prefix_lens   (device) int32 [num_groups]; below 0 counts as 0

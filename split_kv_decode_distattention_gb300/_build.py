@@ -18,8 +18,9 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdattn.so")
 SOURCES = ["abi.cu", "attention.cu", "attention_window.cu", "kv_append.cu", "kv_read.cu",
            "merge.cu", "page_select.cu", "decode_static.cu", "prefill.cu", "prefill_block.cu",
-           "rope.cu", "shared.cu"]
-HEADERS = ["attention.cuh", "common.cuh", "internal.h", "prefill.cuh", "shared.cuh"]
+           "rope.cu", "shared.cu", "window_prefill.cu"]
+HEADERS = ["attention.cuh", "common.cuh", "internal.h", "prefill.cuh", "shared.cuh",
+           "tile_attention.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-warn-spills"]

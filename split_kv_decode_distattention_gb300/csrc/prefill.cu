@@ -45,12 +45,6 @@ namespace dattn {
 
 namespace {
 
-__device__ __forceinline__ uint64_t policy_evict_normal() {
-    uint64_t pol;
-    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
-    return pol;
-}
-
 // ------------------------------------------------------------------ tcgen05 prefill
 
 constexpr int kTcRows = 128;         // query rows per CTA (M of both products)
@@ -137,10 +131,7 @@ __device__ __forceinline__ void tc_build_bitmaps(const PfParams& p, int32_t b, i
     }
 }
 
-// WIN: dattn_prefill_window. The bitmaps are over the blocks that the CTA's windows and the first
-// tokens touch (PfWindow); in a block at a window's edge, or with the last of the first tokens, each
-// row masks its keys.
-template <int D, bool WIN>
+template <int D>
 __global__ void __launch_bounds__(kTcThreads, 2)
 prefill_tc_kernel(const __grid_constant__ PfParams p, const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v, int32_t nwords) {
@@ -245,26 +236,9 @@ prefill_tc_kernel(const __grid_constant__ PfParams p, const __grid_constant__ CU
         if (tid == 0) set_err(p.dev_err, DATTN_DEVERR_LEN_OOB);
         active = false;
     }
-    int32_t nw = active ? (qa + 1 + 1 + 31) / 32 : 0;  // words over blocks 0 .. qa + 1
-    const PfWindow win(p, p_lo, qa + (hasB ? 1 : 0));
-    if constexpr (WIN) nw = active ? (win.count + 31) / 32 : 0;
+    const int32_t nw = active ? (qa + 1 + 1 + 31) / 32 : 0;  // words over blocks 0 .. qa + 1
     if (active) {
-        if constexpr (WIN) {
-            for (int32_t w = tid; w < nw; w += kTcThreads) {
-                uint32_t a = 0u, bb = 0u;
-                for (int bit = 0; bit < 32; ++bit) {
-                    const int32_t j = 32 * w + bit, kb = win.block(j);
-                    if (j >= win.count) break;
-                    a |= (pf_window_keeps(p, kb, qa, p_lo) ? 1u : 0u) << bit;
-                    bb |= (hasB && pf_window_keeps(p, kb, qa + 1, max(p_lo, (qa + 1) * kPfBlock))
-                               ? 1u : 0u) << bit;
-                }
-                bmA[w] = a;
-                bmB[w] = bb;
-            }
-        } else {
-            tc_build_bitmaps(p, b, kvh, qa, hasB, bmA, bmB, nw, tid);
-        }
+        tc_build_bitmaps(p, b, kvh, qa, hasB, bmA, bmB, nw, tid);
         if (hp) {  // both halves keep query block qa's key blocks
             __syncthreads();
             for (int32_t w = tid; w < nw; w += kTcThreads) bmB[w] = bmA[w];
@@ -319,7 +293,7 @@ prefill_tc_kernel(const __grid_constant__ PfParams p, const __grid_constant__ CU
                 const int bit = __ffs(word) - 1;
                 word &= word - 1u;
                 if (grp == i) {
-                    kb_o = WIN ? win.block(32 * w + bit) : 32 * w + bit;
+                    kb_o = 32 * w + bit;
                     fl_o = ((bmA[w] >> bit) & 1u) | (((bmB[w] >> bit) & 1u) << 1);
                 }
                 ++n;
@@ -517,11 +491,7 @@ prefill_tc_kernel(const __grid_constant__ PfParams p, const __grid_constant__ CU
                 const bool keep = rowok && (flags & rbit) != 0u;
                 const int32_t cut = keep ? pos - kb * kPfBlock + 1 : 0;
                 float mxr;  // the row maximum of the raw scores
-                // windowed: key i is seen only from `low` on, or below `sk`
-                const int32_t low = WIN ? pos - p.window + 1 - kb * kPfBlock : 0;
-                const int32_t sk = WIN ? p.sinks - kb * kPfBlock : 0;
-                if (__all_sync(0xffffffffu, cut >= kPfBlock && his == kFullTiles &&
-                                                (!WIN || low <= 0 || sk >= kPfBlock))) {
+                if (__all_sync(0xffffffffu, cut >= kPfBlock && his == kFullTiles)) {
                     mxr = row_max64(x);
                 } else {
                     int32_t lim[kPfTiles];
@@ -529,8 +499,7 @@ prefill_tc_kernel(const __grid_constant__ PfParams p, const __grid_constant__ CU
                     for (int u = 0; u < kPfTiles; ++u)
                         lim[u] = min(16 * u + ((his >> (5 * u)) & 31), cut);
 #pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        x[i] = i < lim[i >> 4] && (!WIN || i >= low || i < sk) ? x[i] : kPfNegInf;
+                    for (int i = 0; i < 64; ++i) x[i] = i < lim[i >> 4] ? x[i] : kPfNegInf;
                     mxr = row_max64(x);
                 }
                 const float mx = mxr * sl2a;  // scaled (log2 units); -inf stays -inf
@@ -639,16 +608,7 @@ prefill_tc_kernel(const __grid_constant__ PfParams p, const __grid_constant__ CU
 #pragma unroll
                 for (int i = 0; i < 32; ++i) t[i] = 0.f;
             }
-            if (WIN && rowok && p.out_bf16 != 0) {
-                uint16_t* to = reinterpret_cast<uint16_t*>(p.out) + row * D + 32 * cc;
-#pragma unroll
-                for (int i = 0; i < 32; i += 8)
-                    *reinterpret_cast<uint4*>(to + i) = make_uint4(
-                        pack_bf16(t[i] * inv, t[i + 1] * inv),
-                        pack_bf16(t[i + 2] * inv, t[i + 3] * inv),
-                        pack_bf16(t[i + 4] * inv, t[i + 5] * inv),
-                        pack_bf16(t[i + 6] * inv, t[i + 7] * inv));
-            } else if (rowok) {
+            if (rowok) {
 #pragma unroll
                 for (int i = 0; i < 32; i += 4)
                     *reinterpret_cast<float4*>(orow + 32 * cc + i) =
@@ -672,10 +632,7 @@ prefill_tc_kernel(const __grid_constant__ PfParams p, const __grid_constant__ CU
 
 }  // namespace
 
-// The pool as rows of d bf16 values split into 128-byte halves (dims {64, rows, d/64}), with
-// a box of one half of 16 rows: the tcgen05 operands keep each half of a key block as 64
-// contiguous 128-byte rows.
-static PFN_cuTensorMapEncodeTiled_v12000 tc_encode_fn() {
+PFN_cuTensorMapEncodeTiled_v12000 tc_encode_fn() {
     static std::once_flag once;
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     std::call_once(once, [] {
@@ -689,6 +646,9 @@ static PFN_cuTensorMapEncodeTiled_v12000 tc_encode_fn() {
     return fn;
 }
 
+// The pool as rows of d bf16 values split into 128-byte halves (dims {64, rows, d/64}), with
+// a box of one half of 16 rows: the tcgen05 operands keep each half of a key block as 64
+// contiguous 128-byte rows.
 dattn_status_t make_half_tensor_map(void* tmap_out, const void* pool, int64_t rows, int D) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = tc_encode_fn();
     if (fn == nullptr) return DATTN_ERR_CUDA;
@@ -707,22 +667,9 @@ namespace {
 
 std::mutex g_pf_mutex;
 
-template <int D, bool WIN>
-dattn_status_t ensure_tc_smem(int bytes) {
-    static int set[kMaxDevices] = {};  // a function attribute belongs to a device
-    std::lock_guard<std::mutex> lock(g_pf_mutex);
-    int& mine = set[device_index()];
-    if (bytes > mine) {
-        if (cudaFuncSetAttribute(prefill_tc_kernel<D, WIN>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 bytes) != cudaSuccess)
-            return DATTN_ERR_CUDA;
-        mine = bytes;
-    }
-    return DATTN_OK;
-}
+int g_tc_smem_set[2] = {0, 0};
 
-template <int D, bool WIN>
+template <int D>
 dattn_status_t launch_prefill_tc_d(const PfParams& p0, const void* k_pool, const void* v_pool,
                                    cudaStream_t stream) {
     PfParams p = p0;
@@ -748,17 +695,27 @@ dattn_status_t launch_prefill_tc_d(const PfParams& p0, const void* k_pool, const
                 break;
             }
     }
-    const int32_t nwords = (int32_t)((pf_bitmap_blocks(p, 1) + 31) / 32);
+    const int32_t nwords = (p.max_pages * p.P / kPfBlock + 2 + 31) / 32;
     const TcSmem L = tc_smem_layout(D, nwords);
     if (L.total > 227u * 1024u) return DATTN_ERR_UNSUPPORTED;
-    dattn_status_t st = ensure_tc_smem<D, WIN>((int)L.total);
-    if (st != DATTN_OK) return st;
+    {
+        std::lock_guard<std::mutex> lock(g_pf_mutex);
+        int& set = g_tc_smem_set[D == 128 ? 1 : 0];
+        if ((int)L.total > set) {
+            if (cudaFuncSetAttribute(prefill_tc_kernel<D>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)L.total) != cudaSuccess)
+                return DATTN_ERR_CUDA;
+            set = (int)L.total;
+        }
+    }
     alignas(64) CUtensorMap tk;
     alignas(64) CUtensorMap tv;
     const int64_t rows = (int64_t)p.num_pages * p.Hkv * p.P;
+    dattn_status_t st;
     if ((st = make_half_tensor_map(&tk, k_pool, rows, D)) != DATTN_OK) return st;
     if ((st = make_half_tensor_map(&tv, v_pool, rows, D)) != DATTN_OK) return st;
-    if (launch_pdl(prefill_tc_kernel<D, WIN>, dim3((unsigned)ctas), dim3(kTcThreads), L.total, stream,
+    if (launch_pdl(prefill_tc_kernel<D>, dim3((unsigned)ctas), dim3(kTcThreads), L.total, stream,
                    p, tk, tv, nwords) != cudaSuccess)
         return DATTN_ERR_CUDA;
     return DATTN_OK;
@@ -771,14 +728,12 @@ bool pf_aligned16(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u)
 
 using namespace dattn;
 
-namespace {
-
-// dattn_prefill (window 0) and dattn_prefill_window.
-dattn_status_t prefill_impl(const dattn_kv_layout* layout, const void* k_pool, const void* v_pool,
-                            const dattn_bf16* q, int32_t B, int32_t Tq, int32_t Hq, float scale,
-                            const int32_t* seq_lens, const dattn_prefill_sparse* sparse,
-                            int32_t window, int32_t sinks, void* out, int32_t out_bf16, float* m,
-                            float* e, int32_t* dev_err, void* stream) {
+extern "C" dattn_status_t dattn_prefill(const dattn_kv_layout* layout, const void* k_pool,
+                                        const void* v_pool, const dattn_bf16* q, int32_t B,
+                                        int32_t Tq, int32_t Hq, float scale,
+                                        const int32_t* seq_lens,
+                                        const dattn_prefill_sparse* sparse, float* out, float* m,
+                                        float* e, int32_t* dev_err, void* stream) {
     // the layout checks every pool-reading call makes
     if (layout == nullptr || layout->block_table == nullptr) return DATTN_ERR_INVALID_ARG;
     if (layout->num_pages <= 0 || layout->num_kv_heads <= 0 || layout->max_pages_per_req <= 0 ||
@@ -840,10 +795,7 @@ dattn_status_t prefill_impl(const dattn_kv_layout* layout, const void* k_pool, c
     p.sl2 = scale * kLog2e;
     p.seq_lens = seq_lens;
     p.nqb = (Tq + kPfBlock - 1) / kPfBlock + 1;  // a chunk spans at most this many blocks
-    p.out = static_cast<float*>(out);
-    p.out_bf16 = out_bf16;
-    p.window = window;
-    p.sinks = sinks;
+    p.out = out;
     p.m_out = m;
     p.e_out = e;
     p.dev_err = dev_err;
@@ -852,34 +804,6 @@ dattn_status_t prefill_impl(const dattn_kv_layout* layout, const void* k_pool, c
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (block)
         return launch_prefill_block(p, k_pool, v_pool, layout->kv_scale, layout->head_dim, s);
-    if (window > 0)
-        return layout->head_dim == 64 ? launch_prefill_tc_d<64, true>(p, k_pool, v_pool, s)
-                                      : launch_prefill_tc_d<128, true>(p, k_pool, v_pool, s);
-    return layout->head_dim == 64 ? launch_prefill_tc_d<64, false>(p, k_pool, v_pool, s)
-                                  : launch_prefill_tc_d<128, false>(p, k_pool, v_pool, s);
-}
-
-}  // namespace
-
-extern "C" dattn_status_t dattn_prefill(const dattn_kv_layout* layout, const void* k_pool,
-                                        const void* v_pool, const dattn_bf16* q, int32_t B,
-                                        int32_t Tq, int32_t Hq, float scale,
-                                        const int32_t* seq_lens,
-                                        const dattn_prefill_sparse* sparse, float* out, float* m,
-                                        float* e, int32_t* dev_err, void* stream) {
-    return prefill_impl(layout, k_pool, v_pool, q, B, Tq, Hq, scale, seq_lens, sparse, 0, 0, out,
-                        0, m, e, dev_err, stream);
-}
-
-extern "C" dattn_status_t dattn_prefill_window(
-    const dattn_kv_layout* layout, const void* k_pool, const void* v_pool, const dattn_bf16* q,
-    int32_t B, int32_t Tq, int32_t Hq, float scale, const int32_t* seq_lens, int32_t window,
-    int32_t sinks, void* out, int32_t out_bf16, float* m, float* e, int32_t* dev_err,
-    void* stream) {
-    if (window < 1 || sinks < 0 || (out_bf16 & ~1)) return DATTN_ERR_INVALID_ARG;
-    // (no length reaches 2^30, so that a window or sinks beyond it see the same)
-    window = window < (1 << 30) ? window : 1 << 30;
-    sinks = sinks < (1 << 30) ? sinks : 1 << 30;
-    return prefill_impl(layout, k_pool, v_pool, q, B, Tq, Hq, scale, seq_lens, nullptr, window,
-                        sinks, out, out_bf16, m, e, dev_err, stream);
+    return layout->head_dim == 64 ? launch_prefill_tc_d<64>(p, k_pool, v_pool, s)
+                                  : launch_prefill_tc_d<128>(p, k_pool, v_pool, s);
 }

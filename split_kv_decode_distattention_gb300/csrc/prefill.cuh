@@ -2,6 +2,8 @@
 // 8-bit pool): the launch parameters, the tcgen05 wrappers and the softmax threads' arithmetic.
 #pragma once
 
+#include <cudaTypedefs.h>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -32,44 +34,17 @@ struct PfParams {
     float* m_out;
     float* e_out;
     int32_t* dev_err;
-    // dattn_prefill_window: the query at position p sees key i <= p only if i > p - window or
-    // i < sinks; out holds bf16 values when out_bf16 is set
-    int32_t window, sinks, out_bf16;
 };
-
-// The key blocks that the query blocks [q0, q0 + n) of a windowed chunk may keep, numbered without a
-// gap: the first `first` blocks hold first tokens that stay visible, then come those from block
-// `from` on, where the first query's window begins (p0: its position).
-struct PfWindow {
-    int32_t first, from, count;
-    __device__ PfWindow(const PfParams& p, int32_t p0, int32_t last) {
-        from = max(p0 - p.window + 1, 0) / kPfBlock;
-        first = min((int32_t)(((int64_t)p.sinks + kPfBlock - 1) / kPfBlock), from);
-        count = first + last - from + 1;  // `last`: the last query's block
-    }
-    __device__ int32_t block(int32_t j) const { return j < first ? j : from + (j - first); }
-};
-// Whether block kb holds a key that a query of block qb (from position p0 on) sees.
-__device__ __forceinline__ bool pf_window_keeps(const PfParams& p, int32_t kb, int32_t qb,
-                                                int32_t p0) {
-    return kb <= qb && (kb * kPfBlock < p.sinks || (kb + 1) * kPfBlock > p0 - p.window + 1);
-}
 
 // The prefill over the block-scaled pool (prefill_block.cu); p.nqb, head_pairs and kv_group are its
 // own to set.
 dattn_status_t launch_prefill_block(const PfParams& p, const void* k_pool, const void* v_pool,
                                     const float* kv_scale, int D, cudaStream_t stream);
 
-// 3-D map over a bf16 pool whose boxes are one 128-byte half of 16 rows (prefill.cu).
+// The driver's tensor-map encoder (nullptr: not found), and a 3-D map over a bf16 pool whose boxes are
+// one 128-byte half of 16 rows (prefill.cu).
+PFN_cuTensorMapEncodeTiled_v12000 tc_encode_fn();
 dattn_status_t make_half_tensor_map(void* tmap_out, const void* pool, int64_t rows, int D);
-
-// The key blocks that bitmaps hold, at most: all of the block table's, or a window's.
-inline int64_t pf_bitmap_blocks(const PfParams& p, int32_t query_blocks) {
-    const int64_t all = (int64_t)p.max_pages * p.P / kPfBlock + 1 + query_blocks;
-    if (p.window == 0) return all;
-    const int64_t seen = ((int64_t)p.sinks + p.window) / kPfBlock + 3 + query_blocks;
-    return seen < all ? seen : all;
-}
 
 constexpr float kTcRescale = 8.f;    // lazy rescale threshold (log2 units)
 

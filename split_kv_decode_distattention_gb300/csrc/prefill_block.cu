@@ -71,9 +71,6 @@ constexpr int kPbSplitBlocks = 3;
 // weight above 2^kPbMost sets it anew (both terms are fp16: below 2^16). With 12 more keys set it anew:
 // 4096 tokens after 28K took 2580 us, 2405 with 9.
 constexpr float kPbTop = 9.f, kPbMost = 15.f;
-// Keys that a query of dattn_prefill_window may see with a bf16 output: 2^17 keys are 2^14 products,
-// each losing 2^-24 of the sum at most, 2^-25 in the mean.
-constexpr int64_t kPbWindowMost = 1 << 17;
 constexpr uint32_t kPbCols = 512;           // O: [0, 128), [128, 256); S: 256 + 128 tile + 64 buffer
 
 // mbarriers
@@ -167,9 +164,7 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) 
 
 // SPLIT: a cluster of pp.split CTAs holds one tile, each CTA a run of its key blocks; their sums and
 // maxima meet in shared memory.
-// WIN: dattn_prefill_window (see prefill.cu). With a bf16 output an accumulator is not emptied: up to
-// kPbWindowMost keys it then shrinks by less than an eighth of the output's half step.
-template <int D, bool SPLIT, bool WIN>
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kPbThreads, 1)
 prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
     constexpr uint32_t kHalf = 64u * 128u;  // a 128-byte half of a key block's rows
@@ -267,13 +262,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
     }
     active = active && has != 0u;
     const int32_t p_hi = min(Ln, (qa + nq) * kPfBlock);  // no row sees a later key
-    int32_t nw = active ? (qa + nq + 31) / 32 : 0;
-    const int32_t q_first = max(c0, qa * kPfBlock);  // the CTA's first query
-    const PfWindow win(p, q_first, (p_hi - 1) / kPfBlock);
-    if constexpr (WIN) nw = active ? (win.count + 31) / 32 : 0;
-    // blocks between two emptyings of an accumulator, and its mask
-    const int32_t wlen = WIN && p.out_bf16 != 0 ? 0x7fffffff : kPbWindow;
-    const uint32_t wmask = WIN && p.out_bf16 != 0 ? 0x7fffffffu : kPbWindow - 1u;
+    const int32_t nw = active ? (qa + nq + 31) / 32 : 0;
     // quarter z (rows 64 z ..): its query block's place and its head
     auto q_block = [&](int z) { return nq == 4 ? z : nq == 2 ? z >> 1 : 0; };
     auto q_head = [&](int z) { return nq == 4 ? 0 : nq == 2 ? z & 1 : z; };
@@ -282,15 +271,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
             const int i = x / nw, w = x - i * nw;
             const int32_t qb = qa + i;
             uint32_t a = 0u;
-            if (WIN && ((has >> i) & 1u)) {
-                for (int bit = 0; bit < 32; ++bit) {
-                    const int32_t at = 32 * w + bit;
-                    const bool keep = at < win.count && pf_window_keeps(p, win.block(at), qb,
-                                                                        max(c0, qb * kPfBlock));
-                    a |= (keep ? 1u : 0u) << bit;
-                }
-            }
-            if (!WIN && kind != DATTN_HEAD_RETRIEVAL && ((has >> i) & 1u)) {
+            if (kind != DATTN_HEAD_RETRIEVAL && ((has >> i) & 1u)) {
                 for (int bit = 0; bit < 32; ++bit) {
                     const int32_t kb = 32 * w + bit;
                     const bool keep = kb <= qb && (kind == DATTN_HEAD_DENSE || kb < p.sink_blocks ||
@@ -394,7 +375,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                 while (word == 0u && w + 1 < nw) word = held_word(bm, nq, nwords, tmask, ++w, q);
                 const int bit = __ffs(word) - 1;
                 if (x == blk) {
-                    kb = WIN ? win.block(32 * w + bit) : 32 * w + bit;
+                    kb = 32 * w + bit;
                     act = ((q[0] >> bit) & 1u) | (((q[1] >> bit) & 1u) << 1) |
                           (((q[2] >> bit) & 1u) << 2) | (((q[3] >> bit) & 1u) << 3);
                 }
@@ -578,7 +559,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
                                 pb_mma_ts(lead, oc, from + 32u * part + 8u * kk, v_lo + (kk * 2048u >> 4),
-                                          idesc_o, (part > 0 || kk > 0) ? 1u : jp & wmask);
+                                          idesc_o, (part > 0 || kk > 0) ? 1u : jp & (kPbWindow - 1u));
                         }
                         pb_commit(lead, bar(kBarPv) + 8u * t);
                     }
@@ -627,12 +608,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
             // The row's query block keeps kb; all keys pass for every row of the warp if they are
             // written and kb is an earlier block (rows without a query compute on zeros).
             const bool keep = (act >> z) & 1;
-            // (windowed: of all rows of the block, the last one's window begins last)
-            const bool all = keep && (act & kPbFull) && kb < qa + qi &&
-                             (!WIN || kb * kPfBlock > (qa + qi) * kPfBlock + 63 - p.window ||
-                              (kb + 1) * kPfBlock <= p.sinks);
-            const int32_t low = WIN ? pos - p.window + 1 - kb * kPfBlock : 0;
-            const int32_t sk = WIN ? p.sinks - kb * kPfBlock : 0;
+            const bool all = keep && (act & kPbFull) && kb < qa + qi;
             int32_t lim[kPfTiles];
             if (!all) {
                 const int32_t cut = keep && rowok ? pos - kb * kPfBlock + 1 : 0;
@@ -643,7 +619,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
             ok = wait(bar(kBarS + 2 * t + buf), (j >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
-            if (j > 0 && (j & wmask) == 0) {
+            if (j > 0 && (j & (kPbWindow - 1)) == 0) {
                 // A window is over: its sum goes to the output row, the next one begins at zero.
                 // (P V of block j - 2 ended before these scores were made, so the barrier is at most
                 // one phase behind, which its parity can tell.)
@@ -664,7 +640,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                         tc_ld16(ocol + 16u * cc, v);
                         tc_wait_ld();
                         uint32_t o[16];
-                        if (j > wlen) {
+                        if (j > kPbWindow) {
                             float e16[16];
                             tc_ld16(ecol + 16u * cc, e16);
                             tc_wait_ld();
@@ -736,8 +712,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
             // Key e of tile u is kept iff e < lim[u].
             if (!all) {
 #pragma unroll
-                for (int e = 0; e < 64; ++e)
-                    x[e] = e < lim[e >> 4] && (!WIN || e >= low || e < sk) ? x[e] : kPfNegInf;
+                for (int e = 0; e < 64; ++e) x[e] = e < lim[e >> 4] ? x[e] : kPfNegInf;
             }
             // the row maximum of the scores (log2 units); -inf stays -inf
             const float mx = fmaxf(fmaxf(max16(x) * fu[0], max16(x + 16) * fu[1]),
@@ -797,7 +772,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                     xfac = pow2i((int)x_new);
                     mref = m_new + x_new;
                 }
-                if ((j & wmask) != 0 && __any_sync(0xffffffffu, fo != 1.f)) {
+                if ((j & (kPbWindow - 1)) != 0 && __any_sync(0xffffffffu, fo != 1.f)) {
                     // O holds the window's blocks before this one: wait for them, then scale it
                     ok = wait(bar(kBarPv + t), (j - 1) & 1);
                     if (!ok) break;
@@ -885,7 +860,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
         if (SPLIT && use > 1) {
             // the row's sum, relative to 2^(m_used + xref), and what it is relative to
             if ((tmask >> t) & 1u) {
-                const bool more = j > wlen;  // (at a multiple of it the last window is still in O)
+                const bool more = j > kPbWindow;  // (at a multiple of it the last window is still in O)
                 const float down =
                     more && ref_m != kPfNegInf ? exp2f((ref_m - m_used) + (ref_x - xref)) : 0.f;
                 float* to = part + (r & 127) * (D + 4);
@@ -932,16 +907,7 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) v[e] = 0.f;
                 }
-                if (WIN && rowok && p.out_bf16 != 0) {
-                    uint16_t* to = reinterpret_cast<uint16_t*>(p.out) + row * D + 16 * cc;
-#pragma unroll
-                    for (int e = 0; e < 16; e += 8)
-                        *reinterpret_cast<uint4*>(to + e) = make_uint4(
-                            pack_bf16(v[e] * inv * up, v[e + 1] * inv * up),
-                            pack_bf16(v[e + 2] * inv * up, v[e + 3] * inv * up),
-                            pack_bf16(v[e + 4] * inv * up, v[e + 5] * inv * up),
-                            pack_bf16(v[e + 6] * inv * up, v[e + 7] * inv * up));
-                } else if (rowok) {
+                if (rowok) {
                     float* to = orow + 16 * cc;
 #pragma unroll
                     for (int e = 0; e < 16; e += 4) {
@@ -1010,13 +976,9 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
                     up2 = pow2i((int)whole);
                 }
                 const int64_t row = ((int64_t)b * p.Tq + (pos - c0)) * p.Hq + h0 + q_head(z);
-                o = make_float4(o.x * inv * up * up2, o.y * inv * up * up2, o.z * inv * up * up2,
+                *reinterpret_cast<float4*>(p.out + row * D + 4 * c4) =
+                    make_float4(o.x * inv * up * up2, o.y * inv * up * up2, o.z * inv * up * up2,
                                 o.w * inv * up * up2);
-                if (WIN && p.out_bf16 != 0)
-                    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + row * D + 4 * c4) =
-                        make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
-                else
-                    *reinterpret_cast<float4*>(p.out + row * D + 4 * c4) = o;
                 if (c4 == 0) {
                     if (p.m_out) p.m_out[row] = m == kPfNegInf ? kPfNegInf : m * kLn2;
                     if (p.e_out) p.e_out[row] = l;
@@ -1038,13 +1000,13 @@ prefill_block_kernel(const __grid_constant__ PbParams pp, int32_t nwords) {
 
 std::mutex g_pb_mutex;
 
-template <int D, bool SPLIT, bool WIN>
+template <int D, bool SPLIT>
 dattn_status_t ensure_smem(uint32_t bytes) {
     static int set[kMaxDevices] = {};  // a function attribute belongs to a device
     std::lock_guard<std::mutex> lock(g_pb_mutex);
     int& mine = set[device_index()];
     if ((int)bytes > mine) {
-        if (cudaFuncSetAttribute(prefill_block_kernel<D, SPLIT, WIN>,
+        if (cudaFuncSetAttribute(prefill_block_kernel<D, SPLIT>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)bytes) != cudaSuccess)
             return DATTN_ERR_CUDA;
@@ -1055,13 +1017,13 @@ dattn_status_t ensure_smem(uint32_t bytes) {
 
 // Clusters of s CTAs that the device holds at once (15 of 8, 36 of 4 and 76 of 2 on 152 SMs, one CTA
 // per SM whatever its shared memory); asked once per device and size.
-template <int D, bool WIN>
+template <int D>
 int32_t clusters_at_once(int32_t s, uint32_t bytes) {
     static std::atomic<int32_t> known[kMaxDevices][9] = {};
     std::atomic<int32_t>& mine = known[device_index()][s];
     int32_t n = mine.load(std::memory_order_relaxed);
     if (n > 0) return n - 1;
-    if (ensure_smem<D, true, WIN>(bytes) != DATTN_OK) return 0;
+    if (ensure_smem<D, true>(bytes) != DATTN_OK) return 0;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)s);
     cfg.blockDim = dim3(kPbThreads);
@@ -1072,7 +1034,7 @@ int32_t clusters_at_once(int32_t s, uint32_t bytes) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int at_once = 0;
-    if (cudaOccupancyMaxActiveClusters(&at_once, prefill_block_kernel<D, true, WIN>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&at_once, prefill_block_kernel<D, true>, &cfg) != cudaSuccess) {
         cudaGetLastError();
         at_once = 0;
     }
@@ -1082,7 +1044,7 @@ int32_t clusters_at_once(int32_t s, uint32_t bytes) {
 
 }  // namespace
 
-template <int D, bool WIN>
+template <int D>
 static dattn_status_t launch_d(const PfParams& p0, const void* k_pool, const void* v_pool,
                                const float* kv_scale, cudaStream_t stream) {
     PbParams pp{};
@@ -1093,10 +1055,7 @@ static dattn_status_t launch_d(const PfParams& p0, const void* k_pool, const voi
     pp.k_pool = static_cast<const uint8_t*>(k_pool);
     pp.v_pool = static_cast<const uint8_t*>(v_pool);
     pp.scale = reinterpret_cast<const float2*>(kv_scale);
-    if (WIN && p.out_bf16 != 0 && (int64_t)p.max_pages * p.P > kPbWindowMost &&
-        (int64_t)p.window + p.sinks > kPbWindowMost)
-        return DATTN_ERR_UNSUPPORTED;
-    const int32_t nwords = (int32_t)((pf_bitmap_blocks(p, 4) + 31) / 32);
+    const int32_t nwords = (p.max_pages * p.P / kPfBlock + 1 + 4 + 31) / 32;
     const PbSmem L = pb_smem_layout(D, pp.nq, nwords);
     if (L.total > 227u * 1024u) return DATTN_ERR_UNSUPPORTED;
     const int32_t blocks = (p.Tq + kPfBlock - 1) / kPfBlock + 1;  // query blocks a chunk can touch
@@ -1114,7 +1073,7 @@ static dattn_status_t launch_d(const PfParams& p0, const void* k_pool, const voi
     for (int32_t s = 8; s > 1 && pp.split == 1; s /= 2)
         if (tiles * s <= sms &&
             (int64_t)p.max_pages * p.P >= (int64_t)s * kPbSplitBlocks * kPfBlock &&
-            tiles <= clusters_at_once<D, WIN>(s, L.total)) {
+            tiles <= clusters_at_once<D>(s, L.total)) {
             pp.split = s;
             pp.whole = 0;
         }
@@ -1127,10 +1086,9 @@ static dattn_status_t launch_d(const PfParams& p0, const void* k_pool, const voi
             p.kv_group = G;
             break;
         }
-    auto kern = pp.split > 1 ? prefill_block_kernel<D, true, WIN>
-                             : prefill_block_kernel<D, false, WIN>;
+    auto kern = pp.split > 1 ? prefill_block_kernel<D, true> : prefill_block_kernel<D, false>;
     const dattn_status_t st =
-        pp.split > 1 ? ensure_smem<D, true, WIN>(L.total) : ensure_smem<D, false, WIN>(L.total);
+        pp.split > 1 ? ensure_smem<D, true>(L.total) : ensure_smem<D, false>(L.total);
     if (st != DATTN_OK) return st;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)ctas);
@@ -1149,11 +1107,8 @@ static dattn_status_t launch_d(const PfParams& p0, const void* k_pool, const voi
 
 dattn_status_t launch_prefill_block(const PfParams& p, const void* k_pool, const void* v_pool,
                                     const float* kv_scale, int D, cudaStream_t stream) {
-    if (p.window > 0)
-        return D == 64 ? launch_d<64, true>(p, k_pool, v_pool, kv_scale, stream)
-                       : launch_d<128, true>(p, k_pool, v_pool, kv_scale, stream);
-    return D == 64 ? launch_d<64, false>(p, k_pool, v_pool, kv_scale, stream)
-                   : launch_d<128, false>(p, k_pool, v_pool, kv_scale, stream);
+    return D == 64 ? launch_d<64>(p, k_pool, v_pool, kv_scale, stream)
+                   : launch_d<128>(p, k_pool, v_pool, kv_scale, stream);
 }
 
 }  // namespace dattn

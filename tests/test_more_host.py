@@ -99,15 +99,13 @@ def test_prefill_refusals(lib):
     assert prefill(lib, Tq=65) == INVALID  # more than the block table holds
     for fmt in (dattn.KV_FP8_E4M3, dattn.KV_INT4, dattn.KV_MIXED):
         assert prefill(lib, layout(fmt)) == UNSUPPORTED
-    wide = layout(dattn.KV_FP8_BLOCK, cols=1 << 14)  # 2^18 tokens
-    assert prefill(lib, wide, W=1 << 17, S=1, bf16=1) == UNSUPPORTED
 
 
 def test_shared_refusals(lib):
     assert shared(lib, T=0) == INVALID and shared(lib, T=5) == UNSUPPORTED
     assert shared(lib, groups=-1) == INVALID
     assert shared(lib, groups=3) == INVALID  # more groups than requests
-    assert shared(lib, B=2000, groups=1025) == UNSUPPORTED
+    assert shared(lib, B=2000, groups=513) == UNSUPPORTED
     assert shared(lib, indptr=None) == INVALID and shared(lib, prefix=None) == INVALID
     for fmt in (dattn.KV_FP8_E4M3, dattn.KV_INT4, dattn.KV_MIXED):
         assert shared(lib, layout(fmt)) == UNSUPPORTED
