@@ -121,17 +121,17 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 // 2-D map over a pool of codes seen as rows of row_bytes bytes (8-bit: d; packed 4-bit:
-// d / 2): one box {row_bytes, 16} is a 16-token row group of one (page, KV head), landing as
+// d / 2): one box {row_bytes, box_rows} (16: a 16-token row group of one (page, KV head)) lands as
 // [row][row_bytes] with the swizzle of the row's size (128, 64 or 32 bytes), which keeps
 // ldmatrix conflict-free.
 dattn_status_t make_kv_tensor_map_u8(void* tmap_out, const void* pool, int64_t rows,
-                                     int row_bytes) {
+                                     int row_bytes, int box_rows) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
     if (fn == nullptr) return DATTN_ERR_CUDA;
     if (row_bytes != 128 && row_bytes != 64 && row_bytes != 32) return DATTN_ERR_UNSUPPORTED;
     cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
-    cuuint32_t box[2] = {(cuuint32_t)row_bytes, 16};
+    cuuint32_t box[2] = {(cuuint32_t)row_bytes, (cuuint32_t)box_rows};
     cuuint32_t estr[2] = {1, 1};
     const CUtensorMapSwizzle swz = row_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
                                    : row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B

@@ -204,9 +204,9 @@ int device_index();
 int sm_count_current();
 dattn_status_t make_kv_tensor_map(void* tmap_out, const void* pool, int64_t rows, int D);
 // 2-D map over rows of `row_bytes` one-byte elements (8-bit codes: d; packed 4-bit codes:
-// d / 2), one box of 16 rows, swizzled by the row size (128, 64 or 32 bytes).
+// d / 2), one box of box_rows rows, swizzled by the row size (128, 64 or 32 bytes).
 dattn_status_t make_kv_tensor_map_u8(void* tmap_out, const void* pool, int64_t rows,
-                                     int row_bytes);
+                                     int row_bytes, int box_rows = 16);
 
 // The kernels of dattn_rope and dattn_rope_append (rope.cu).
 dattn_status_t launch_rope(const dattn_rotation* rot, const void* x, int64_t x_stride, void* out,

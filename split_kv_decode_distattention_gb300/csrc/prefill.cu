@@ -647,14 +647,15 @@ PFN_cuTensorMapEncodeTiled_v12000 tc_encode_fn() {
 }
 
 // The pool as rows of d bf16 values split into 128-byte halves (dims {64, rows, d/64}), with
-// a box of one half of 16 rows: the tcgen05 operands keep each half of a key block as 64
+// a box of one half of box_rows rows: the tcgen05 operands keep each half of a key block as 64
 // contiguous 128-byte rows.
-dattn_status_t make_half_tensor_map(void* tmap_out, const void* pool, int64_t rows, int D) {
+dattn_status_t make_half_tensor_map(void* tmap_out, const void* pool, int64_t rows, int D,
+                                    int box_rows) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = tc_encode_fn();
     if (fn == nullptr) return DATTN_ERR_CUDA;
     cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)(D / 64)};
     cuuint64_t strides[2] = {(cuuint64_t)D * 2, 128};
-    cuuint32_t box[3] = {64, 16, 1};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = fn(static_cast<CUtensorMap*>(tmap_out), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                     const_cast<void*>(pool), dims, strides, box, estr,

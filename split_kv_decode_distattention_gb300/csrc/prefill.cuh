@@ -42,9 +42,10 @@ dattn_status_t launch_prefill_block(const PfParams& p, const void* k_pool, const
                                     const float* kv_scale, int D, cudaStream_t stream);
 
 // The driver's tensor-map encoder (nullptr: not found), and a 3-D map over a bf16 pool whose boxes are
-// one 128-byte half of 16 rows (prefill.cu).
+// one 128-byte half of `box` rows (prefill.cu).
 PFN_cuTensorMapEncodeTiled_v12000 tc_encode_fn();
-dattn_status_t make_half_tensor_map(void* tmap_out, const void* pool, int64_t rows, int D);
+dattn_status_t make_half_tensor_map(void* tmap_out, const void* pool, int64_t rows, int D,
+                                    int box_rows = 16);
 
 constexpr float kTcRescale = 8.f;    // lazy rescale threshold (log2 units)
 

@@ -27,7 +27,7 @@ namespace {
 // workspace in fp32.
 constexpr int32_t kShEmpty = 64;
 constexpr int32_t kShSegCost = 4;    // a piece's fixed cost in blocks
-constexpr int32_t kShMinCost = 6;    // blocks (and fixed costs) of a CTA at least
+constexpr int32_t kShMinCost = 4;    // blocks (and fixed costs) of a CTA at least
 constexpr int32_t kShMaxGroups = kTaThreads;  // (a thread for each)
 
 struct SharedParams {

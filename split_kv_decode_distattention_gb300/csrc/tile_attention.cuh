@@ -12,7 +12,7 @@
 //             base 2 on packed fp32 pairs, and the weights back as two bf16 terms (p cut to its upper 16
 //             bits, and the exact rest, rounded), which the second product reads; the accumulator is
 //             rescaled only when a row's maximum rises by more than 2^8;
-//   8-11      bf16 pool: warps 8 and 9 copy K and V tiles by TMA. Block-scaled pool: all four widen the
+//   8-11      bf16 pool: warps 8 and 10 copy K, 9 and 11 V by TMA. Block-scaled pool: all four widen the
 //             codes that warp 15 copied to code * scale, which is a bf16 number: both formats compute alike;
 //   12, 13    tile 0, 1: S = Q K^T of the next block, then O += P V of this one, issued by one lane;
 //   14        the queries, by TMA.
@@ -42,9 +42,13 @@ constexpr int kTaQWarp = 14;
 constexpr int kTaCodeWarp = 15;
 constexpr int kTaMeta = 16;          // blocks' metadata slots
 
-// Stages of a key block's K and of its V (bf16 rows), and of its codes (block-scaled pool)
+// Stages of a key block's K and of its V (bf16 rows), and of its codes (block-scaled pool). A wait tells
+// the phase at hand from the one before, so whoever fills (or reads) a stage has to have waited for its
+// use before. Two warps fill the bf16 stages in turn, and an alt item's tiles read every other block: the
+// numbers of bf16 stages are even, so that a stage has one of the warps, and within an item one of the
+// tiles, to itself.
 __host__ __device__ constexpr int ta_kstages(int fmt) { return fmt == DATTN_KV_BF16 ? 4 : 2; }
-__host__ __device__ constexpr int ta_vstages(int fmt) { return fmt == DATTN_KV_BF16 ? 5 : 3; }
+__host__ __device__ constexpr int ta_vstages(int fmt) { return fmt == DATTN_KV_BF16 ? 4 : 3; }
 __host__ __device__ constexpr int ta_cstages(int fmt) { return fmt == DATTN_KV_BF16 ? 0 : 4; }
 
 struct TaSmem {
@@ -82,6 +86,7 @@ struct TaParams {
     int32_t num_pages, Hkv, P, max_pages;
     const int32_t* block_table;
     int32_t Hq, g, tok;   // tok: query tokens of a tile
+    int32_t box;          // rows of a copy: 16, 32 or 64, a divisor of P
     float sl2;            // scale * log2(e)
     const float2* scale;  // block-scaled pool: [num_pages][Hkv][P/16] (K, V)
     int32_t* dev_err;
@@ -104,6 +109,11 @@ struct TaRow {
     int32_t lim, low, sinks;
 };
 
+// Bits 0 .. n - 1 (n of any sign and size).
+__device__ __forceinline__ uint64_t below64(int32_t n) {
+    return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
+}
+
 template <class Job, int D, int FMT>
 __global__ void __launch_bounds__(kTaThreads, 1)
 tile_attention_kernel(const __grid_constant__ TaParams p, const __grid_constant__ typename Job::Params jp,
@@ -114,6 +124,8 @@ tile_attention_kernel(const __grid_constant__ TaParams p, const __grid_constant_
     constexpr bool BLK = FMT == DATTN_KV_FP8_BLOCK;
     constexpr int NK = ta_kstages(FMT), NV = ta_vstages(FMT), NC = BLK ? ta_cstages(FMT) : 1;
     static_assert(NK <= 5 && NV <= 5 && NC <= 5, "the barriers' place");
+    static_assert(BLK || (NK % 2 == 0 && NV % 2 == 0), "a stage belongs to one of two warps");
+    static_assert(NK % 2 == 0 && kTaMeta % 2 == 0, "within an alt item, to one tile");
     constexpr uint32_t kHalf = 64u * 128u;  // a 128-byte half of a key block's rows
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = smem_raw;
@@ -169,14 +181,10 @@ tile_attention_kernel(const __grid_constant__ TaParams p, const __grid_constant_
         tc_alloc(smem_u32(base + L.taddr), 512u);
         tc_relinquish();
     }
-    // Rows of the queries that no copy fills (128 is no multiple of g) compute, on zeros. V rows that the
-    // MMA reads with weight 0 (tiles that are never loaded) must hold finite data.
+    // Rows of the queries that no copy fills (128 is no multiple of g) compute, on zeros.
     if (128 % p.g != 0)
         for (uint32_t i = tid; i < 256u * D * 2u / 16u; i += kTaThreads)
             reinterpret_cast<uint4*>(base + L.q)[i] = make_uint4(0u, 0u, 0u, 0u);
-    if constexpr (!BLK)
-        for (uint32_t i = tid; i < NV * L.blk_bytes / 16u; i += kTaThreads)
-            reinterpret_cast<uint4*>(base + L.vst)[i] = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
     tc_fence_before();
     Job job(p, jp, base + L.job);  // (waits for the previous kernel where the job reads its results)
@@ -235,13 +243,18 @@ tile_attention_kernel(const __grid_constant__ TaParams p, const __grid_constant_
                 const int32_t k0 = mt.x * kPfBlock, cut = lim - k0, from = low - k0, sk = sinks - k0;
                 if (!__all_sync(0xffffffffu, cut >= kPfBlock && mt.y == kFull &&
                                                  (from <= 0 || sk >= kPfBlock))) {
-                    int32_t lims[kPfTiles];
+                    uint64_t see = below64(cut) & (~below64(from) | below64(sk));
+                    if (mt.y != kFull) {
+                        uint64_t held = 0ull;
 #pragma unroll
-                    for (int u = 0; u < kPfTiles; ++u)
-                        lims[u] = min(16 * u + ((mt.y >> (5 * u)) & 31), cut);
+                        for (int u = 0; u < kPfTiles; ++u)
+                            held |= below64((mt.y >> (5 * u)) & 31) << (16 * u);
+                        see &= held;
+                    }
+                    const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
 #pragma unroll
                     for (int e = 0; e < 64; ++e)
-                        xs[e] = e < lims[e >> 4] && (e >= from || e < sk) ? xs[e] : kPfNegInf;
+                        xs[e] = ((e < 32 ? s0 : s1) >> (e & 31)) & 1u ? xs[e] : kPfNegInf;
                 }
                 const float mx = row_max64(xs) * sl2a;  // log2 units; -inf stays -inf
                 m_true = fmaxf(m_true, mx);
@@ -295,22 +308,15 @@ tile_attention_kernel(const __grid_constant__ TaParams p, const __grid_constant_
                 l = l * f + (((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7])));
                 tc_wait_st();
                 if (!BLK) {
-                    // V rows of keys that do not exist, in a tile where others do, hold other tokens or
-                    // nothing: zeros, so that a zero weight cannot meet a NaN (P V of this block waits
-                    // for this warp, and the stage's next use for P V)
-                    bool short_tile = false;
-#pragma unroll
-                    for (int u = 0; u < kPfTiles; ++u) {
-                        const int32_t hi = (mt.y >> (5 * u)) & 31;
-                        short_tile = short_tile || (hi > 0 && hi < 16);
-                    }
-                    if (short_tile && wait(bar(kTaVFull + i % NV), (i / NV) & 1)) {
+                    // V rows of keys that do not exist hold other tokens or nothing: zeros, so that a zero
+                    // weight cannot meet a NaN (P V of this block waits for this warp, and the stage's
+                    // next use for P V)
+                    if (mt.y != kFull && wait(bar(kTaVFull + i % NV), (i / NV) & 1)) {
                         uint8_t* vst = base + L.vst + (i % NV) * L.blk_bytes;
                         for (int idx = r; idx < 64 * KH * 8; idx += 128) {
                             const int kr = idx / (KH * 8), rem = idx - kr * (KH * 8);
                             const int hh = rem >> 3, ch = rem & 7;
-                            const int32_t hi = (mt.y >> (5 * (kr >> 4))) & 31;
-                            if (hi > 0 && (kr & 15) >= hi)
+                            if ((kr & 15) >= ((mt.y >> (5 * (kr >> 4))) & 31))
                                 *reinterpret_cast<uint4*>(vst + hh * kHalf + kr * 128 + ch * 16) =
                                     make_uint4(0u, 0u, 0u, 0u);
                         }
@@ -407,8 +413,12 @@ tile_attention_kernel(const __grid_constant__ TaParams p, const __grid_constant_
             // ones. A stage is given back by both warps, or twice by the one that read it.
             auto second = [&](uint32_t i, uint32_t jj, uint32_t more) -> bool {
                 const uint32_t s = i % NV;
-                if (!wait(bar(kTaVFull + s), (i / NV) & 1)) return false;
+                // The weights first: with them, every product of earlier items is done, by both tiles, and
+                // so the stage's earlier uses are over. (Within an alt item the use before was this tile's
+                // own, or, of three stages, one whose V was written before this block's K. K's stages need
+                // no such care: an item's queries come when both tiles have read all K of the one before.)
                 if (!wait(bar(kTaP) + 16u * t + 8u * (jj & 1u), (jj >> 1) & 1u)) return false;
+                if (!wait(bar(kTaVFull + s), (i / NV) & 1)) return false;
                 tc_fence_after();
                 const uint32_t v_lo = vd + s * (64u * D * 2u >> 4), from = sc + 64u * (jj & 1u);
 #pragma unroll
@@ -497,12 +507,17 @@ tile_attention_kernel(const __grid_constant__ TaParams p, const __grid_constant_
             }
         }
         __syncwarp();
-    } else if (warp == (BLK ? kTaCodeWarp : kTaConvWarp) || (!BLK && warp == kTaConvWarp + 1)) {
+    } else if (BLK ? warp == kTaCodeWarp : warp >= kTaConvWarp && warp < kTaConvWarp + 4) {
         // -------------------------------------------------------------------- the key blocks
-        // bf16: warp 8 copies K and leaves the blocks' metadata, warp 9 copies V; block-scaled pool:
-        // warp 15 copies the codes of both. Lane (grp, u) resolves tile u of block grp of eight.
+        // bf16: warps 8 and 10 copy K and leave the blocks' metadata, warps 9 and 11 copy V, each every
+        // other block (a warp issues the copies of a block of four pages in about a microsecond); block-
+        // scaled pool: warp 15 copies the codes of both. Lane (grp, u) resolves tile u of block grp of
+        // eight, and copies p.box rows, one or two or all of the block's tiles.
         const int grp = lane >> 2, u = lane & 3;
-        const bool isv = !BLK && warp == kTaConvWarp + 1;
+        const bool isv = !BLK && (warp & 1) != 0;
+        const uint32_t turn = BLK ? 0u : (uint32_t)(warp - kTaConvWarp) >> 1;
+        const int32_t box = p.box;
+        const bool copies = (u * 16) % box == 0;
         const uint64_t pol = policy_evict_normal();
         const uint32_t NS = BLK ? NC : isv ? NV : NK;
         const int full0 = BLK ? kTaCFull : isv ? kTaVFull : kTaKFull;
@@ -534,7 +549,7 @@ tile_attention_kernel(const __grid_constant__ TaParams p, const __grid_constant_
             place(grp, y, hi, sc);
             for (int32_t b0 = 0; b0 < it.count && ok; b0 += 8) {
                 place(b0 + 8 + grp, ny, nhi, nsc);  // (on its way behind this group's copies)
-                int32_t his = hi << (5 * u), valid = hi > 0 ? 1 : 0;
+                int32_t his = hi << (5 * u), valid = hi > 0 && copies ? 1 : 0;
 #pragma unroll
                 for (int o = 1; o < 4; o <<= 1) {
                     his |= __shfl_xor_sync(0xffffffffu, his, o);
@@ -542,6 +557,7 @@ tile_attention_kernel(const __grid_constant__ TaParams p, const __grid_constant_
                 }
                 for (int k = 0; k < 8 && b0 + k < it.count; ++k) {
                     const uint32_t i = done + b0 + k, ms = i % kTaMeta, s = i % NS;
+                    if (!BLK && (i & 1u) != turn) continue;
                     if (!isv && i >= (uint32_t)kTaMeta)
                         ok = wait(bar(kTaMetaEmpty + ms), ((i / kTaMeta) & 1) ^ 1);
                     if (ok && i >= NS) ok = wait(bar(empty0 + s), ((i / NS) & 1) ^ 1);
@@ -556,9 +572,9 @@ tile_attention_kernel(const __grid_constant__ TaParams p, const __grid_constant_
                     }
                     __syncwarp();
                     if (grp == k && u == 0)
-                        mbar_arrive_expect_tx(full, (uint32_t)valid * (BLK ? 2u * 16u * D : KH * 2048u));
+                        mbar_arrive_expect_tx(full, (uint32_t)(valid * box) * (BLK ? 2u * D : KH * 128u));
                     __syncwarp();
-                    if (grp == k && hi > 0) {
+                    if (grp == k && hi > 0 && copies) {
                         if constexpr (BLK) {
                             const uint32_t dst = st0 + s * 2u * L.code_bytes + u * 16u * D;
                             tma_load_2d(dst, &tmap_k, 0, y, full, pol);
@@ -597,15 +613,22 @@ tile_attention_kernel(const __grid_constant__ TaParams p, const __grid_constant_
         const int c16 = D == 64 ? ct & 3 : (ct & 3) | ((ct >> 1) & 4);
         const int rr = D == 64 ? ct >> 2 : ((ct >> 2) & 1) | ((ct >> 4) << 1);
         const uint32_t half = (c16 >> 2) * kHalf, ch = 2u * (c16 & 3);
-        // a block's K or V: rows without a token become zeros
+        // A block's K or V; rows without a token become zeros. All codes are read before the first row is
+        // written: the compiler cannot tell the stages apart, and read them one after another (a 4K chunk
+        // through a window of 4096: 427 us, 386 so). Shifting the codes' bits to a bf16's places and two
+        // bf16 products instead of the conversions by fp16 and fp32 load the pipe that the softmax fills
+        // (533 us).
         auto widen = [&](const uint8_t* from, uint8_t* to, const float* sc, int32_t his) {
+            uint4 c[NP];
+#pragma unroll
+            for (int a = 0; a < NP; ++a)
+                c[a] = *reinterpret_cast<const uint4*>(from + swz_rows<D>((uint32_t)(rr + RP * a), c16));
 #pragma unroll
             for (int a = 0; a < NP; ++a) {
                 const uint32_t r = (uint32_t)(rr + RP * a);
-                const uint4 c = *reinterpret_cast<const uint4*>(from + swz_rows<D>(r, c16));
                 const bool some = (int32_t)(r & 15u) < ((his >> (5 * (r >> 4))) & 31);
                 const float f = sc[2 * (r >> 4)];
-                const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+                const uint32_t w[4] = {c[a].x, c[a].y, c[a].z, c[a].w};
                 uint32_t o[8];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
@@ -672,7 +695,7 @@ inline dattn_status_t make_q_tensor_map(void* tmap_out, const void* q, int64_t t
 }
 
 template <class Job, int D, int FMT>
-dattn_status_t launch_tiles(const TaParams& p, const typename Job::Params& jp, const void* q,
+dattn_status_t launch_tiles(const TaParams& p0, const typename Job::Params& jp, const void* q,
                             int64_t tokens, const void* k_pool, const void* v_pool, int32_t grid,
                             uint32_t job_bytes, cudaStream_t stream) {
     const TaSmem L = ta_smem_layout(D, FMT, job_bytes);
@@ -690,6 +713,8 @@ dattn_status_t launch_tiles(const TaParams& p, const typename Job::Params& jp, c
             mine = (int)L.total;
         }
     }
+    TaParams p = p0;
+    p.box = p.P % 64 == 0 ? 64 : p.P % 32 == 0 ? 32 : 16;
     alignas(64) CUtensorMap tq;
     alignas(64) CUtensorMap tk;
     alignas(64) CUtensorMap tv;
@@ -697,11 +722,11 @@ dattn_status_t launch_tiles(const TaParams& p, const typename Job::Params& jp, c
     dattn_status_t st;
     if ((st = make_q_tensor_map(&tq, q, tokens, p.Hq, p.g, p.tok, D)) != DATTN_OK) return st;
     if (FMT == DATTN_KV_BF16) {
-        if ((st = make_half_tensor_map(&tk, k_pool, rows, D)) != DATTN_OK) return st;
-        if ((st = make_half_tensor_map(&tv, v_pool, rows, D)) != DATTN_OK) return st;
+        if ((st = make_half_tensor_map(&tk, k_pool, rows, D, p.box)) != DATTN_OK) return st;
+        if ((st = make_half_tensor_map(&tv, v_pool, rows, D, p.box)) != DATTN_OK) return st;
     } else {
-        if ((st = make_kv_tensor_map_u8(&tk, k_pool, rows, D)) != DATTN_OK) return st;
-        if ((st = make_kv_tensor_map_u8(&tv, v_pool, rows, D)) != DATTN_OK) return st;
+        if ((st = make_kv_tensor_map_u8(&tk, k_pool, rows, D, p.box)) != DATTN_OK) return st;
+        if ((st = make_kv_tensor_map_u8(&tv, v_pool, rows, D, p.box)) != DATTN_OK) return st;
     }
     return launch_pdl(tile_attention_kernel<Job, D, FMT>, dim3((unsigned)grid), dim3(kTaThreads),
                       L.total, stream, p, jp, tq, tk, tv) == cudaSuccess

@@ -304,3 +304,25 @@ def test_chunk_of_many_tiles_for_each_sm(dattn, fmt, g):
                                             pool.rows("k", b)[:, h // g], pool.rows("v", b)[:, h // g],
                                             0.125, sees(lens[b], T, W, S), weight_error("bf16"))
             check(out[b, :, h], None, None, ref, bound, 0, 0, 0, f"{fmt} g={g} b={b} h={h}")
+
+
+def test_every_code_of_the_block_scaled_pool_comes_through_exactly(dattn):
+    """One key with weight 1: the output is its V row. All codes but NaN, scales from 2^-100 to 2^100;
+    a NaN code gives NaN in its channel."""
+    d, P = 128, 16
+    codes = torch.arange(256, dtype=torch.uint8)
+    for k in (-100, -9, 0, 20, 100):
+        kp = torch.zeros(2, 1, P, d, dtype=torch.uint8)
+        vp = torch.zeros(2, 1, P, d, dtype=torch.uint8)
+        vp[:, 0, 0] = codes.view(2, d)
+        sc = torch.tensor([1.0, 2.0 ** k, 1.0, 2.0 ** k], device=DEV)
+        lay = dattn.KVLayout(2, 1, d, P, torch.tensor([[0], [1]], dtype=torch.int32, device=DEV),
+                             dattn.KV_FP8_BLOCK, sc)
+        q = torch.zeros(2, 1, 1, d, dtype=torch.bfloat16, device=DEV)
+        out = torch.empty(2, 1, 1, d, device=DEV)
+        dattn.dattn_prefill_window(lay, kp.to(DEV), vp.to(DEV), q, 1.0,
+                                   torch.ones(2, dtype=torch.int32, device=DEV), 5, 0, out)
+        ref = codes.view(torch.float8_e4m3fn).double() * 2.0 ** k
+        got = out.double().cpu().view(-1)
+        assert torch.equal(torch.isnan(got), torch.isnan(ref))
+        assert torch.equal(torch.nan_to_num(got), torch.nan_to_num(ref))
