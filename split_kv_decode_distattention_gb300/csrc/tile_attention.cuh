@@ -114,6 +114,16 @@ __device__ __forceinline__ uint64_t below64(int32_t n) {
     return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
 }
 
+// Two fp16 values times a packed pair of factors, as bf16 values (exact for codes and powers of two).
+__device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t h, uint64_t f) {
+    float a, b;
+    asm("{\n\t.reg .b64 x;\n\tmov.b64 x, {%2, %3};\n\tmul.rn.f32x2 x, x, %4;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(a), "=f"(b)
+        : "f"(f16_lo(h)), "f"(f16_hi(h)), "l"(f));
+    return pack_bf16(a, b);
+}
+
 template <class Job, int D, int FMT>
 __global__ void __launch_bounds__(kTaThreads, 1)
 tile_attention_kernel(const __grid_constant__ TaParams p, const __grid_constant__ typename Job::Params jp,
@@ -127,6 +137,7 @@ tile_attention_kernel(const __grid_constant__ TaParams p, const __grid_constant_
     static_assert(BLK || (NK % 2 == 0 && NV % 2 == 0), "a stage belongs to one of two warps");
     static_assert(NK % 2 == 0 && kTaMeta % 2 == 0, "within an alt item, to one tile");
     constexpr uint32_t kHalf = 64u * 128u;  // a 128-byte half of a key block's rows
+    constexpr int32_t kFull = 16 | (16 << 5) | (16 << 10) | (16 << 15);  // tokens of a whole block's tiles
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = smem_raw;
     const TaSmem L = ta_smem_layout(D, FMT, 0u);
@@ -206,7 +217,6 @@ tile_attention_kernel(const __grid_constant__ TaParams p, const __grid_constant_
         float4* ml = reinterpret_cast<float4*>(base + L.ml);
         // |scale| log2(e), at least 1e-30 so that a masked key (-inf) never meets a zero factor
         const float sl2a = fmaxf(fabsf(p.sl2), 1e-30f);
-        constexpr int32_t kFull = 16 | (16 << 5) | (16 << 10) | (16 << 15);
         uint32_t j = 0u, held = 0u;  // blocks that the tile kept; items of which it kept some
         // (after an abort a warp still walks the items: all meet at the barriers of the alt ones)
         while (job.next(it)) {
@@ -623,19 +633,27 @@ tile_attention_kernel(const __grid_constant__ TaParams p, const __grid_constant_
 #pragma unroll
             for (int a = 0; a < NP; ++a)
                 c[a] = *reinterpret_cast<const uint4*>(from + swz_rows<D>((uint32_t)(rr + RP * a), c16));
+            if (his != kFull) {  // codes of +0 for rows without a token
+#pragma unroll
+                for (int a = 0; a < NP; ++a) {
+                    const uint32_t r = (uint32_t)(rr + RP * a);
+                    if ((int32_t)(r & 15u) >= ((his >> (5 * (r >> 4))) & 31))
+                        c[a] = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
 #pragma unroll
             for (int a = 0; a < NP; ++a) {
                 const uint32_t r = (uint32_t)(rr + RP * a);
-                const bool some = (int32_t)(r & 15u) < ((his >> (5 * (r >> 4))) & 31);
                 const float f = sc[2 * (r >> 4)];
+                const uint64_t f2 = pack_f32x2(f, f);
                 const uint32_t w[4] = {c[a].x, c[a].y, c[a].z, c[a].w};
                 uint32_t o[8];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     uint32_t lo, hi;
                     e4m3x4_to_f16(w[x], lo, hi);
-                    o[2 * x] = some ? pack_bf16(f16_lo(lo) * f, f16_hi(lo) * f) : 0u;
-                    o[2 * x + 1] = some ? pack_bf16(f16_lo(hi) * f, f16_hi(hi) * f) : 0u;
+                    o[2 * x] = scaled_bf16x2(lo, f2);
+                    o[2 * x + 1] = scaled_bf16x2(hi, f2);
                 }
                 *reinterpret_cast<uint4*>(to + half + swz128(r, ch)) = make_uint4(o[0], o[1], o[2], o[3]);
                 *reinterpret_cast<uint4*>(to + half + swz128(r, ch + 1u)) =
