@@ -84,21 +84,30 @@ __device__ __forceinline__ void chunk_values(const Chunk<FMT>& c, float scale, b
     }
 }
 
+// By a whole warp; `some`: this lane's row is read. In fp32 two neighbouring lanes (of one row) write
+// their 64 bytes in two stores of 32 bytes each, the lanes' halves exchanged, so that a store fills
+// whole sectors (three requests of 4-bit and 8-bit heads: 22.9 us without).
 template <int FMT, bool F32>
 __device__ __forceinline__ void store_chunk(void* out, int64_t at, const Chunk<FMT>& c, float scale,
-                                            bool i4) {
+                                            bool i4, bool some) {
     if constexpr (FMT == DATTN_KV_BF16 && !F32) {  // the values as they are
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) =
-            make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
+        if (some)
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) =
+                make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
         return;
     }
     float x[8];
     chunk_values<FMT>(c, scale, i4, x);
     if constexpr (F32) {
-        float4* to = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-        to[0] = make_float4(x[0], x[1], x[2], x[3]);
-        to[1] = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
+        const bool odd = threadIdx.x & 1;
+        float y[4];  // the other lane's: an even lane gets the first half, an odd one the second
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = __shfl_xor_sync(0xffffffffu, odd ? x[i] : x[4 + i], 1);
+        if (!some) return;
+        float4* to = reinterpret_cast<float4*>(static_cast<float*>(out) + at) - (odd ? 2 : 0);
+        to[odd] = odd ? make_float4(y[0], y[1], y[2], y[3]) : make_float4(x[0], x[1], x[2], x[3]);
+        to[2 + odd] = odd ? make_float4(x[4], x[5], x[6], x[7]) : make_float4(y[0], y[1], y[2], y[3]);
+    } else if (some) {
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) =
             make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
                        pack_bf16(x[6], x[7]));
@@ -178,6 +187,7 @@ kv_read_kernel(const __grid_constant__ ReadParams p) {
             const int r = r0 + a * RPA + rr;
             const int32_t page = pages[r], slot = slots[r];
             ks[a] = vs[a] = 1.f;
+            k[a] = v[a] = Chunk<FMT>{};
             if (page < 0) continue;
             const int64_t at = (((int64_t)page * heads + hc) * p.P + slot) * row_bytes + at_bytes;
             if (p.k_out) load_chunk<FMT>(k[a], kp + at, i4);
@@ -196,10 +206,10 @@ kv_read_kernel(const __grid_constant__ ReadParams p) {
 #pragma unroll
         for (int a = 0; a < NA; ++a) {
             const int r = r0 + a * RPA + rr;
-            if (pages[r] < 0) continue;
+            const bool some = pages[r] >= 0;
             const int64_t n = row0 + r, c = (int64_t)h * D + 8 * c8;
-            if (p.k_out) store_chunk<FMT, F32>(p.k_out, n * p.k_stride + c, k[a], ks[a], i4);
-            if (p.v_out) store_chunk<FMT, F32>(p.v_out, n * p.v_stride + c, v[a], vs[a], i4);
+            if (p.k_out) store_chunk<FMT, F32>(p.k_out, n * p.k_stride + c, k[a], ks[a], i4, some);
+            if (p.v_out) store_chunk<FMT, F32>(p.v_out, n * p.v_stride + c, v[a], vs[a], i4, some);
         }
     }
 }
