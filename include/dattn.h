@@ -623,9 +623,11 @@ dattn_status_t dattn_prefill(const dattn_kv_layout *layout, const void *k_pool,
  *   out      (device) fp32, or bf16 when out_bf16 = 1, [B][Tq][Hq][d]
  *   m, e     (device, nullable) fp32 [B][Tq][Hq], as for dattn_prefill
  * A seq_len below Tq is flagged with DATTN_DEVERR_LEN_OOB, and that request's outputs are left
- * untouched. The precision is dattn_prefill's; over the block-scaled pool with a bf16 output the sums
- * are not emptied on the way, so that window + sinks above 2^17 needs an fp32 output there
- * (DATTN_ERR_UNSUPPORTED, unless the block table holds no more tokens than that).
+ * untouched. As for dattn_prefill the products take a key block of 64 tokens as a whole, so that a NaN
+ * among the values of a token (or an infinity) reaches every query of its tile that meets the block.
+ * Precision, over both pools: weights of 16 bits or more, sums in fp32 that the tensor cores round
+ * towards zero, 8 times a key block: over n keys a result is smaller than the exact one by up to
+ * n / 8 * 2^-24 of its norm.
  */
 dattn_status_t dattn_prefill_window(const dattn_kv_layout *layout, const void *k_pool,
                                     const void *v_pool, const dattn_bf16 *q, int32_t B,

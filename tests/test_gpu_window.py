@@ -185,6 +185,8 @@ CHUNKS = [
     ([500], 300, 4, 2, 128, 16, 5, OVER),             # all tokens are first tokens
     ([3000], 1, 8, 2, 128, 128, 777, 10),             # one token
     ([4200], 70, 4, 4, 64, 16, 3000, 5),              # more than 32 blocks seen by a row
+    ([500, 333], 200, 7, 1, 128, 96, 150, 20),        # pages of 96 and 48 tokens; g = 7 and 6
+    ([500, 333], 200, 12, 2, 64, 48, 150, 20),
 ]
 
 
