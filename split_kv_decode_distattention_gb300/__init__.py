@@ -721,11 +721,55 @@ def dattn_decode_multi(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_le
         _stream_on(stream, here)), "dattn_decode_multi")
 
 
-def _out_bf16(out) -> bool:
-    """Whether the attention's output is bf16 (else it is float32)."""
-    if out.dtype != torch.float32 and out.dtype != torch.bfloat16:
+def _arg(t, here: int, n: int, dtype, name: str):
+    """The pointer of a tensor argument: contiguous, of the dtype, on device `here`, with at least the
+    n elements that the call touches (None: None). All of a tensor's checks in one step: a call's host
+    time is mostly its checks."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {str(dtype)[6:]}")
+    if t.numel() < n:
+        raise ValueError(f"{name} holds {t.numel()} elements; the call needs {n}")
+    if t.get_device() != here:
+        _elsewhere(t, here)
+    if not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _pools(layout, k_pool, v_pool, B: int):
+    """(device, pointer of k_pool, of v_pool) of a call over B requests' block-table rows."""
+    pool, scales, _, table = layout.sizes
+    types = layout.pool_types
+    for t, name in ((k_pool, "k_pool"), (v_pool, "v_pool")):
+        if t.dtype not in types:
+            raise TypeError(f"{name} must be {types[0]} for this layout")
+    here = _layout_device(layout, k_pool)
+    _size(layout.block_table, B * table, "block_table")
+    if scales:
+        _size(layout.kv_scale, scales, "kv_scale")
+    return (here, _arg(k_pool, here, pool, k_pool.dtype, "k_pool"),
+            _arg(v_pool, here, pool, v_pool.dtype, "v_pool"))
+
+
+def _attended(layout, k_pool, v_pool, q, seq_lens, out, m, e):
+    """The checks that the calls with fp32 or bf16 outputs share: (device, B, T, Hq, the pointers of
+    k_pool, v_pool, q, seq_lens, out, whether out is bf16, the pointers of m and e)."""
+    size = q.shape
+    if len(size) != 4:
+        raise ValueError("q must be bf16 [B][T][Hq][d]")
+    B, T, Hq, _ = size
+    here, kp, vp = _pools(layout, k_pool, v_pool, B)
+    rows = B * T * Hq
+    n = rows * layout.c.head_dim
+    dtype = out.dtype
+    bf16 = dtype == torch.bfloat16
+    if not bf16 and dtype != torch.float32:
         raise TypeError("out must be float32 or bfloat16")
-    return out.dtype == torch.bfloat16
+    return (here, B, T, Hq, kp, vp, _arg(q, here, n, torch.bfloat16, "q"),
+            _arg(seq_lens, here, B, torch.int32, "seq_lens"), _arg(out, here, n, dtype, "out"), bf16,
+            _arg(m, here, rows, torch.float32, "m"), _arg(e, here, rows, torch.float32, "e"))
 
 
 def dattn_decode_window(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_lens, window: int,
@@ -735,19 +779,13 @@ def dattn_decode_window(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_l
     the last T tokens of each request) attends tokens i <= p with i > p - window or i < sinks. out
     float32 or bf16 [B][T][Hq][d] (+ m_g, e_g fp32 [B][T][Hq]); the workspace as for
     dattn_decode_multi."""
-    _pool(layout, k_pool, "k_pool"); _pool(layout, v_pool, "v_pool"); _bf16(q, "q")
-    _i32(seq_lens, "seq_lens"); _f32(m_g, "m_g"); _f32(e_g, "e_g")
-    bf16 = _out_bf16(out)
-    if q.dim() != 4:
-        raise ValueError("q must be bf16 [B][T][Hq][d]")
-    B, T, Hq = q.shape[0], q.shape[1], q.shape[2]
-    _decode_sizes(layout, B, T, Hq, k_pool, v_pool, q, seq_lens, out, m_g, e_g, None)
-    here = _layout_device(layout, k_pool)
+    here, B, T, Hq, kp, vp, qp, lp, op, bf16, mp, ep = _attended(layout, k_pool, v_pool, q, seq_lens,
+                                                                 out, m_g, e_g)
+    buf = ws.buffer
     _check(load_library().dattn_decode_window(
-        ctypes.byref(layout.c), _at(k_pool, here), _at(v_pool, here), _at(q, here), B, T, Hq,
-        scale, _at(seq_lens, here), window, sinks, num_splits, _at(ws.buffer, here),
-        ws.buffer.numel(), _at(out, here), bf16, _at(m_g, here), _at(e_g, here),
-        _at(dev_err, here), _stream_on(stream, here)), "dattn_decode_window")
+        ctypes.byref(layout.c), kp, vp, qp, B, T, Hq, scale, lp, window, sinks, num_splits,
+        _at(buf, here), buf.numel(), op, bf16, mp, ep, _at(dev_err, here),
+        _stream_on(stream, here)), "dattn_decode_window")
 
 
 def dattn_kv_read(layout: KVLayout, k_pool, v_pool, k_out, v_out, out_indptr, seq_lens,
@@ -757,32 +795,34 @@ def dattn_kv_read(layout: KVLayout, k_pool, v_pool, k_out, v_out, out_indptr, se
     token starts[b] + n - out_indptr[b] of request b (out_indptr int32 [B+1]; starts int32 [B],
     None: from the first token). Other rows, and rows of tokens that the request or the pool does
     not hold, stay as they are."""
-    _pool(layout, k_pool, "k_pool"); _pool(layout, v_pool, "v_pool")
-    _i32(out_indptr, "out_indptr"); _i32(seq_lens, "seq_lens"); _i32(starts, "starts")
     any_out = k_out if k_out is not None else v_out
     if any_out is None:
         raise ValueError("k_out or v_out is needed")
-    f32 = any_out.dtype == torch.float32
-    if not f32 and any_out.dtype != torch.bfloat16:
+    dtype = any_out.dtype
+    f32 = dtype == torch.float32
+    if not f32 and dtype != torch.bfloat16:
         raise TypeError("k_out and v_out must both be bfloat16 or both float32")
     if out_indptr.dim() != 1 or out_indptr.shape[0] < 1:
         raise ValueError("out_indptr must be int32 [B + 1]")
-    B, Hkv, d = out_indptr.shape[0] - 1, layout.num_kv_heads, layout.head_dim
-    N = any_out.shape[0] if any_out.dim() == 3 else -1
-    here = _layout_device(layout, k_pool)
-    outs = []
-    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is not None and (t.dim() != 3 or tuple(t.shape) != (N, Hkv, d)):
-            raise ValueError(f"{name} must be [N][Hkv][d]")
-        if t is not None and t.dtype != any_out.dtype:
+    B = out_indptr.shape[0] - 1
+    here, kp, vp = _pools(layout, k_pool, v_pool, B)
+    c, size = layout.c, any_out.shape
+    if len(size) != 3 or size[1] != c.num_kv_heads or size[2] != c.head_dim:
+        raise ValueError("k_out and v_out must be [N][Hkv][d]")
+    ko = vo = (None, 0)
+    if k_out is not None:
+        ko = _tokens(k_out, "k_out", here)
+    if v_out is not None:
+        if v_out.dtype != dtype:
             raise TypeError("k_out and v_out must both be bfloat16 or both float32")
-        outs += _tokens(t, name, here) if t is not None else (None, 0)
-    _layout_sizes(layout, B, k_pool, v_pool)
-    _size(seq_lens, B, "seq_lens"); _size(starts, B, "starts")
+        if v_out.shape != size:
+            raise ValueError("k_out and v_out must be [N][Hkv][d]")
+        vo = _tokens(v_out, "v_out", here)
     _check(load_library().dattn_kv_read(
-        ctypes.byref(layout.c), _at(k_pool, here), _at(v_pool, here), B, _at(out_indptr, here),
-        _at(starts, here), _at(seq_lens, here), N, *outs, f32, _at(dev_err, here),
-        _stream_on(stream, here)), "dattn_kv_read")
+        ctypes.byref(c), kp, vp, B, _arg(out_indptr, here, 1, torch.int32, "out_indptr"),
+        _arg(starts, here, B, torch.int32, "starts"),
+        _arg(seq_lens, here, B, torch.int32, "seq_lens"), size[0], *ko, *vo, f32,
+        _at(dev_err, here), _stream_on(stream, here)), "dattn_kv_read")
 
 
 def dattn_prefill(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_lens, out, m=None,
@@ -816,24 +856,18 @@ def dattn_decode_shared(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_l
     group_indptr[i] .. group_indptr[i+1] - 1 (int32 [groups + 1]) hold their first prefix_lens[i]
     tokens (int32 [groups]) in the same pages, which are read once for the group. out float32 or bf16
     [B][T][Hq][d] (+ m_g, e_g fp32 [B][T][Hq]); bf16 or KV_FP8_BLOCK pools."""
-    _pool(layout, k_pool, "k_pool"); _pool(layout, v_pool, "v_pool"); _bf16(q, "q")
-    _i32(seq_lens, "seq_lens"); _i32(group_indptr, "group_indptr"); _i32(prefix_lens, "prefix_lens")
-    _f32(m_g, "m_g"); _f32(e_g, "e_g")
-    bf16 = _out_bf16(out)
-    if q.dim() != 4:
-        raise ValueError("q must be bf16 [B][T][Hq][d]")
-    B, T, Hq = q.shape[0], q.shape[1], q.shape[2]
     groups = prefix_lens.numel()
-    _decode_sizes(layout, B, T, Hq, k_pool, v_pool, q, seq_lens, out, m_g, e_g, None)
+    here, B, T, Hq, kp, vp, qp, lp, op, bf16, mp, ep = _attended(layout, k_pool, v_pool, q, seq_lens,
+                                                                 out, m_g, e_g)
     if group_indptr.numel() != groups + 1:
         raise ValueError(f"group_indptr holds {group_indptr.numel()} elements; {groups} groups need "
                          f"{groups + 1}")
-    here = _layout_device(layout, k_pool)
+    buf = ws.buffer
     _check(load_library().dattn_decode_shared(
-        ctypes.byref(layout.c), _at(k_pool, here), _at(v_pool, here), _at(q, here), B, T, Hq,
-        scale, _at(seq_lens, here), groups, _at(group_indptr, here), _at(prefix_lens, here),
-        _at(ws.buffer, here), ws.buffer.numel(), _at(out, here), bf16, _at(m_g, here),
-        _at(e_g, here), _at(dev_err, here), _stream_on(stream, here)), "dattn_decode_shared")
+        ctypes.byref(layout.c), kp, vp, qp, B, T, Hq, scale, lp, groups,
+        _arg(group_indptr, here, 0, torch.int32, "group_indptr"),
+        _arg(prefix_lens, here, 0, torch.int32, "prefix_lens"), _at(buf, here), buf.numel(), op, bf16,
+        mp, ep, _at(dev_err, here), _stream_on(stream, here)), "dattn_decode_shared")
 
 
 def dattn_prefill_window(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_lens, window: int,
@@ -841,17 +875,10 @@ def dattn_prefill_window(layout: KVLayout, k_pool, v_pool, q, scale: float, seq_
     """Prefill of q bf16 [B][Tq][Hq][d], the last Tq tokens of each request, through a sliding
     window: the query at position p attends tokens i <= p with i > p - window or i < sinks. out
     float32 or bf16 [B][Tq][Hq][d] (+ m, e fp32 [B][Tq][Hq]); bf16 or KV_FP8_BLOCK pools."""
-    _pool(layout, k_pool, "k_pool"); _pool(layout, v_pool, "v_pool"); _bf16(q, "q")
-    _i32(seq_lens, "seq_lens"); _f32(m, "m"); _f32(e, "e")
-    bf16 = _out_bf16(out)
-    if q.dim() != 4:
-        raise ValueError("q must be bf16 [B][Tq][Hq][d]")
-    B, Tq, Hq = q.shape[0], q.shape[1], q.shape[2]
-    _decode_sizes(layout, B, Tq, Hq, k_pool, v_pool, q, seq_lens, out, m, e, None)
-    here = _layout_device(layout, k_pool)
+    here, B, Tq, Hq, kp, vp, qp, lp, op, bf16, mp, ep = _attended(layout, k_pool, v_pool, q, seq_lens,
+                                                                  out, m, e)
     _check(load_library().dattn_prefill_window(
-        ctypes.byref(layout.c), _at(k_pool, here), _at(v_pool, here), _at(q, here), B, Tq, Hq,
-        scale, _at(seq_lens, here), window, sinks, _at(out, here), bf16, _at(m, here), _at(e, here),
+        ctypes.byref(layout.c), kp, vp, qp, B, Tq, Hq, scale, lp, window, sinks, op, bf16, mp, ep,
         _at(dev_err, here), _stream_on(stream, here)), "dattn_prefill_window")
 
 
