@@ -40,11 +40,12 @@ struct SharedParams {
     int32_t groups;
     const int32_t* group_indptr;
     const int32_t* prefix_lens;
-    // the workspace: the pieces' rows, and (m in log2 units, e) of each; the plan: W, CTAs with work, then
-    // per group its first cost unit, then per group its prefix
+    // the workspace: the pieces' rows, and (m in log2 units, e) of each; the plan: per group its first
+    // request, its requests, its prefix and its first cost unit; then W and the CTAs with work, and per
+    // request its group (-1: none)
     float* slots;
     float2* slot_me;
-    int32_t* plan;
+    int4* plan;
 };
 
 // The rows of pieces in the workspace: a piece of segment s in CTA c begins at rowbase(s) + 256 c, where
@@ -131,9 +132,11 @@ struct SharedJob {
                     const int32_t mid = (lo + hi) >> 1;
                     if (id[mid + 1] <= i) lo = mid + 1; else hi = mid;
                 }
-                if (lo < w.groups && id[lo] <= i)
+                const bool in = lo < w.groups && id[lo] <= i;
+                if (in)
                     atomicMax(key + lo,
                               ((unsigned long long)min(max(len, 0), cap) << 32) | (uint32_t)~i);
+                if (blockIdx.x == 0) reinterpret_cast<int32_t*>(w.plan + w.groups + 1)[i] = in ? lo : -1;
             }
             __syncthreads();
             int32_t cost = 0;
@@ -162,14 +165,9 @@ struct SharedJob {
         }
         const int32_t cta = blockIdx.x, Gw = shared_ctas(W, gridDim.x);
         if (cta == 0) {  // for the merge
-            if (tid < w.groups) {
-                w.plan[2 + tid] = W > 0 ? st[tid] : 0;
-                w.plan[2 + w.groups + tid] = W > 0 ? inf[tid].x : 0;
-            }
-            if (tid == 0) {
-                w.plan[0] = W;
-                w.plan[1] = Gw;
-            }
+            if (tid < w.groups && W > 0)
+                w.plan[tid] = make_int4(id[tid], id[tid + 1] - id[tid], inf[tid].x, st[tid]);
+            if (tid == 0) w.plan[w.groups] = make_int4(W, Gw, 0, 0);
         }
         x = X1 = 0;
         j = j1 = 0;
@@ -270,10 +268,9 @@ struct SharedJob {
 
 struct MergeParams {
     int32_t B, T, Hq, g, tok, groups;
-    const int32_t* group_indptr;
     const float* slots;
     const float2* slot_me;
-    const int32_t* plan;
+    const int4* plan;
     const float* own;    // [B][T][Hq][D] MA of the own tokens
     const float* own_m;  // [B][T][Hq], log2 units
     const float* own_e;
@@ -287,11 +284,13 @@ constexpr int kMergeThreads = 128;
 
 // Joins the pieces of a row, (m, e, MA) of its own tokens and of every run of its prefix. A block takes
 // 512 / D rows, in the order of the segments' rows (KV head, token, query head of the KV head), a thread
-// four channels of one; neighbouring threads take neighbouring rows, as the pieces lie.
+// four channels of one; neighbouring threads take neighbouring rows, as the pieces lie. Bound by latency: what
+// a row needs to know takes two loads in turn, and the runs of most rows are asked for in one go (64
+// requests of 32 heads, 20 runs: 8.5 us with four loads in turn and eight runs at a time).
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
 shared_merge_kernel(const __grid_constant__ MergeParams p) {
-    constexpr int RB = 512 / D, kBatch = 8;
+    constexpr int RB = 512 / D, kBatch = 24;
     grid_dependency_wait();
     grid_launch_dependents();
     const int64_t n = (int64_t)blockIdx.x * RB + threadIdx.x % RB;
@@ -300,28 +299,28 @@ shared_merge_kernel(const __grid_constant__ MergeParams p) {
     if (n >= (int64_t)N * p.Hq) return;
     const int32_t kvh = (int32_t)(n / ((int64_t)N * p.g));
     const int32_t k = (int32_t)(n - (int64_t)kvh * N * p.g);
-    const int32_t bt = k / p.g, b = bt / p.T;
+    const int32_t bt = k / p.g, b = bt / p.T;  // the query token and its request
     const int64_t row = (int64_t)bt * p.Hq + kvh * p.g + (k - bt * p.g);
     float m = __ldcg(p.own_m + row), e = __ldcg(p.own_e + row);
     float4 acc = __ldcg(reinterpret_cast<const float4*>(p.own + row * D) + c4);
-    const int32_t W = __ldcg(p.plan), Gw = __ldcg(p.plan + 1);
-    const int32_t i = W > 0 ? shared_group(p.group_indptr, p.groups, b) : -1;
+    const int4 head = __ldcg(p.plan + p.groups);
+    const int32_t i = head.x > 0 ? __ldcg(reinterpret_cast<const int32_t*>(p.plan + p.groups + 1) + b) : -1;
     // the q'th run's rows begin at first + 256 q; this thread's is the r'th of `rows`
     int64_t first = 0;
     int32_t runs = 0, rows = 0, r = 0;
     if (i >= 0) {
-        const int32_t prefix = __ldcg(p.plan + 2 + p.groups + i), c0 = __ldcg(p.group_indptr + i);
-        const SharedGroup G(__ldcg(p.group_indptr + i + 1) - c0, p.T, p.tok, prefix);
+        const int4 group = __ldcg(p.plan + i);
+        const SharedGroup G(group.y, p.T, p.tok, group.z);
         if (G.blocks > 0) {
-            const int32_t tk = bt - c0 * p.T, pair = tk / (2 * p.tok), in = tk - pair * 2 * p.tok;
+            const int32_t tk = bt - group.x * p.T, pair = tk / (2 * p.tok), in = tk - pair * 2 * p.tok;
             const int32_t t = in / p.tok, left = G.tokens - pair * 2 * p.tok - t * p.tok;
-            const int64_t cs = __ldcg(p.plan + 2 + i) + (int64_t)(kvh * G.pairs + pair) * G.cost;
-            const int32_t cf = split_owner(cs, W, Gw), cl = split_owner(cs + G.blocks - 1, W, Gw);
+            const int64_t cs = group.w + (int64_t)(kvh * G.pairs + pair) * G.cost;
+            const int32_t cf = split_owner(cs, head.x, head.y);
+            runs = split_owner(cs + G.blocks - 1, head.x, head.y) - cf + 1;
             rows = min(p.tok, left) * p.g;
             r = (in - t * p.tok) * p.g + (k - bt * p.g);
-            first = (int64_t)c0 * p.T * p.Hq + (int64_t)kvh * G.tokens * p.g +
+            first = (int64_t)group.x * p.T * p.Hq + (int64_t)kvh * G.tokens * p.g +
                     (pair * 2 + t) * p.tok * p.g + 256ll * cf;
-            runs = cl - cf + 1;
         }
     }
     for (int32_t q0 = 0; q0 < runs; q0 += kBatch) {
@@ -386,7 +385,7 @@ ShWorkspace shared_workspace(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int3
     w.own_e = take((size_t)rows * 4);
     w.slots = take((size_t)slots * D * 4);
     w.slot_me = take((size_t)slots * 8);
-    w.plan = take((size_t)(2 * (B < kShMaxGroups ? B : kShMaxGroups) + 3) * 4);
+    w.plan = take((size_t)((B < kShMaxGroups ? B : kShMaxGroups) + 1) * 16 + (size_t)B * 4);
     w.total = o;
     return w;
 }
@@ -495,7 +494,7 @@ dattn_status_t dattn_decode_shared(const dattn_kv_layout* layout, const void* k_
     sp.prefix_lens = prefix_lens;
     sp.slots = reinterpret_cast<float*>(wb + w.slots);
     sp.slot_me = reinterpret_cast<float2*>(wb + w.slot_me);
-    sp.plan = reinterpret_cast<int32_t*>(wb + w.plan);
+    sp.plan = reinterpret_cast<int4*>(wb + w.plan);
     const bool blk = layout->kv_format == DATTN_KV_FP8_BLOCK;
     auto launch = D == 64 ? (blk ? launch_tiles<SharedJob<64>, 64, DATTN_KV_FP8_BLOCK>
                                  : launch_tiles<SharedJob<64>, 64, DATTN_KV_BF16>)
@@ -511,7 +510,6 @@ dattn_status_t dattn_decode_shared(const dattn_kv_layout* layout, const void* k_
     m.g = g;
     m.tok = p.tok;
     m.groups = num_groups;
-    m.group_indptr = group_indptr;
     m.slots = sp.slots;
     m.slot_me = sp.slot_me;
     m.plan = sp.plan;
