@@ -16,8 +16,8 @@
 //   3. shared_merge_kernel, which joins the pieces.
 // What bounds 2: from 128 rows on the tensor cores (1.1 us for a block of 256 rows on an SM), below the tiles'
 // latency (0.8 us a block; block-scaled pool: the widening, 1.3 us). Measured on a GB300, 32 / 8 heads of 128: 64
-// requests behind 16384 tokens with 100-2000 of their own 72 us, of which the engine takes 34 by itself; 4 requests
-// behind 1808 tokens 17.6 us; 4 and 64 requests of 10 tokens behind 65536 tokens 65 and 97 us (268 MB of prefix).
+// requests behind 16384 tokens with 100-2000 of their own 69 us (engine 34, prefix 22, merge 7); 4 requests behind
+// 1808 tokens 18 us; 4 and 64 requests of 10 tokens behind 65536 tokens 65 and 97 us (268 MB of prefix).
 #include "shared.cuh"
 #include "tile_attention.cuh"
 

@@ -14,7 +14,7 @@
 // What bounds it: the tensor cores, three products of 128 x 64 x d for two that count, and the softmax
 // (with a short window an item's first scores and its epilogue; over the block-scaled pool the widening).
 // Measured on a GB300, 32 / 8 heads of 128: a prompt of 16K tokens, bf16 pool, through a window of 64, 1024, 4096
-// and without one 130, 357, 1001 and 2275 us (967 TFLOP/s counted); 4096 tokens after 28K through 4096,
+// and without one 130, 354, 1001 and 2275 us (967 TFLOP/s counted); 4096 tokens after 28K through 4096,
 // block-scaled pool, 362 us (772 TFLOP/s).
 #include "tile_attention.cuh"
 
