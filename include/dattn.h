@@ -616,8 +616,8 @@ dattn_status_t dattn_prefill(const dattn_kv_layout *layout, const void *k_pool,
  * position p = L_b - Tq + t attends the tokens i <= p with i > p - window or i < sinks, token by
  * token (dattn_prefill's streaming heads keep whole 64-token blocks). Otherwise as dattn_prefill
  * with sparse == NULL: the chunk is the last Tq of the L_b tokens of request b, the pool is bf16 or
- * DATTN_KV_FP8_BLOCK, and no workspace is needed. Only the key blocks that a window or the first
- * tokens touch are read; pages of others may be unmapped.
+ * DATTN_KV_FP8_BLOCK, and no workspace is needed. Pages of which no query of the chunk sees a token
+ * are not read: they may be unmapped.
  *
  *   window   tokens of the window, the query's own the last: >= 1;  sinks >= 0
  *   out      (device) fp32, or bf16 when out_bf16 = 1, [B][Tq][Hq][d]

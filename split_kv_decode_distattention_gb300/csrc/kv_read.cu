@@ -240,8 +240,8 @@ extern "C" dattn_status_t dattn_kv_read(const dattn_kv_layout* layout, const voi
     if (st != DATTN_OK) return st;
     if (B < 0 || N < 0 || (out_f32 & ~1)) return DATTN_ERR_INVALID_ARG;
     if (B > kMaxItems || N > (1 << 30)) return DATTN_ERR_UNSUPPORTED;
-    if (!k_out && !v_out) return DATTN_ERR_INVALID_ARG;
     if (B == 0 || N == 0) return DATTN_OK;
+    if (!k_out && !v_out) return DATTN_ERR_INVALID_ARG;
     if (!k_pool || !v_pool || !out_indptr || !seq_lens) return DATTN_ERR_INVALID_ARG;
     const int64_t row = (int64_t)layout->num_kv_heads * layout->head_dim, align = out_f32 ? 4 : 8;
     if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(k_out) || !aligned16(v_out) ||

@@ -208,7 +208,7 @@ struct SharedJob {
             it.n0 = ind[lo] * w.T + tok0;
             it.trow = info[lo].y;
             it.kmax = info[lo].x;
-            it.first = 0;
+            it.first = it.low = it.sinks = 0;
         }
         it.from = j;
         it.count = min(j1 - j, it.alt ? 2 * kShEmpty : kShEmpty);

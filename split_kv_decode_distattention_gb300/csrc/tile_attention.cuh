@@ -98,6 +98,7 @@ struct TaItem {
     int32_t kvh, trow;           // KV head; row of the block table
     int32_t first, from, count;  // its key blocks: [0, first), then from `from` on, `count` in all
     int32_t kmax;                // keys from kmax on do not exist
+    int32_t low, sinks;          // its rows see no key below `low` but those below `sinks`
     int32_t alt;
     int32_t last[2];             // the last of its blocks (by number) that tile 0, 1 keeps; -1: none
     __device__ int32_t block(int32_t j) const { return j < first ? j : from + (j - first); }
@@ -543,7 +544,10 @@ tile_attention_kernel(const __grid_constant__ TaParams p, const __grid_constant_
                 if (b >= it.count) return;
                 const int32_t t0 = it.block(b) * kPfBlock + 16 * u;
                 if (t0 >= it.kmax) return;
-                const int32_t lp = t0 / p.P, page = __ldcg(trow + lp);
+                // a page of which no row sees a token may be gone (it counts as keys that do not exist)
+                const int32_t lp = t0 / p.P;
+                if (lp * p.P >= it.sinks && (lp + 1) * p.P <= it.low) return;
+                const int32_t page = __ldcg(trow + lp);
                 if (page < 0) {
                     if (!isv) set_err(p.dev_err, DATTN_DEVERR_UNMAPPED_PAGE);
                 } else if (page >= p.num_pages) {

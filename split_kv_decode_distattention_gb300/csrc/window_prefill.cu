@@ -73,6 +73,8 @@ struct WindowJob {
             it.trow = b;
             it.kmax = L;
             pos = L - w.Tq + t0;
+            it.low = pos - w.window + 1;
+            it.sinks = w.sinks;
             const int32_t last0 = (pos + it.tok[0] - 1) / kPfBlock;
             const int32_t last1 = (pos + it.tok[0] + it.tok[1] - 1) / kPfBlock;
             it.from = max(pos - w.window + 1, 0) / kPfBlock;

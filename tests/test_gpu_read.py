@@ -99,6 +99,13 @@ def test_tokens_that_are_not_there_are_flagged_and_left(dattn):
     assert read(2, 14, 4) == (E["PAGE_OOB"], [True] * 2 + [False] * 2)
 
 
+def test_no_rows_is_nothing_to_read(dattn):
+    pool = Paged("bf16", [40], 2, 64, 16, seed=4)
+    lay, (kp, vp) = pool.layout(dattn), pool.pools()
+    none = torch.empty(0, 2, 64, device=DEV)
+    dattn.dattn_kv_read(lay, kp, vp, none, none, i32([0, 0]), i32([40]))
+
+
 def test_bounds_out_of_order_are_flagged(dattn):
     pool = Paged("bf16", [40, 40, 40], 2, 64, 16, seed=4)
     lay, (kp, vp) = pool.layout(dattn), pool.pools()

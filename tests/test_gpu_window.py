@@ -274,6 +274,25 @@ def test_chunk_behind_a_long_context_reads_its_window_alone(dattn, fmt):
         check(out[0, :, h], None, None, ref, bound, 0, 0, 0, f"{fmt} h={h}")
 
 
+@pytest.mark.parametrize("fmt", ("bf16", "fp8-block"))
+@pytest.mark.parametrize("P", (16, 32, 48, 64))
+def test_chunk_does_not_look_at_pages_that_its_windows_left(dattn, fmt, P):
+    """Pages without a token that some query sees may be given back, inside a block of 64 too."""
+    lens, T, W, S = [1000, 431], 90, 190, 5
+    pool = Paged(fmt, lens, 2, 64, P, seed=12)
+    q = queries(2, T, 4, 64, 7)
+    (kp, vp), L = pool.pools(), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    a, b = (torch.empty(2, T, 4, 64, device=DEV) for _ in range(2))
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    dattn.dattn_prefill_window(pool.layout(dattn), kp, vp, q, 0.1, L, W, S, a)
+    pool.table = pool.table.copy()
+    for r, n in enumerate(lens):
+        first = n - T - W + 1  # the first key of the first query's window
+        pool.table[r, -(-S // P):first // P] = -1
+    dattn.dattn_prefill_window(pool.layout(dattn), kp, vp, q, 0.1, L, W, S, b, dev_err=err)
+    assert int(err) == 0 and torch.equal(a, b)
+
+
 def test_chunk_flags_a_length_below_it(dattn):
     pool = Paged("bf16", [100, 100], 2, 64, 16, seed=1)
     lay, (kp, vp) = pool.layout(dattn), pool.pools()

@@ -124,6 +124,7 @@ def test_read_refusals(lib):
     assert read(lib, N=-1) == INVALID and read(lib, N=0) == OK
     assert read(lib, N=(1 << 30) + 1) == UNSUPPORTED
     assert read(lib, k=None, v=None) == INVALID
+    assert read(lib, N=0, k=None, v=None) == OK  # (a tensor without rows has no address)
     assert read(lib, indptr=None) == INVALID and read(lib, lens=None) == INVALID
     assert read(lib, k=8) == INVALID and read(lib, v=8) == INVALID
     assert read(lib, ks=260) == INVALID and read(lib, ks=258, f32=1) == INVALID
