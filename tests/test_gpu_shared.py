@@ -215,3 +215,45 @@ def test_in_a_graph_and_twice_alike(dattn, fmt):
         assert torch.equal(out, want)
         pool.lens = lens2
         check_all(pool, q, out, None, None, 0.1, f"{fmt} {ends2}")
+
+
+@pytest.mark.parametrize("fmt", ("bf16", "fp8-block"))
+@pytest.mark.parametrize("B", (3, 40))
+def test_prefix_whose_pieces_are_joined_in_the_workspace(dattn, fmt, B):
+    """1.4M tokens of prefix, so that a CTA's run is longer than what stays in its accumulators, for one
+    tile of rows and for two. The prefix's pages repeat: a key counts as often as its page does."""
+    Hq, Hkv, d, P, pages, reps = 4, 1, 64, 256, 4, 1370
+    n = pages * reps
+    base = Paged(fmt, [pages * P + P], Hkv, d, P, seed=13, spare=0)
+    phys = base.table[0, :pages + 1]
+    table = np.tile(phys[:pages], reps)[None].repeat(B, 0)
+    table = np.concatenate((table, np.full((B, 1), phys[pages], np.int32)), 1).astype(np.int32)
+    own = [1 + 5 * b for b in range(B)]  # of the last page, the same rows for all
+    lens = [n * P + x for x in own]
+    kp, vp = base.pools()
+    sc = None if base.kv_scale is None else base.kv_scale.to(DEV)
+    lay = dattn.KVLayout(base.pages, Hkv, d, P, torch.from_numpy(table).to(DEV),
+                         0 if fmt == "bf16" else dattn.KV_FP8_BLOCK, sc)
+    q = queries(B, 1, Hq, d, 14)
+    ws = dattn.SharedWorkspace(B, 1, Hq, Hkv, d)
+    err = i32([0])
+    out, again = (torch.empty(B, 1, Hq, d, device=DEV) for _ in range(2))
+    for to in (out, again):
+        dattn.dattn_decode_shared(lay, kp, vp, q, 0.125, i32(lens), i32([0, B]), i32([n * P - 77]), to,
+                                  ws, dev_err=err)
+    assert int(err) == 0 and torch.equal(out, again)
+    K, V = base.rows("k", 0)[:, 0], base.rows("v", 0)[:, 0]
+    qn = q.double().cpu().numpy()
+    for b in (0, 1, B - 1):
+        L = pages * P + own[b]
+        count = np.where(np.arange(L) < pages * P, reps, 1)
+        for h in range(Hq):
+            s = K[:L] @ qn[b, 0, h] * 0.125
+            w = count * np.exp(s - s.max())
+            ref = w @ V[:L] / w.sum()
+            mag = np.abs(K[:L]) @ np.abs(qn[b, 0, h]) * 0.125
+            # logits and weights as in attention(); sums of up to 64 blocks of 8 products, then of up to
+            # 200 partials: each addition at most 2^-23 off
+            t = d * 2.0 ** -23 * mag.max() + weight_error("bf16") + (64 * 8 + 200) * 2.0 ** -23
+            check(out[b, :, h], None, None, ref[None], np.array([2 * t * np.abs(V[:L]).max()]), 0, 0, 0,
+                  f"{fmt} b={b} h={h}")
